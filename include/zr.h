@@ -77,6 +77,7 @@ typedef enum {
 } zr_status;
 
 typedef enum { ZR_FP32 = 0, ZR_BF16 = 1 } zr_dtype;
+typedef enum { ZR_I32 = 0, ZR_I64 = 1 } zr_index;   /* token ids */
 
 /* One parameter, in list (gradient-ready) order.  numel > 0; group indexes
  * the zr_group array. */
@@ -449,6 +450,142 @@ zr_status zr_all_gather_params(const zr_plan* plan, int32_t group,
 zr_status zr_ring_ag_step(float* const* rank_bufs, int32_t n_ranks,
                           int64_t chunk_numel, int32_t step,
                           hipStream_t stream);
+
+/* ---------------------------------------------------- layer operators --- */
+
+/* The operators between a model's layers and the flat space: they read what
+ * the partitions hold and write the main_grad window that zr_ipg_accumulate
+ * fills, without the full parameter or its gradient ever being written out.
+ *
+ * Conventions beyond those above:
+ *   - Matrices are rows of contiguous elements, `stride` elements from one
+ *     row to the next (>= the columns).  Rows need only be element-aligned.
+ *   - A workspace is device memory of the caller's, 16-byte aligned, of at
+ *     least the bytes the matching query gives.  Its contents do not outlive
+ *     the call and need no initialisation.  Two calls that may run at once
+ *     (on two streams, or in two graphs replayed without an order between
+ *     them) need a workspace each.  No call allocates, so all of them may be
+ *     recorded into a HIP graph, the first call included.
+ *   - A parameter is clipped to the window [window_base, +window_len) as in
+ *     zr_ipg_accumulate, and a `_first` form writes what the plain form
+ *     gives on a window zeroed at the start of the step, to every element of
+ *     the parameter in the window, without reading it.
+ *   - Sums are fp32 in an order that depends on the sizes alone: the same
+ *     inputs give the same bits on every run.
+ */
+
+/* zr_embedding_lookup -- rows of a [vocab, dim] table that lies in the ranks'
+ * partitions, scaled ([Megatron DP] "通信模式": the updated slices that the
+ * forward pass reads; here without stitching the whole parameter together):
+ *   out[i * out_stride + c] = rnd(scale * W[token_i, c]),  0 <= c < dim
+ *   param       the table's param id; its numel is vocab * dim.
+ *   parts[R_g]  host array of device partition pointers (P_g elements of
+ *               dtype each); only those that hold some of the table are read
+ *               and may not be null.  A gathered flat vector serves too:
+ *               parts[k] = flat + k * P_g.
+ *   tokens[n]   device array of ids.  An id outside [0, vocab) -- padding --
+ *               gives a row of zeros.
+ * The product is one fp32 operation, rounded once to dtype (scale 1: a copy
+ * of the values; NaNs come out quiet).  out must not overlap parts. */
+zr_status zr_embedding_lookup(const zr_plan* plan, int64_t param, int64_t dim,
+                              const void* const* parts, zr_dtype dtype,
+                              const void* tokens, zr_index token_type, int64_t n,
+                              float scale, void* out, int64_t out_stride,
+                              hipStream_t stream);
+
+/* Workspace bytes of zr_ipg_accumulate_embedding and its _first form. */
+zr_status zr_ipg_embedding_workspace(const zr_plan* plan, int64_t param, int64_t dim,
+                                     int64_t n, int64_t window_base,
+                                     int64_t window_len, int64_t* bytes);
+
+/* zr_ipg_accumulate_embedding -- the lookup's gradient, added to main_grad
+ * ([Megatron DP] "深入：朴素 DP 的 all-reduce" step 2: the fp32 buffer each
+ * micro-batch's gradient is added into):
+ *   main_grad[o_p + r*dim + c - window_base] += scale * sum_i dY[i, c]
+ * over the tokens i with token_i == r, in fp32: sums of runs of consecutive
+ * such tokens first, each in their order, then those sums in theirs; one
+ * product and one add.  Tokens outside [0, vocab) or the window add nothing,
+ * and their rows of dY are not read.  Elements of rows without tokens are not
+ * touched; the _first form writes 0 to them.
+ *   dy   device rows of dim elements of dy_dtype, one per token. */
+zr_status zr_ipg_accumulate_embedding(const zr_plan* plan, int64_t param, int64_t dim,
+                                      const void* tokens, zr_index token_type,
+                                      int64_t n, float scale, const void* dy,
+                                      zr_dtype dy_dtype, int64_t dy_stride,
+                                      float* main_grad, int64_t window_base,
+                                      int64_t window_len, void* workspace,
+                                      int64_t workspace_bytes, hipStream_t stream);
+zr_status zr_ipg_accumulate_embedding_first(const zr_plan* plan, int64_t param, int64_t dim,
+                                            const void* tokens, zr_index token_type,
+                                            int64_t n, float scale, const void* dy,
+                                            zr_dtype dy_dtype, int64_t dy_stride,
+                                            float* main_grad, int64_t window_base,
+                                            int64_t window_len, void* workspace,
+                                            int64_t workspace_bytes, hipStream_t stream);
+
+/* An activation checkpoint of X [rows, cols] in 8 bits: for every row and
+ * every 32 columns the scale 2^E, E the least integer >= -110 with
+ * |x| <= 448 * 2^E for the finite x of the block, kept as the byte E + 127
+ * (17 to 247); and for every element the e4m3 code (4 exponent bits, 3
+ * mantissa bits, largest value 448, no infinities) of x / 2^E rounded to
+ * nearest even.  Infinities and NaNs become the code NaN and do not touch
+ * their neighbours.  A row of codes holds code_pitch bytes, a row of scales
+ * scale_pitch bytes (zr_act_layout: cols rounded up to whole blocks of 32,
+ * and the number of blocks); the codes behind the last column are 0. */
+zr_status zr_act_layout(int64_t cols, int64_t* code_pitch, int64_t* scale_pitch);
+
+/* zr_act_quantize -- the checkpoint of x.  codes must be 16-byte aligned. */
+zr_status zr_act_quantize(const void* x, zr_dtype dtype, int64_t rows, int64_t cols,
+                          int64_t x_stride, uint8_t* codes, uint8_t* scales,
+                          hipStream_t stream);
+
+/* zr_act_dequantize -- the activations a checkpoint stands for: code * 2^E,
+ * exact in either dtype (a value that coding rounded up past the dtype's
+ * largest number becomes infinite). */
+zr_status zr_act_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                            int64_t cols, void* out, zr_dtype dtype,
+                            int64_t out_stride, hipStream_t stream);
+
+/* One linear layer's part of a backward pass: Y = X W^T for the weight W
+ * [n_out, n_in], stored so (in_major 0) or as its transpose [n_in, n_out]
+ * (in_major 1); dy holds `tokens` bf16 rows of n_out elements and
+ * (codes, scales) the checkpoint of X's `tokens` rows of n_in columns.  Rows
+ * of dy may share a checkpoint between items. */
+typedef struct {
+  int64_t param;
+  int64_t n_out, n_in;
+  int64_t tokens;
+  const uint16_t* dy;
+  int64_t dy_stride;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int32_t in_major;
+} zr_linear_grad;
+
+/* Workspace bytes of zr_ipg_accumulate_linear and its _first form for these
+ * items (device pointers are checked, not read). */
+zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linear_grad* items,
+                                  int64_t n, int64_t window_base, int64_t window_len,
+                                  int64_t* bytes);
+
+/* zr_ipg_accumulate_linear -- the weights' gradients of the listed layers,
+ * taken from 8-bit checkpoints and added to main_grad ([Megatron DP] "深入：朴素
+ * DP 的 all-reduce" step 2):
+ *   main_grad[o_p + e - window_base] += sum_t dY[t, o] * X^[t, i],
+ *   e = o*n_in + i (in_major: i*n_out + o), X^ = code * 2^E
+ * in fp32 on the matrix cores; the products are of bf16 values and exact.
+ * Only the weight rows that meet the window are computed.  items[n] is a
+ * host array; all params must be in one group and none twice; an item
+ * without tokens (an expert nobody was routed to) adds nothing.  dY and X
+ * should be finite: a NaN or infinity spreads as in the formula. */
+zr_status zr_ipg_accumulate_linear(const zr_plan* plan, const zr_linear_grad* items,
+                                   int64_t n, float* main_grad, int64_t window_base,
+                                   int64_t window_len, void* workspace,
+                                   int64_t workspace_bytes, hipStream_t stream);
+zr_status zr_ipg_accumulate_linear_first(const zr_plan* plan, const zr_linear_grad* items,
+                                         int64_t n, float* main_grad, int64_t window_base,
+                                         int64_t window_len, void* workspace,
+                                         int64_t workspace_bytes, hipStream_t stream);
 
 /* ------------------------------------------------------------- errors --- */
 

@@ -35,6 +35,8 @@ Modules:
 * ``adam``   -- textbook Adam in fp32 (plus an fp64 twin for sanity).
 * ``bf16``   -- round-to-nearest-even fp32 -> bf16 from its definition.
 * ``ring``   -- literal ring reduce-scatter / all-gather message passing.
+* ``layers`` -- embedding lookup and gradient, 8-bit activation checkpoints,
+  weight gradients from them, in float64.
 * ``volume`` -- communication-volume and per-card byte accounting.
 
 Parity pins: every function is pinned by ``tests/test_oracle_*.py`` against

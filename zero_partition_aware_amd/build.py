@@ -8,6 +8,7 @@ import os
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,6 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libzr.so")
+# HIP translation units: the reduction path, and the layer operators
+HIP_SOURCES = ["zr_kernels", "zr_embed", "zr_linear"]
 ARCH = os.environ.get("ZR_OFFLOAD_ARCH", "gfx950")
 
 
@@ -34,7 +37,7 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 
 # Per-kernel fingerprints of the device code: for every kernel in the gfx950
-# code object, a hash of its instruction bytes (.text) and of its kernel
+# code object of the reduction path (the kernels bench.py measures), a hash of its instruction bytes (.text) and of its kernel
 # descriptor (.rodata, register and segment sizes), written beside the
 # library at build time as {demangled kernel name: hash}.  The code holds no
 # relocations or PC-relative references, so a kernel's bytes do not depend on
@@ -122,19 +125,22 @@ def build(verbose=False):
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     plan_o = os.path.join(BUILD_DIR, "zr_plan.o")
-    kern_o = os.path.join(BUILD_DIR, "zr_kernels.o")
+    kern_o = [os.path.join(BUILD_DIR, name + ".o") for name in HIP_SOURCES]
     # The planner is plain C++ (no device code): compiled by the host compiler.
     out = _run(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-Wextra",
                 "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE, "-I", CSRC,
                 "-I", "/opt/rocm/include", "-c",
                 os.path.join(CSRC, "zr_plan.cpp"), "-o", plan_o])
-    out += _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c",
-                 os.path.join(CSRC, "zr_kernels.hip"), "-o", kern_o])
+    with ThreadPoolExecutor(len(HIP_SOURCES)) as pool:
+        out += "".join(pool.map(
+            lambda name, obj: _run([hipcc, *HIP_FLAGS, "-I", INCLUDE, "-I", CSRC, "-c",
+                                    os.path.join(CSRC, name + ".hip"), "-o", obj]),
+            HIP_SOURCES, kern_o))
     tmp = LIB + ".tmp"
     # The HIP runtime is a dependency by soname (libamdhip64.so.7): in a
     # process that already holds torch's copy of the runtime (same soname) the
     # loader reuses it; standalone, RUNPATH finds the ROCm installation's.
-    out += _run(["g++", "-shared", "-fPIC", plan_o, kern_o,
+    out += _run(["g++", "-shared", "-fPIC", plan_o, *kern_o,
                  "-L/opt/rocm/lib", "-lamdhip64", "-Wl,-rpath,/opt/rocm/lib",
                  "-Wl,--no-undefined", "-o", tmp])
     os.replace(tmp, LIB)

@@ -1,0 +1,552 @@
+// The embedding table's operators (gfx950): rows looked up in the ranks'
+// partitions, and the table's gradient by sorted tokens into main_grad.
+// Both are HBM-bound streams over rows: no product is large enough for MFMA.
+
+#include "zr_layers.h"
+
+using namespace zr;
+
+namespace {
+
+// Token ids of either width.
+struct Tokens {
+  const void* ids;
+  int32_t wide;  // 1: int64, 0: int32
+};
+__device__ __forceinline__ int64_t token_at(const Tokens& t, int64_t i) {
+  return t.wide ? as_global<int64_t>(t.ids)[i] : as_global<int32_t>(t.ids)[i];
+}
+
+// ---------------------------------------------------------------- lookup ---
+
+struct LookupArgs {
+  const void* parts[ZR_MAX_WORLD];
+  Tokens tokens;
+  void* out;
+  int64_t n, vocab, dim, out_stride;
+  int64_t base, part;     // the table's flat offset; partition elements
+  double part_inverse;
+  float scale;
+  int32_t chunks;         // pieces of kLookupCols columns per row
+};
+
+constexpr int kLookupWaves = 4;
+template <typename T> constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+template <typename T> constexpr int kLookupCols = 64 * kVec<T> * 4;
+
+template <typename T>
+__device__ __forceinline__ T scaled(T x, float s);
+template <>
+__device__ __forceinline__ float scaled(float x, float s) { return x * s; }
+template <>
+__device__ __forceinline__ uint16_t scaled(uint16_t x, float s) {
+  return static_cast<uint16_t>(pack_bf16(bf16_lo(x) * s, 0.0f));
+}
+template <typename T>
+__device__ __forceinline__ u32x4 scaled_vec(u32x4 w, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = sizeof(T) == 2 ? pack_bf16(bf16_lo(w[i]) * s, bf16_hi(w[i]) * s)
+                          : float_bits(bits_float(w[i]) * s);
+  return w;
+}
+
+// out[i, c] = rnd(scale * table[token_i, c]).  One wave copies one piece of
+// up to kLookupCols columns of one row, 16 bytes a lane and four loads in
+// flight; the partition that holds the piece is found once a wave, and only
+// a piece that a partition border cuts goes element by element.  An id
+// outside [0, vocab) gives a row of zeros and reads nothing.
+template <typename T>
+__global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupArgs a) {
+  constexpr int V = kVec<T>, C = kLookupCols<T>;
+  const int lane = threadIdx.x & 63;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kLookupWaves + uniform(static_cast<int>(threadIdx.x >> 6));
+  const int64_t row = unit / a.chunks;
+  if (row >= a.n) return;
+  const int64_t c0 = (unit - row * a.chunks) * C;
+  const int64_t len = a.dim - c0 < C ? a.dim - c0 : C;
+  const int64_t t = uniform(token_at(a.tokens, row));
+  T* out = static_cast<T*>(a.out) + row * a.out_stride + c0;
+  const bool valid = t >= 0 && t < a.vocab;
+  const int64_t f = a.base + (valid ? t * a.dim + c0 : 0);
+  // f < 2^53, so the quotient is off by one at most.
+  int64_t k = static_cast<int64_t>(static_cast<double>(f) * a.part_inverse);
+  if (k * a.part > f) --k;
+  if ((k + 1) * a.part <= f) ++k;
+  if (!valid || f + len <= (k + 1) * a.part) {
+    const T* src = valid ? static_cast<const T*>(a.parts[k]) + (f - k * a.part) : nullptr;
+    u32x4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = (u * 64 + lane) * V;
+      x[u] = u32x4{0, 0, 0, 0};
+      if (valid && c + V <= len) x[u] = *as_global<u32x4_a2>(src + c);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = (u * 64 + lane) * V;
+      if (c + V <= len) {
+        *as_global<u32x4_a2>(out + c) = scaled_vec<T>(x[u], a.scale);
+      } else {
+        for (int e = c; e < len; ++e) out[e] = valid ? scaled<T>(src[e], a.scale) : T(0);
+      }
+    }
+    return;
+  }
+  for (int64_t e = lane; e < len; e += 64) {
+    while (f + e >= (k + 1) * a.part) ++k;
+    out[e] = scaled<T>(static_cast<const T*>(a.parts[k])[f + e - k * a.part], a.scale);
+  }
+}
+
+// -------------------------------------------------------------- gradient ---
+//
+// main_grad[row] (+)= scale * sum of dY over the tokens with that row's id.
+// 1. sort: the positions of the tokens whose row meets the window, by row and
+//    in their own order within a row;
+// 2. sum: pieces of kPiece sorted positions, each summed by waves of its own
+//    in that order.  A row whose tokens lie in one piece is added to
+//    main_grad at once; one that spans pieces leaves a partial sum per piece;
+// 3. join: the partial sums of such a row, added in the order of the pieces.
+// The pieces are cut by position and never by row, so that a token that fills
+// half the batch is spread over the GPU like any other; and nothing depends
+// on which wave comes first, so the sums have the same bits on every run.
+
+constexpr int kSortWaves = 16;
+constexpr int kSortRows = 1024;   // rows one workgroup sorts, at most
+
+struct EmbedWork {       // the caller's workspace
+  int32_t* count;        // sorted positions
+  int32_t* pos;          // their places in the batch
+  int32_t* row;          // their rows, relative to the window's first row
+  float* partial;        // [pieces][2][cols]: a piece's first and last run
+};
+
+struct SortArgs {
+  Tokens tokens;
+  EmbedWork w;
+  int64_t n, row0, rows;  // the window's rows: [row0, row0 + rows)
+  int32_t span;           // rows per workgroup
+  // first micro-batch only: rows without tokens are zeroed
+  float* main_grad;       // null otherwise; where the table's element 0 lies
+  int64_t dim, first, last;
+};
+
+// Workgroup g sorts the tokens of rows [g*span, (g+1)*span): it counts, over
+// the whole batch, the tokens of earlier rows (its first place in the order)
+// and those of each row of its own, by wave; then every wave places its share
+// of the batch, in order, behind what earlier rows and earlier waves have.
+// Two reads of the ids by each workgroup, which stay in L2, in one launch:
+// measured against the work that follows, the ids are 1/1000 of the bytes.
+__global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortArgs a) {
+  __shared__ int32_t place[kSortWaves][kSortRows];
+  __shared__ int32_t wave_sum[kSortWaves];
+  __shared__ int32_t before_s;
+  __shared__ uint8_t empty[kSortRows];
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.span;
+  const int span = static_cast<int>(a.rows - lo < a.span ? a.rows - lo : a.span);
+  for (int i = tid; i < kSortWaves * kSortRows; i += blockDim.x) (&place[0][0])[i] = 0;
+  if (tid == 0) before_s = 0;
+  __syncthreads();
+  const int64_t share = (a.n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
+  const int64_t i0 = w * share, i1 = i0 + share < a.n ? i0 + share : a.n;
+  int before = 0;
+  for (int64_t i = i0 + lane; i < i1; i += 64) {
+    const int64_t r = token_at(a.tokens, i) - a.row0;
+    if (r >= 0 && r < lo) ++before;
+    if (r >= lo && r < lo + span) atomicAdd(&place[w][r - lo], 1);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+  if (lane == 0) atomicAdd(&before_s, before);
+  __syncthreads();
+  // One thread a row: its count, then an exclusive scan over the rows.
+  int count = 0;
+  for (int v = 0; v < kSortWaves; ++v) count += place[v][tid];
+  int scan = count;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(scan, d);
+    if (lane >= d) scan += up;
+  }
+  if (lane == 63) wave_sum[w] = scan;
+  __syncthreads();
+  int at = before_s + scan - count;
+  for (int v = 0; v < w; ++v) at += wave_sum[v];
+  empty[tid] = count == 0;
+  if (blockIdx.x == gridDim.x - 1 && tid == 64 * kSortWaves - 1) *a.w.count = at + count;
+  for (int v = 0; v < kSortWaves; ++v) {
+    const int c = place[v][tid];
+    place[v][tid] = at;
+    at += c;
+  }
+  __syncthreads();
+  for (int64_t b = i0; b < i1; b += 64) {
+    const int64_t i = b + lane;
+    int64_t r = -1;
+    if (i < i1) r = token_at(a.tokens, i) - a.row0 - lo;
+    const bool mine = r >= 0 && r < span;
+    uint64_t left = __ballot(mine);
+    while (left) {
+      const int row = __builtin_amdgcn_readlane(static_cast<int>(r), __builtin_ctzll(left));
+      const uint64_t same = __ballot(mine && static_cast<int>(r) == row);
+      const int p = place[w][row];
+      if (mine && static_cast<int>(r) == row) {
+        const int q = p + __popcll(same & ((1ull << lane) - 1));
+        a.w.pos[q] = static_cast<int32_t>(i);
+        a.w.row[q] = static_cast<int32_t>(lo) + row;
+      }
+      place[w][row] = p + __popcll(same);
+      left &= ~same;
+    }
+  }
+  if (!a.main_grad) return;
+  // Zeros for the elements of rows without tokens, four to a lane.
+  const int64_t e0 = (a.row0 + lo) * a.dim;
+  const int64_t b0 = e0 > a.first ? e0 : a.first;
+  const int64_t e1 = (a.row0 + lo + span) * a.dim;
+  const int64_t b1 = e1 < a.last ? e1 : a.last;
+  const int64_t lead = (16 - (reinterpret_cast<uintptr_t>(a.main_grad + b0) & 15)) / 4 % 4;
+  for (int64_t e = b0 - (4 - lead) % 4 + 4 * tid; e < b1; e += 4 * blockDim.x) {
+    const int64_t f = e < b0 ? b0 : e, l = e + 4 < b1 ? e + 4 : b1;
+    const uint32_t rf = static_cast<uint64_t>(f - e0) / a.dim;
+    const uint32_t rl = static_cast<uint64_t>(l - 1 - e0) / a.dim;
+    if (rf == rl && l - f == 4) {
+      if (empty[rf]) *as_global<f32x4_a4>(a.main_grad + f) = f32x4{0, 0, 0, 0};
+    } else {
+      for (int64_t x = f; x < l; ++x)
+        if (empty[static_cast<uint64_t>(x - e0) / a.dim]) a.main_grad[x] = 0.0f;
+    }
+  }
+}
+
+struct SumArgs {
+  const void* dy;
+  EmbedWork w;
+  float* main_grad;            // where the table's element 0 lies
+  int64_t dy_stride, dim, row0, first, last;
+  int32_t piece, cols;         // positions per piece; columns of a partial sum
+  float scale;
+};
+
+// Four columns of a row's gradient into main_grad, clipped to the window.
+template <bool kFirst>
+__device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, f32x4 s) {
+  const int64_t e = (a.row0 + row) * a.dim + col;
+  s *= a.scale;
+  if (col + 4 <= a.dim && e >= a.first && e + 4 <= a.last) {
+    auto* p = as_global<f32x4_a4>(a.main_grad + e);
+    *p = (kFirst ? f32x4{0, 0, 0, 0} : f32x4(*p)) + s;
+  } else {
+    for (int j = 0; j < 4; ++j)
+      if (col + j < a.dim && e + j >= a.first && e + j < a.last)
+        a.main_grad[e + j] = (kFirst ? 0.0f : a.main_grad[e + j]) + s[j];
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T* p, int left);
+template <>
+__device__ __forceinline__ f32x4 load4(const uint16_t* p, int left) {
+  if (left >= 4) {
+    const u32x2 w = *as_global<u32x2_a2>(p);
+    return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+  }
+  f32x4 x{0, 0, 0, 0};
+  for (int j = 0; j < left; ++j) x[j] = bf16_lo(p[j]);
+  return x;
+}
+template <>
+__device__ __forceinline__ f32x4 load4(const float* p, int left) {
+  if (left >= 4) return *as_global<f32x4_a4>(p);
+  f32x4 x{0, 0, 0, 0};
+  for (int j = 0; j < left; ++j) x[j] = p[j];
+  return x;
+}
+
+constexpr int kSumVecs = 4;                     // column groups of four per lane
+constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of one wave
+
+template <typename T, bool kFirst>
+__global__ __launch_bounds__(64) void embed_sum_kernel(const SumArgs a) {
+  const int lane = threadIdx.x;
+  const int count = *a.w.count;
+  const int p0 = blockIdx.x * a.piece;
+  if (p0 >= count) return;
+  const int p1 = p0 + a.piece < count ? p0 + a.piece : count;
+  const int c0 = blockIdx.y * kSumCols + 4 * lane;
+  int row = a.w.row[p0];
+  bool head = p0 > 0 && a.w.row[p0 - 1] == row;   // the run began in an earlier piece
+  f32x4 s[kSumVecs] = {};
+  for (int p = p0; p < p1; ++p) {
+    const int r = a.w.row[p];
+    if (r != row) {
+#pragma unroll
+      for (int u = 0; u < kSumVecs; ++u) {
+        const int c = c0 + 256 * u;
+        if (c < a.dim) {
+          if (head)
+            *as_global<f32x4>(a.w.partial + int64_t(blockIdx.x) * 2 * a.cols + c) = s[u];
+          else
+            put_row<kFirst>(a, row, c, s[u]);
+        }
+        s[u] = f32x4{0, 0, 0, 0};
+      }
+      row = r;
+      head = false;
+    }
+    const T* src = static_cast<const T*>(a.dy) + static_cast<int64_t>(a.w.pos[p]) * a.dy_stride;
+#pragma unroll
+    for (int u = 0; u < kSumVecs; ++u) {
+      const int c = c0 + 256 * u;
+      if (c < a.dim) s[u] += load4<T>(src + c, static_cast<int>(a.dim) - c);
+    }
+  }
+  const bool on = p1 < count && a.w.row[p1] == row;   // the run goes on
+#pragma unroll
+  for (int u = 0; u < kSumVecs; ++u) {
+    const int c = c0 + 256 * u;
+    if (c >= a.dim) continue;
+    if (head || on)
+      *as_global<f32x4>(a.w.partial + (int64_t(blockIdx.x) * 2 + (head ? 0 : 1)) * a.cols + c) = s[u];
+    else
+      put_row<kFirst>(a, row, c, s[u]);
+  }
+}
+
+// The rows that span pieces: workgroup (piece, columns) adds up the run that
+// starts in its piece and goes on behind it, if there is one.
+template <bool kFirst>
+__global__ __launch_bounds__(256) void embed_join_kernel(const SumArgs a) {
+  __shared__ f32x4 part[4][64];
+  const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
+  const int count = *a.w.count;
+  const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.piece, p1 = p0 + a.piece;
+  if (p1 >= count) return;
+  const int row = a.w.row[p1];
+  if (a.w.row[p1 - 1] != row || (p0 > 0 && a.w.row[p0 - 1] == row)) return;
+  // The run's last position, by bisection: rows are sorted.
+  int64_t in = p1, out = count;
+  while (in + 1 < out) {
+    const int64_t mid = (in + out) / 2;
+    if (a.w.row[mid] == row) in = mid; else out = mid;
+  }
+  const int64_t links = in / a.piece - blockIdx.x;   // pieces that follow
+  const int c = blockIdx.y * 256 + 4 * lane;
+  f32x4 s{0, 0, 0, 0};
+  if (c < a.dim) {
+    const int64_t each = (links + 3) / 4;
+    const int64_t j1 = (w + 1) * each < links ? (w + 1) * each : links;
+    const float* head = a.w.partial + (blockIdx.x + 1) * int64_t(2) * a.cols + c;
+    if (w == 0) s = *as_global<f32x4>(a.w.partial + (blockIdx.x * int64_t(2) + 1) * a.cols + c);
+#pragma unroll 8
+    for (int64_t j = w * each; j < j1; ++j) s += *as_global<f32x4>(head + j * 2 * a.cols);
+  }
+  part[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < a.dim)
+    put_row<kFirst>(a, row, c, ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane]);
+}
+
+// Positions per piece: enough pieces to fill the chip, and no more partial
+// sums than that takes.
+int64_t piece_of(int64_t n, int64_t dim) {
+  const int64_t waves = ceil_div(dim, kSumCols);
+  int64_t piece = 64;
+  while (piece > 8 && ceil_div(n, piece) * waves < 2048) piece /= 2;
+  return piece;
+}
+
+struct Shape {
+  int64_t piece, pieces, cols, pos, row, partial, bytes;   // offsets in the workspace
+};
+Shape shape_of(int64_t n, int64_t dim) {
+  Shape s;
+  s.piece = piece_of(n, dim);
+  s.pieces = ceil_div(n, s.piece);
+  s.cols = ceil_div(dim, 4) * 4;
+  s.pos = 256;
+  s.row = s.pos + ceil_div(4 * n, 256) * 256;
+  s.partial = s.row + ceil_div(4 * n, 256) * 256;
+  s.bytes = s.partial + (s.pieces > 1 ? s.pieces * 2 * s.cols * 4 : 0);
+  return s;
+}
+
+zr_status check_table(const zr_plan* plan, int64_t param, int64_t dim, int64_t n) {
+  if (!plan) return fail(ZR_ERR_INVALID, "plan is null");
+  if (param < 0 || param >= static_cast<int64_t>(plan->params.size()))
+    return fail(ZR_ERR_INVALID, "param id out of range");
+  if (dim < 1 || plan->params[param].numel % dim)
+    return fail(ZR_ERR_INVALID, "dim must be >= 1 and divide the param's elements");
+  if (dim >= (int64_t(1) << 24)) return fail(ZR_ERR_UNSUPPORTED, "dim of 2^24 or more");
+  if (n < 0) return fail(ZR_ERR_INVALID, "n must be >= 0");
+  if (n >= (int64_t(1) << 31) - 64 * kSortWaves) return fail(ZR_ERR_UNSUPPORTED, "2^31 tokens or more");
+  return ZR_OK;
+}
+
+zr_status check_tokens(const void* tokens, zr_index type, int64_t n) {
+  if (type != ZR_I32 && type != ZR_I64) return fail(ZR_ERR_INVALID, "unsupported token type");
+  if (n > 0 && (!tokens || !aligned_to(tokens, type == ZR_I64 ? 8 : 4)))
+    return fail(ZR_ERR_INVALID, "tokens is null or not element-aligned");
+  return ZR_OK;
+}
+
+template <typename T, bool kFirst>
+void launch_sum(const SumArgs& a, int64_t pieces, hipStream_t stream) {
+  embed_sum_kernel<T, kFirst><<<dim3(pieces, ceil_div(a.dim, kSumCols)), 64, 0, stream>>>(a);
+}
+
+zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const void* tokens,
+                        zr_index token_type, int64_t n, float scale, const void* dy,
+                        zr_dtype dy_dtype, int64_t dy_stride, float* main_grad,
+                        int64_t window_base, int64_t window_len, void* workspace,
+                        int64_t workspace_bytes, bool first, hipStream_t stream) {
+  return guarded([&]() -> zr_status {
+    zr_status st = check_table(plan, param, dim, n);
+    if (st != ZR_OK) return st;
+    st = check_tokens(tokens, token_type, n);
+    if (st != ZR_OK) return st;
+    if (!valid_dtype(dy_dtype)) return fail(ZR_ERR_INVALID, "unsupported gradient dtype");
+    if (n > 0 && (!dy || !aligned_to(dy, dtype_size(dy_dtype))))
+      return fail(ZR_ERR_INVALID, "dy is null or not element-aligned");
+    if (dy_stride < dim) return fail(ZR_ERR_INVALID, "dy_stride must be >= dim");
+    Clip clip;
+    st = clip_param(plan, param, main_grad, window_base, window_len, &clip);
+    if (st != ZR_OK) return st;
+    const Shape s = shape_of(n, dim);
+    if (!workspace || !aligned_to(workspace, 16) || workspace_bytes < s.bytes)
+      return fail(ZR_ERR_INVALID, "workspace is null, not 16-byte aligned or smaller than " +
+                                      std::to_string(s.bytes) + " bytes");
+    if (clip.first == clip.last || (n == 0 && !first)) return ZR_OK;
+    char* ws = static_cast<char*>(workspace);
+    const EmbedWork w{reinterpret_cast<int32_t*>(ws), reinterpret_cast<int32_t*>(ws + s.pos),
+                      reinterpret_cast<int32_t*>(ws + s.row),
+                      reinterpret_cast<float*>(ws + s.partial)};
+    float* table = main_grad + clip.place;
+    SortArgs sa{};
+    sa.tokens = Tokens{tokens, token_type == ZR_I64};
+    sa.w = w;
+    sa.n = n;
+    sa.row0 = clip.first / dim;
+    sa.rows = ceil_div(clip.last, dim) - sa.row0;
+    sa.span = static_cast<int32_t>(std::min<int64_t>(kSortRows, ceil_div(sa.rows, 256)));
+    sa.main_grad = first ? table : nullptr;
+    sa.dim = dim;
+    sa.first = clip.first;
+    sa.last = clip.last;
+    if (ceil_div(sa.rows, sa.span) > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "too many rows");
+    embed_sort_kernel<<<ceil_div(sa.rows, sa.span), 64 * kSortWaves, 0, stream>>>(sa);
+    st = launched("embedding sort launch");
+    if (st != ZR_OK || n == 0) return st;
+    SumArgs a{};
+    a.dy = dy;
+    a.w = w;
+    a.main_grad = table;
+    a.dy_stride = dy_stride;
+    a.dim = dim;
+    a.row0 = sa.row0;
+    a.first = clip.first;
+    a.last = clip.last;
+    a.piece = static_cast<int32_t>(s.piece);
+    a.cols = static_cast<int32_t>(s.cols);
+    a.scale = scale;
+    if (dy_dtype == ZR_BF16) {
+      if (first) launch_sum<uint16_t, true>(a, s.pieces, stream);
+      else launch_sum<uint16_t, false>(a, s.pieces, stream);
+    } else {
+      if (first) launch_sum<float, true>(a, s.pieces, stream);
+      else launch_sum<float, false>(a, s.pieces, stream);
+    }
+    st = launched("embedding sum launch");
+    if (st != ZR_OK || s.pieces == 1) return st;
+    const dim3 grid(s.pieces - 1, ceil_div(dim, 256));
+    if (first) embed_join_kernel<true><<<grid, 256, 0, stream>>>(a);
+    else embed_join_kernel<false><<<grid, 256, 0, stream>>>(a);
+    return launched("embedding join launch");
+  });
+}
+
+}  // namespace
+
+extern "C" zr_status zr_embedding_lookup(const zr_plan* plan, int64_t param, int64_t dim,
+                                         const void* const* parts, zr_dtype dtype,
+                                         const void* tokens, zr_index token_type, int64_t n,
+                                         float scale, void* out, int64_t out_stride,
+                                         hipStream_t stream) {
+  return guarded([&]() -> zr_status {
+    zr_status st = check_table(plan, param, dim, n);
+    if (st != ZR_OK) return st;
+    st = check_tokens(tokens, token_type, n);
+    if (st != ZR_OK) return st;
+    if (!valid_dtype(dtype)) return fail(ZR_ERR_INVALID, "unsupported element dtype");
+    const int64_t es = dtype_size(dtype);
+    if (out_stride < dim) return fail(ZR_ERR_INVALID, "out_stride must be >= dim");
+    if (n > 0 && (!out || !aligned_to(out, es)))
+      return fail(ZR_ERR_INVALID, "out is null or not element-aligned");
+    if (!parts) return fail(ZR_ERR_INVALID, "parts is null");
+    const ParamInfo& pi = plan->params[param];
+    const GroupInfo& gi = plan->groups[pi.group];
+    LookupArgs a{};
+    for (int32_t k = 0; k < gi.world; ++k) {
+      // only the partitions that hold some of the table are read
+      if ((k + 1) * gi.part <= pi.offset || k * gi.part >= pi.offset + pi.numel) continue;
+      if (!parts[k] || !aligned_to(parts[k], es))
+        return fail(ZR_ERR_INVALID, "partition " + std::to_string(k) + " is null or misaligned");
+      a.parts[k] = parts[k];
+    }
+    if (n == 0) return ZR_OK;
+    a.tokens = Tokens{tokens, token_type == ZR_I64};
+    a.out = out;
+    a.n = n;
+    a.vocab = pi.numel / dim;
+    a.dim = dim;
+    a.out_stride = out_stride;
+    a.base = pi.offset;
+    a.part = gi.part;
+    a.part_inverse = 1.0 / static_cast<double>(gi.part);
+    a.scale = scale;
+    const int64_t cols = dtype == ZR_BF16 ? kLookupCols<uint16_t> : kLookupCols<float>;
+    a.chunks = static_cast<int32_t>(ceil_div(dim, cols));
+    const int64_t grid = ceil_div(n * a.chunks, kLookupWaves);
+    if (grid > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "too many rows for one call");
+    if (dtype == ZR_BF16) lookup_kernel<uint16_t><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
+    else lookup_kernel<float><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
+    return launched("embedding lookup launch");
+  });
+}
+
+extern "C" zr_status zr_ipg_embedding_workspace(const zr_plan* plan, int64_t param, int64_t dim,
+                                                int64_t n, int64_t window_base,
+                                                int64_t window_len, int64_t* bytes) {
+  return guarded([&]() -> zr_status {
+    if (!bytes) return fail(ZR_ERR_INVALID, "null output pointer");
+    zr_status st = check_table(plan, param, dim, n);
+    if (st != ZR_OK) return st;
+    Clip clip;
+    st = clip_param(plan, param, reinterpret_cast<const float*>(4), window_base, window_len, &clip);
+    if (st != ZR_OK) return st;
+    *bytes = shape_of(n, dim).bytes;
+    return ZR_OK;
+  });
+}
+
+extern "C" zr_status zr_ipg_accumulate_embedding(
+    const zr_plan* plan, int64_t param, int64_t dim, const void* tokens, zr_index token_type,
+    int64_t n, float scale, const void* dy, zr_dtype dy_dtype, int64_t dy_stride,
+    float* main_grad, int64_t window_base, int64_t window_len, void* workspace,
+    int64_t workspace_bytes, hipStream_t stream) {
+  return run_embedding(plan, param, dim, tokens, token_type, n, scale, dy, dy_dtype, dy_stride,
+                       main_grad, window_base, window_len, workspace, workspace_bytes, false,
+                       stream);
+}
+
+extern "C" zr_status zr_ipg_accumulate_embedding_first(
+    const zr_plan* plan, int64_t param, int64_t dim, const void* tokens, zr_index token_type,
+    int64_t n, float scale, const void* dy, zr_dtype dy_dtype, int64_t dy_stride,
+    float* main_grad, int64_t window_base, int64_t window_len, void* workspace,
+    int64_t workspace_bytes, hipStream_t stream) {
+  return run_embedding(plan, param, dim, tokens, token_type, n, scale, dy, dy_dtype, dy_stride,
+                       main_grad, window_base, window_len, workspace, workspace_bytes, true,
+                       stream);
+}

@@ -44,6 +44,7 @@ if len(_hip_runtimes_loaded()) > 1:
 
 ZR_OK, ZR_ERR_INVALID, ZR_ERR_OOM, ZR_ERR_HIP, ZR_ERR_UNSUPPORTED = range(5)
 ZR_FP32, ZR_BF16 = 0, 1
+ZR_I32, ZR_I64 = 0, 1
 ZR_MAX_WORLD = 64
 STATUS_NAMES = {0: "ZR_OK", 1: "ZR_ERR_INVALID", 2: "ZR_ERR_OOM",
                 3: "ZR_ERR_HIP", 4: "ZR_ERR_UNSUPPORTED"}
@@ -79,7 +80,16 @@ class zr_adam(ctypes.Structure):
                 ("step", c_i64)]
 
 
+class zr_linear_grad(ctypes.Structure):
+    _fields_ = [("param", c_i64), ("n_out", c_i64), ("n_in", c_i64), ("tokens", c_i64),
+                ("dy", c_vp), ("dy_stride", c_i64), ("codes", c_vp), ("scales", c_vp),
+                ("in_major", c_i32)]
+
+
 _P = ctypes.POINTER
+_embedding_grad = [c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, ctypes.c_float, c_vp, c_i32, c_i64,
+                   c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]
+_linear_grads = [c_vp, _P(zr_linear_grad), c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]
 _sigs = {
     "zr_plan_buckets": (c_i32, [_P(zr_param), c_i64, _P(zr_group), c_i32, c_i64,
                                 c_i32, c_i64, _P(c_vp)]),
@@ -125,6 +135,18 @@ _sigs = {
     "zr_ring_ag_step": (c_i32, [_P(c_vp), c_i32, c_i64, c_i32, c_vp]),
     "zr_all_gather_params": (c_i32, [c_vp, c_i32, _P(c_vp), c_i32, c_vp, c_i64, c_i64,
                                      c_vp]),
+    "zr_embedding_lookup": (c_i32, [c_vp, c_i64, c_i64, _P(c_vp), c_i32, c_vp, c_i32, c_i64,
+                                    ctypes.c_float, c_vp, c_i64, c_vp]),
+    "zr_ipg_embedding_workspace": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_i64, c_i64, _P(c_i64)]),
+    "zr_ipg_accumulate_embedding": (c_i32, _embedding_grad),
+    "zr_ipg_accumulate_embedding_first": (c_i32, _embedding_grad),
+    "zr_act_layout": (c_i32, [c_i64, _P(c_i64), _P(c_i64)]),
+    "zr_act_quantize": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp]),
+    "zr_act_dequantize": (c_i32, [c_vp, c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp]),
+    "zr_ipg_linear_workspace": (c_i32, [c_vp, _P(zr_linear_grad), c_i64, c_i64, c_i64,
+                                        _P(c_i64)]),
+    "zr_ipg_accumulate_linear": (c_i32, _linear_grads),
+    "zr_ipg_accumulate_linear_first": (c_i32, _linear_grads),
     "zr_last_error": (ctypes.c_char_p, []),
     "zr_version": (c_i32, []),
 }
@@ -283,11 +305,12 @@ def _adam(lr, beta1, beta2, eps, step):
 class Plan:
     """Owns a zr_plan handle (freed with zr_plan_free)."""
 
-    def __init__(self, handle, numels=(), worlds=()):
+    def __init__(self, handle, numels=(), worlds=(), param_groups=()):
         self._h = handle
         self.part_numel = {}      # group -> P_g (the plan is immutable)
         self.numels = tuple(int(n) for n in numels)   # param sizes, list order
         self.worlds = tuple(int(w) for w in worlds)   # R_g per group
+        self.param_groups = tuple(int(g) for g in param_groups)   # per param
 
     @property
     def handle(self):
@@ -323,7 +346,7 @@ def zr_plan_buckets(numels, param_groups, groups, reduce_bucket_size,
                                 _i32(partition_gradients, "partition_gradients"),
                                 _i64(align, "align"),
                                 ctypes.byref(out)))
-    return Plan(out.value, numels, [w for w, _ in groups])
+    return Plan(out.value, numels, [w for w, _ in groups], param_groups)
 
 
 def zr_plan_free(plan):
@@ -692,3 +715,205 @@ def zr_all_gather_params(plan, group, parts, out, out_base=0, out_len=None,
     _check(_lib.zr_all_gather_params(plan.handle, _i32(group, "group"), arr, dt,
                                      _buf(out, "out", dt, ol), _i64(out_base, "out_base"), ol,
                                      _stream(stream)))
+
+
+# -------------------------------------------------------- layer operators
+
+def _rows(t, name, shape, dtypes):
+    """Checks one matrix of contiguous rows and returns (address, stride):
+    rows x columns as ``shape`` says (None: any), of one of the torch dtypes,
+    on the current device.  Rows may lie apart (a slice of wider rows); a
+    strided or broadcast column axis is refused."""
+    if t.dtype not in dtypes:
+        raise ZrError(ZR_ERR_INVALID, f"{name} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != 2 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; the call needs "
+                                      f"{tuple('any' if w is None else w for w in shape)}")
+    _on_device(t, name)
+    rows, cols = t.shape
+    stride, step = t.stride()
+    if rows < 2:
+        stride = max(stride, cols)
+    if (step != 1 and cols > 1) or stride < cols:
+        raise ZrError(ZR_ERR_INVALID, f"{name} must have contiguous rows")
+    return t.data_ptr(), stride
+
+
+def _on_device(t, name):
+    if not t.is_cuda:
+        raise ZrError(ZR_ERR_INVALID, f"{name} must be a device tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ZrError(ZR_ERR_INVALID, f"{name} is on device {t.get_device()}, not on the current "
+                                      f"one ({torch.cuda.current_device()})")
+
+
+def _dense(t, name, dtype, min_numel=0):
+    """Address of a contiguous tensor of the current device."""
+    if t.dtype is not dtype:
+        raise ZrError(ZR_ERR_INVALID, f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ZrError(ZR_ERR_INVALID, f"{name} must be contiguous")
+    _on_device(t, name)
+    if t.numel() < min_numel:
+        raise ZrError(ZR_ERR_INVALID,
+                      f"{name} holds {t.numel()} elements; the call touches {min_numel}")
+    return t.data_ptr()
+
+
+def _token_ids(tokens):
+    if tokens.dtype is torch.int64:
+        return _dense(tokens, "tokens", torch.int64), ZR_I64
+    return _dense(tokens, "tokens", torch.int32), ZR_I32
+
+
+def zr_embedding_lookup(plan, param, dim, parts, tokens, out, scale=1.0, stream=None):
+    """out[i] = scale * row tokens[i] of the [vocab, dim] table ``param``,
+    read from the R_g partition tensors ``parts`` (bf16 or fp32, those that
+    hold none of the table may be None); ids outside [0, vocab) give zeros.
+    tokens: int64 or int32, any shape; out: [tokens.numel(), dim]."""
+    ids, wide = _token_ids(tokens)
+    n, d = tokens.numel(), _i64(dim, "dim")
+    ptr, stride = _rows(out, "out", (n, d), (torch.bfloat16, torch.float32))
+    p = _i64(param, "param")
+    group = plan.param_groups[p] if 0 <= p < len(plan.param_groups) else 0
+    _expect_len(parts, _world(plan, group), "parts")
+    P = _part_numel(plan, group)
+    arr = (c_vp * len(parts))(*[None if t is None else _dense(t, f"parts[{k}]", out.dtype, P)
+                                for k, t in enumerate(parts)])
+    _check(_lib.zr_embedding_lookup(plan.handle, p, d, arr, _dtype_code(out), ids, wide, n,
+                                    scale, ptr, stride, _stream(stream)))
+
+
+def zr_ipg_embedding_workspace(plan, param, dim, n, window_base, window_len):
+    """Bytes of workspace the embedding gradient of n tokens needs."""
+    v = c_i64()
+    _check(_lib.zr_ipg_embedding_workspace(
+        plan.handle, _i64(param, "param"), _i64(dim, "dim"), _i64(n, "n"),
+        _i64(window_base, "window_base"), _i64(window_len, "window_len"), ctypes.byref(v)))
+    return v.value
+
+
+def zr_ipg_accumulate_embedding(plan, param, dim, tokens, dy, main_grad, workspace,
+                                window_base=0, window_len=None, scale=1.0, stream=None):
+    """main_grad rows of the table ``param`` += scale * the sums of the rows of
+    dy (bf16 or fp32, [tokens.numel(), dim]) over equal ids; ids outside
+    [0, vocab) add nothing.  workspace: a uint8 tensor of at least
+    zr_ipg_embedding_workspace bytes that no other call uses meanwhile."""
+    _embedding(_lib.zr_ipg_accumulate_embedding, plan, param, dim, tokens, dy, main_grad,
+               workspace, window_base, window_len, scale, stream)
+
+
+def zr_ipg_accumulate_embedding_first(plan, param, dim, tokens, dy, main_grad, workspace,
+                                      window_base=0, window_len=None, scale=1.0, stream=None):
+    """The step's first micro-batch: as zr_ipg_accumulate_embedding on a zeroed
+    window, without reading (or zeroing) main_grad."""
+    _embedding(_lib.zr_ipg_accumulate_embedding_first, plan, param, dim, tokens, dy, main_grad,
+               workspace, window_base, window_len, scale, stream)
+
+
+def _embedding(fn, plan, param, dim, tokens, dy, main_grad, workspace, window_base, window_len,
+               scale, stream):
+    ids, wide = _token_ids(tokens)
+    n, d = tokens.numel(), _i64(dim, "dim")
+    ptr, stride = _rows(dy, "dy", (n, d), (torch.bfloat16, torch.float32))
+    wl = main_grad.numel() if window_len is None else _i64(window_len, "window_len")
+    _check(fn(plan.handle, _i64(param, "param"), d, ids, wide, n, scale, ptr, _dtype_code(dy),
+              stride, _dense(main_grad, "main_grad", torch.float32, wl),
+              _i64(window_base, "window_base"), wl, _dense(workspace, "workspace", torch.uint8),
+              workspace.numel(), _stream(stream)))
+
+
+def zr_act_layout(cols):
+    """(codes, scales) per row of a checkpoint of ``cols`` columns."""
+    c, s = c_i64(), c_i64()
+    _check(_lib.zr_act_layout(_i64(cols, "cols"), ctypes.byref(c), ctypes.byref(s)))
+    return c.value, s.value
+
+
+def act_empty(rows, cols, device="cuda"):
+    """Uninitialised (codes, scales) for a checkpoint of [rows, cols]: codes
+    float8_e4m3fn [rows, cols rounded up to 32], scales uint8 [rows, blocks]."""
+    c, s = zr_act_layout(cols)
+    return (torch.empty((rows, c), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((rows, s), dtype=torch.uint8, device=device))
+
+
+def _checkpoint(codes, scales, rows, cols):
+    """Checks a checkpoint's tensors and returns their addresses."""
+    c = -(-cols // 32) * 32
+    for t, name, dtype, want in ((codes, "codes", torch.float8_e4m3fn, (rows, c)),
+                                 (scales, "scales", torch.uint8, (rows, c // 32))):
+        if tuple(t.shape) != want:
+            raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; a checkpoint of "
+                                          f"[{rows}, {cols}] has {want}")
+    return _dense(codes, "codes", torch.float8_e4m3fn), _dense(scales, "scales", torch.uint8)
+
+
+def zr_act_quantize(x, codes, scales, stream=None):
+    """The 8-bit checkpoint of x (bf16 or fp32, [rows, cols]) into the tensors
+    of act_empty."""
+    ptr, stride = _rows(x, "x", (None, None), (torch.bfloat16, torch.float32))
+    rows, cols = x.shape
+    c, s = _checkpoint(codes, scales, rows, cols)
+    _check(_lib.zr_act_quantize(ptr, _dtype_code(x), rows, cols, stride, c, s, _stream(stream)))
+
+
+def zr_act_dequantize(codes, scales, out, stream=None):
+    """The activations a checkpoint stands for, into out (bf16 or fp32,
+    [rows, cols])."""
+    ptr, stride = _rows(out, "out", (None, None), (torch.bfloat16, torch.float32))
+    rows, cols = out.shape
+    c, s = _checkpoint(codes, scales, rows, cols)
+    _check(_lib.zr_act_dequantize(c, s, rows, cols, ptr, _dtype_code(out), stride,
+                                  _stream(stream)))
+
+
+def _linear_items(plan, items):
+    arr = (zr_linear_grad * max(len(items), 1))()
+    for k, (param, dy, codes, scales, *in_major) in enumerate(items):
+        p = _i64(param, f"items[{k}].param")
+        ptr, stride = _rows(dy, f"items[{k}].dy", (None, None), (torch.bfloat16,))
+        tokens, n_out = dy.shape
+        # an out-of-range id is left to the C call's check
+        n_in = plan.numels[p] // max(n_out, 1) if 0 <= p < len(plan.numels) else 1
+        c, s = _checkpoint(codes, scales, tokens, max(n_in, 1))
+        arr[k] = zr_linear_grad(p, n_out, n_in, tokens, ptr, stride, c, s,
+                                int(bool(in_major and in_major[0])))
+    return arr
+
+
+def zr_ipg_linear_workspace(plan, items, window_base, window_len):
+    """Bytes of workspace zr_ipg_accumulate_linear needs for these items."""
+    v = c_i64()
+    _check(_lib.zr_ipg_linear_workspace(plan.handle, _linear_items(plan, items), len(items),
+                                        _i64(window_base, "window_base"),
+                                        _i64(window_len, "window_len"), ctypes.byref(v)))
+    return v.value
+
+
+def zr_ipg_accumulate_linear(plan, items, main_grad, workspace, window_base=0, window_len=None,
+                             stream=None):
+    """main_grad of each item's weight += dY^T X^, X^ the activations of an
+    8-bit checkpoint.  items: (param, dy, codes, scales) or (..., in_major);
+    dy bf16 [tokens, n_out]; in_major True for a weight stored [n_in, n_out].
+    workspace: a uint8 tensor of at least zr_ipg_linear_workspace bytes that
+    no other call uses meanwhile (None where that is 0)."""
+    _linear(_lib.zr_ipg_accumulate_linear, plan, items, main_grad, workspace, window_base,
+            window_len, stream)
+
+
+def zr_ipg_accumulate_linear_first(plan, items, main_grad, workspace, window_base=0,
+                                   window_len=None, stream=None):
+    """The step's first micro-batch: as zr_ipg_accumulate_linear on a zeroed
+    window, without reading (or zeroing) main_grad."""
+    _linear(_lib.zr_ipg_accumulate_linear_first, plan, items, main_grad, workspace, window_base,
+            window_len, stream)
+
+
+def _linear(fn, plan, items, main_grad, workspace, window_base, window_len, stream):
+    wl = main_grad.numel() if window_len is None else _i64(window_len, "window_len")
+    arr = _linear_items(plan, items)
+    ws = None if workspace is None else _dense(workspace, "workspace", torch.uint8)
+    _check(fn(plan.handle, arr, len(items),
+              _dense(main_grad, "main_grad", torch.float32, wl), _i64(window_base, "window_base"),
+              wl, ws, 0 if workspace is None else workspace.numel(), _stream(stream)))
