@@ -145,21 +145,35 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
 // ------------------------------------------------------- weight gradients ---
 //
 // dW[o, i] = sum over tokens t of dY[t, o] * X^[t, i], added to main_grad.
-// Both operands lie token by token, so the sum runs over their slow axis:
-// tiles of kDepth tokens are staged in LDS as bf16 (X decoded once, on the
-// way in), and the transposing LDS read hands each lane of an MFMA its eight
-// tokens of one column.  16-byte units of a staged row are exchanged by the
-// token's number (xor), which spreads the four rows that 16 lanes read over
-// all banks.
+// Both operands lie token by token, so the sum runs over their slow axis.  A
+// workgroup of 2 x 4 waves owns 256 x 256 weights, 128 x 64 a wave in the
+// accumulators; tiles of 64 tokens go through registers (X decoded there, once
+// for the workgroup) into one of two LDS buffers, and the transposing LDS read
+// hands each lane of a 32x32x16 MFMA the eight tokens of its column.  The
+// 16-byte units of a staged row are exchanged (xor) by four times the token's
+// number mod 4, so that the four rows that 16 lanes read, and the two blocks
+// that 32 do, lie in different banks: 3.0 cycles a read, 4.0 with half the
+// distance and 8.0 without.  One barrier a tile: while a tile multiplies, the
+// next fragments, the next tile's stores and the loads of the one after it are
+// under way (phase below).
+//
+// What bounds it: LDS.  A tile costs 64 kB of stores (13.8 cycles a 1 kB
+// store) and 192 kB of reads a CU, 880 and 1150 cycles against the 2050 of
+// its MFMAs; smaller tiles read and store more for each product.  Measured
+// (4096 x 4096 weights, 8192 tokens): 1234 TFLOP/s; 256 x 128 tiles of four
+// waves, two workgroups a CU, 1042; four waves of 128 x 128 1156.
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using s16x4 = short __attribute__((ext_vector_type(4)));
 using f32x16 = float __attribute__((ext_vector_type(16)));
 
 constexpr int kMaxItems = 16;
+
+constexpr int kTileOut = 256;   // columns of dY per workgroup
+constexpr int kTileIn = 256;    // columns of X per workgroup
 constexpr int kDepth = 64;      // tokens per staged tile
-constexpr int kTile = 128;      // columns of dY and of X per workgroup
-constexpr int kThreads = 256;   // 2 x 2 waves of 64 x 64
+constexpr int kWavesOut = 2, kWavesIn = 4;
+constexpr int kThreads = 64 * kWavesOut * kWavesIn;
 
 struct Item {
   const uint16_t* dy;
@@ -181,99 +195,334 @@ struct LinearArgs {
   int32_t first;               // main_grad is written, not added to
 };
 
-// Byte offset of the 16-byte unit u of staged row k.
+// A tile of kDepth tokens and C columns in LDS: 16-byte units (8 bf16) of a
+// token's row, exchanged by the token's number.
+template <int C>
 __device__ __forceinline__ int staged(int k, int u) {
-  return k * (kTile * 2) + ((u ^ (2 * (k & 3))) << 4);
+  return k * (C * 2) + ((u ^ (4 * (k & 3))) << 4);
 }
 
+// The eight tokens of one column that a lane of an MFMA takes, from the
+// 16-token, 32-column block whose place `at` the lane has.
+template <int C>
 __device__ __forceinline__ bf16x8 read_columns(const char* lds, int at) {
   using lds_s16x4 = __attribute__((address_space(3))) s16x4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
-  const s16x4 hi =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at + 4 * (kTile * 2)));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at + 4 * (C * 2)));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-__global__ __launch_bounds__(kThreads) void linear_kernel(const LinearArgs a) {
-  __shared__ __align__(16) char lds[2][kDepth * kTile * 2];
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  int k = 0;
-  while (k + 1 < a.n && a.item[k + 1].tile0 <= static_cast<int>(blockIdx.x)) ++k;
-  const Item& it = a.item[k];
-  const int tile = blockIdx.x - it.tile0;
-  const int64_t o0 = static_cast<int64_t>(it.out_tile0 + tile / it.in_tiles) * kTile;
-  const int64_t i0 = static_cast<int64_t>(it.in_tile0 + tile % it.in_tiles) * kTile;
-  f32x16 acc[2][2] = {};
-  // A lane's place in the transposing read of a 16-token, 32-column block.
-  const int g = lane >> 4, q = lane & 15;
-  const int k_lane = 8 * (g >> 1) + (q >> 2);
-  const int c_lane = 16 * (g & 1) + 4 * (q & 3);
-  for (int64_t t0 = 0; t0 < it.tokens; t0 += kDepth) {
-    __syncthreads();
-    // dY: 64 rows of 16 units of eight bf16.
-    for (int j = tid; j < kDepth * (kTile / 8); j += kThreads) {
-      const int r = j / (kTile / 8), u = j % (kTile / 8);
-      const int64_t t = t0 + r, c = o0 + 8 * u;
-      u32x4 v{0, 0, 0, 0};
-      if (t < it.tokens && c < it.out) {
-        const uint16_t* p = it.dy + t * it.dy_stride + c;
-        if (c + 8 <= it.out) {
-          v = *as_global<u32x4_a2>(p);
-        } else {
-          for (int e = 0; e < it.out - c; ++e)
-            v[e / 2] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
-        }
-      }
-      *reinterpret_cast<u32x4*>(lds[0] + staged(r, u)) = v;
-    }
-    // X: 64 rows of 16 units of eight codes, decoded.
-    for (int j = tid; j < kDepth * (kTile / 8); j += kThreads) {
-      const int r = j / (kTile / 8), u = j % (kTile / 8);
-      const int64_t t = t0 + r, c = i0 + 8 * u;
-      u32x4 v{0, 0, 0, 0};
-      if (t < it.tokens && c < it.pitch) {
-        const u32x2 x = *as_global<u32x2>(it.codes + t * it.pitch + c);
-        const float s = bits_float(
-            static_cast<uint32_t>(it.scales[t * (it.pitch / kBlock) + c / kBlock]) << 23);
+// One step's share of a thread: rows of dY and of X's codes, in registers
+// between their loads and their places in LDS.
+constexpr int kOutUnits = kTileOut / 8, kOutRows = kThreads / kOutUnits;
+constexpr int kOutLoads = kDepth / kOutRows;
+constexpr int kInUnits = kTileIn / 16, kInRows = kThreads / kInUnits;
+constexpr int kInLoads = kDepth / kInRows;
+static_assert(kOutLoads * kOutRows == kDepth && kInLoads * kInRows == kDepth, "staging shape");
+
+struct Staged {
+  u32x4 dy[kOutLoads];
+  u32x4 x[kInLoads];
+  uint32_t scale[kInLoads];
+};
+
+// Where a thread's units of a tile come from.  A unit behind the matrix's last
+// column is read from the tile's first instead: its columns are never stored.
+struct Loader {
+  const char* dy;              // row 0 of the tile's columns
+  const char* codes;
+  const char* scales;
+  int64_t dy_step, x_step, s_step;   // bytes per token
+  uint32_t dy_off, x_off, s_off;     // this thread's first unit
+  int32_t dy_row, x_row, dy_left;    // its rows; dY's columns from its unit on
+
+  __device__ __forceinline__ Loader(const Item& it, int64_t o0, int64_t i0, int tid) {
+    int u = 8 * (tid % kOutUnits), v = 16 * (tid % kInUnits);
+    if (o0 + u >= it.out) u = 0;
+    if (i0 + v >= it.pitch) v = 0;
+    dy_row = tid / kOutUnits;
+    x_row = tid / kInUnits;
+    dy_step = it.dy_stride * 2;
+    x_step = it.pitch;
+    s_step = it.pitch / kBlock;
+    dy = reinterpret_cast<const char*>(it.dy) + o0 * 2;
+    codes = reinterpret_cast<const char*>(it.codes) + i0;
+    scales = reinterpret_cast<const char*>(it.scales) + i0 / kBlock;
+    dy_off = dy_row * static_cast<uint32_t>(dy_step) + 2 * u;
+    x_off = x_row * static_cast<uint32_t>(x_step) + v;
+    s_off = x_row * static_cast<uint32_t>(s_step) + v / kBlock;
+    dy_left = static_cast<int>(it.out - o0 < kTileOut ? it.out - o0 : kTileOut) - u;
+  }
+  // Loads [j0, j1) of dY and of X for the tokens from t on, all there.  A unit
+  // that the row's end cuts is read whole: it ends in the next row.
+  template <int kJ0, int kJ1>
+  __device__ __forceinline__ void load_dy(Staged& s, int64_t t) const {
+    const char* d = dy + t * dy_step;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          v[2 * e] = __builtin_bit_cast(
-              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[e], s, false));
-          v[2 * e + 1] = __builtin_bit_cast(
-              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x[e], s, true));
-        }
-      }
-      *reinterpret_cast<u32x4*>(lds[1] + staged(r, u)) = v;
-    }
-    __syncthreads();
+    for (int j = kJ0; j < kJ1; ++j)
+      s.dy[j] = *as_global<u32x4_a2>(d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step))));
+  }
+  template <int kJ0, int kJ1>
+  __device__ __forceinline__ void load_x(Staged& s, int64_t t) const {
+    const char* x = codes + t * x_step;
+    const char* c = scales + t * s_step;
 #pragma unroll
-    for (int kk = 0; kk < kDepth; kk += 16) {
-      bf16x8 d[2], x[2];
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int cd = (w >> 1) * 64 + 32 * b + c_lane, cx = (w & 1) * 64 + 32 * b + c_lane;
-        d[b] = read_columns(lds[0], staged(kk + k_lane, cd / 8) + (cd % 8) * 2);
-        x[b] = read_columns(lds[1], staged(kk + k_lane, cx / 8) + (cx % 8) * 2);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(d[i], x[j], acc[i][j], 0, 0, 0);
+    for (int j = kJ0; j < kJ1; ++j) {
+      s.x[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
+      s.scale[j] = *as_global<uint8_t>(c + (s_off + j * (kInRows * static_cast<uint32_t>(s_step))));
     }
   }
+  // The same for `tokens` tokens, fewer than kDepth perhaps, up to the last.
+  __device__ __forceinline__ void load_some(Staged& s, int64_t t, int64_t tokens) const {
+    const char* d = dy + t * dy_step;
+    const char* x = codes + t * x_step;
+    const char* c = scales + t * s_step;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < kOutLoads; ++j) {
+      s.dy[j] = u32x4{0, 0, 0, 0};
+      if (dy_row + j * kOutRows < tokens) {
+        const char* p = d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step)));
+        if (dy_left >= 8) {
+          s.dy[j] = *as_global<u32x4_a2>(p);
+        } else {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int64_t o = o0 + (w >> 1) * 64 + 32 * i + 8 * (v / 4) + 4 * (lane >> 5) + (v & 3);
-        const int64_t c = i0 + (w & 1) * 64 + 32 * j + (lane & 31);
-        const int64_t e = it.in_major ? c * it.out + o : o * it.in + c;
-        if (o < it.out && c < it.in && e >= it.first && e < it.last)
-          it.grad[e] = (a.first ? 0.0f : it.grad[e]) + acc[i][j][v];
+          for (int e = 0; e < 7; ++e)
+            if (e < dy_left)
+              s.dy[j][e / 2] |= static_cast<uint32_t>(as_global<uint16_t>(p)[e]) << (16 * (e & 1));
+        }
       }
+    }
+#pragma unroll
+    for (int j = 0; j < kInLoads; ++j) {
+      s.x[j] = u32x4{0, 0, 0, 0};
+      s.scale[j] = 127;
+      if (x_row + j * kInRows < tokens) {
+        s.x[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
+        s.scale[j] = *as_global<uint8_t>(c + (s_off + j * (kInRows * static_cast<uint32_t>(s_step))));
+      }
+    }
+  }
+};
+
+// A staged tile in LDS: dY's columns, then X's, decoded.
+constexpr int kOutBytes = kDepth * kTileOut * 2, kInBytes = kDepth * kTileIn * 2;
+constexpr int kStage = kOutBytes + kInBytes;
+
+template <int kJ0, int kJ1>
+__device__ __forceinline__ void store_dy(const Staged& s, char* lds, int tid) {
+#pragma unroll
+  for (int j = kJ0; j < kJ1; ++j)
+    *reinterpret_cast<u32x4*>(lds + staged<kTileOut>(tid / kOutUnits + j * kOutRows, tid % kOutUnits)) =
+        s.dy[j];
+}
+template <int kJ0, int kJ1>
+__device__ __forceinline__ void store_x(const Staged& s, char* lds, int tid) {
+  const int v = tid % kInUnits, half = (tid >> 2) & 1;
+#pragma unroll
+  for (int j = kJ0; j < kJ1; ++j) {
+    const float scale = bits_float(s.scale[j] << 23);
+    u32x4 w[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      w[e / 2][2 * (e & 1)] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.x[j][e], scale, false));
+      w[e / 2][2 * (e & 1) + 1] = __builtin_bit_cast(
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.x[j][e], scale, true));
+    }
+    // Eight lanes write eight different units of 128 bytes at a time.
+    char* x = lds + kOutBytes;
+    const int k = tid / kInUnits + j * kInRows;
+    *reinterpret_cast<u32x4*>(x + staged<kTileIn>(k, 2 * v + half)) = half ? w[1] : w[0];
+    *reinterpret_cast<u32x4*>(x + staged<kTileIn>(k, 2 * v + 1 - half)) = half ? w[0] : w[1];
+  }
+}
+
+constexpr int kOutBlocks = kTileOut / kWavesOut / 32;   // 32-column blocks of a wave
+constexpr int kInBlocks = kTileIn / kWavesIn / 32;
+
+using Acc = f32x16[kOutBlocks][kInBlocks];
+
+// The fragments of sixteen tokens that a wave multiplies.
+struct Fragments {
+  bf16x8 d[kOutBlocks], x[kInBlocks];
+};
+struct Reader {
+  int d[kOutBlocks], x[kInBlocks];   // a lane's places in a staged tile
+  __device__ __forceinline__ Reader(int lane, int w) {
+    const int g = lane >> 4, q = lane & 15;
+    const int k = 8 * (g >> 1) + (q >> 2), c = 16 * (g & 1) + 4 * (q & 3);
+#pragma unroll
+    for (int b = 0; b < kOutBlocks; ++b) {
+      const int at = (w / kWavesIn) * (32 * kOutBlocks) + 32 * b + c;
+      d[b] = staged<kTileOut>(k, at / 8) + (at % 8) * 2;
+    }
+#pragma unroll
+    for (int b = 0; b < kInBlocks; ++b) {
+      const int at = (w % kWavesIn) * (32 * kInBlocks) + 32 * b + c;
+      x[b] = kOutBytes + staged<kTileIn>(k, at / 8) + (at % 8) * 2;
+    }
+  }
+  __device__ __forceinline__ void read(Fragments& f, const char* lds, int k) const {
+#pragma unroll
+    for (int b = 0; b < kOutBlocks; ++b) f.d[b] = read_columns<kTileOut>(lds, d[b] + k * (kTileOut * 2));
+#pragma unroll
+    for (int b = 0; b < kInBlocks; ++b) f.x[b] = read_columns<kTileIn>(lds, x[b] + k * (kTileIn * 2));
+  }
+};
+
+template <bool kInMajor>
+__device__ __forceinline__ void multiply(Acc& acc, const Fragments& f) {
+#pragma unroll
+  for (int i = 0; i < kOutBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < kInBlocks; ++j)
+      acc[i][j] = kInMajor
+                      ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[j], f.d[i], acc[i][j], 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.d[i], f.x[j], acc[i][j], 0, 0, 0);
+}
+
+// All waves' LDS accesses before it are done after it; loads from global
+// memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Sixteen tokens of the pipelined loop: the next fragments are read, a third
+// of the next tile is put into LDS and a third of the one after it loaded
+// while these multiply.
+template <bool kInMajor, int kPhase>
+__device__ __forceinline__ void phase(Acc& acc, Fragments (&f)[2], Staged& s, const Loader& in,
+                                      const Reader& reader, char* cur, char* next, int64_t t_load,
+                                      int tid) {
+  constexpr int kPhases = kDepth / 16, kParts = kPhases - 1;
+  static_assert(kPhases == 4, "tile_sums runs four phases");
+  if constexpr (kPhase == kPhases - 1) {
+    lds_barrier();
+    reader.read(f[(kPhase + 1) & 1], next, 0);
+  } else {
+    reader.read(f[(kPhase + 1) & 1], cur, 16 * (kPhase + 1));
+    constexpr int d0 = kOutLoads * kPhase / kParts, d1 = kOutLoads * (kPhase + 1) / kParts;
+    constexpr int x0 = kInLoads * kPhase / kParts, x1 = kInLoads * (kPhase + 1) / kParts;
+    store_dy<d0, d1>(s, next, tid);
+    store_x<x0, x1>(s, next, tid);
+    in.load_dy<d0, d1>(s, t_load);
+    in.load_x<x0, x1>(s, t_load);
+  }
+  multiply<kInMajor>(acc, f[kPhase & 1]);
+}
+
+// The tile's sums over the tokens [t0, t1), added to the MFMAs' accumulators:
+// a block's rows are the weight's stored rows, its columns a row's elements.
+template <bool kInMajor>
+__device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0, int64_t t0,
+                                          int64_t t1, char* lds, Acc& acc) {
+  const int tid = threadIdx.x;
+  const Loader in(it, o0, i0, tid);
+  const Reader reader(tid & 63, uniform(tid >> 6));
+  Staged s;
+  // Whole tiles of tokens.  The matrix's last row cannot be read past its end,
+  // and a row of fewer than eight columns ends behind the next row.
+  int64_t end = it.out % 8 && t1 == it.tokens ? t1 - 1 : t1;
+  const int steps = it.out < 8 ? 0 : static_cast<int>((end - t0) / kDepth);
+  if (steps > 0) {
+    in.load_dy<0, kOutLoads>(s, t0);
+    in.load_x<0, kInLoads>(s, t0);
+    store_dy<0, kOutLoads>(s, lds, tid);
+    store_x<0, kInLoads>(s, lds, tid);
+    const int64_t last = t0 + static_cast<int64_t>(steps - 1) * kDepth;
+    int64_t t = t0 + kDepth < last ? t0 + kDepth : last;
+    in.load_dy<0, kOutLoads>(s, t);
+    in.load_x<0, kInLoads>(s, t);
+    lds_barrier();
+    Fragments f[2];
+    reader.read(f[0], lds, 0);
+    int stage = 0;
+    for (int n = 0; n < steps; ++n) {
+      char* cur = lds + stage;
+      stage = kStage - stage;
+      char* next = lds + stage;
+      // behind the last tile, the last is loaded and staged again, unused
+      t = t + kDepth < last ? t + kDepth : last;
+      phase<kInMajor, 0>(acc, f, s, in, reader, cur, next, t, tid);
+      phase<kInMajor, 1>(acc, f, s, in, reader, cur, next, t, tid);
+      phase<kInMajor, 2>(acc, f, s, in, reader, cur, next, t, tid);
+      phase<kInMajor, 3>(acc, f, s, in, reader, cur, next, t, tid);
+    }
+    t0 += static_cast<int64_t>(steps) * kDepth;
+  }
+  for (; t0 < t1; t0 += kDepth) {
+    in.load_some(s, t0, t1 - t0);
+    lds_barrier();
+    store_dy<0, kOutLoads>(s, lds, tid);
+    store_x<0, kInLoads>(s, lds, tid);
+    lds_barrier();
+#pragma unroll 1
+    for (int k = 0; k < kDepth; k += 16) {
+      Fragments f;
+      reader.read(f, lds, k);
+      multiply<kInMajor>(acc, f);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a) {
+  __shared__ __align__(16) char lds[2 * kStage];
+  const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
+  // Workgroups go round the eight XCDs; each XCD takes neighbouring tiles.
+  const int total = gridDim.x, per = total / 8, more = total % 8;
+  const int xcd = blockIdx.x % 8;
+  const int id = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
+  int k = 0;
+  while (k + 1 < a.n && a.item[k + 1].tile0 <= id) ++k;
+  const Item& it = a.item[k];
+  // Bands of eight tiles of dY's columns, walked along X's columns.
+  const int tile = id - it.tile0;
+  const int band = tile / (8 * it.in_tiles), in_band = tile - band * 8 * it.in_tiles;
+  const int height = it.out_tiles - 8 * band < 8 ? it.out_tiles - 8 * band : 8;
+  const int64_t o0 = static_cast<int64_t>(it.out_tile0 + 8 * band + in_band % height) * kTileOut;
+  const int64_t i0 = static_cast<int64_t>(it.in_tile0 + in_band / height) * kTileIn;
+  Acc acc = {};
+  if (it.tokens > 0) {
+    if (it.in_major) tile_sums<true>(it, o0, i0, 0, it.tokens, lds, acc);
+    else tile_sums<false>(it, o0, i0, 0, it.tokens, lds, acc);
+  }
+  // Stored rows and columns of the wave's blocks.
+  const int64_t r0 = it.in_major ? i0 + (w % kWavesIn) * (32 * kInBlocks)
+                                 : o0 + (w / kWavesIn) * (32 * kOutBlocks);
+  const int64_t c0 = it.in_major ? o0 + (w / kWavesIn) * (32 * kOutBlocks)
+                                 : i0 + (w % kWavesIn) * (32 * kInBlocks);
+  const int64_t rows = it.in_major ? it.in : it.out, cols = it.in_major ? it.out : it.in;
+  const int64_t rb = it.in_major ? kTileIn : kTileOut, cb = it.in_major ? kTileOut : kTileIn;
+  const int64_t tr = it.in_major ? i0 : o0, tc = it.in_major ? o0 : i0;
+  const bool whole = tr + rb <= rows && tc + cb <= cols && tr * cols + tc >= it.first &&
+                     (tr + rb - 1) * cols + tc + cb <= it.last;
+#pragma unroll
+  for (int i = 0; i < kOutBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < kInBlocks; ++j) {
+      const int64_t r = r0 + 32 * (it.in_major ? j : i) + 4 * (lane >> 5);
+      const int64_t c = c0 + 32 * (it.in_major ? i : j) + (lane & 31);
+      if (whole) {
+        float* p = it.grad + r * cols + c;
+        float old[16] = {};
+        if (!a.first) {
+#pragma unroll
+          for (int v = 0; v < 16; ++v) old[v] = *as_global<float>(p + (8 * (v / 4) + (v & 3)) * cols);
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+          *as_global<float>(p + (8 * (v / 4) + (v & 3)) * cols) = old[v] + acc[i][j][v];
+      } else {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int64_t row = r + 8 * (v / 4) + (v & 3), e = row * cols + c;
+          if (row < rows && c < cols && e >= it.first && e < it.last)
+            it.grad[e] = (a.first ? 0.0f : it.grad[e]) + acc[i][j][v];
+        }
+      }
+    }
 }
 
 zr_status check_rows(const void* codes, const uint8_t* scales, int64_t rows, int64_t cols) {
@@ -330,7 +579,8 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
       return fail(ZR_ERR_INVALID, "n_out * n_in must be the param's elements");
     st = check_rows(z.codes, z.scales, z.tokens, z.n_in);
     if (st != ZR_OK) return st;
-    if (z.n_out >= (int64_t(1) << 30)) return fail(ZR_ERR_UNSUPPORTED, "2^30 outputs or more");
+    if (z.n_in >= (int64_t(1) << 24) || z.dy_stride >= (int64_t(1) << 24))
+      return fail(ZR_ERR_UNSUPPORTED, "n_in or dy_stride of 2^24 or more");   // 32-bit offsets in a tile
     if (z.dy_stride < z.n_out) return fail(ZR_ERR_INVALID, "dy_stride must be >= n_out");
     if (z.tokens > 0 && (!z.dy || !aligned_to(z.dy, 2)))
       return fail(ZR_ERR_INVALID, "dy is null or not element-aligned");
@@ -350,8 +600,9 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
     it.in_major = z.in_major != 0;
     // Tiles of the stored rows that meet the window; within a row, all.
     const int64_t row = it.in_major ? it.out : it.in;
-    const int64_t r0 = clip.first / row / kTile, r1 = ceil_div(ceil_div(clip.last, row), kTile);
-    const int64_t all = ceil_div(row, kTile);
+    const int64_t high = it.in_major ? kTileIn : kTileOut, wide = it.in_major ? kTileOut : kTileIn;
+    const int64_t r0 = clip.first / row / high, r1 = ceil_div(ceil_div(clip.last, row), high);
+    const int64_t all = ceil_div(row, wide);
     if ((r1 - r0) * all > 0x3fffffff) return fail(ZR_ERR_UNSUPPORTED, "weight too large for one call");
     (it.in_major ? it.in_tile0 : it.out_tile0) = static_cast<int32_t>(r0);
     it.in_tiles = static_cast<int32_t>(it.in_major ? r1 - r0 : all);
