@@ -186,13 +186,18 @@ struct Item {
   int64_t pitch;               // bytes per row of codes
   int32_t out_tile0, in_tile0; // first tiles that meet the window
   int32_t out_tiles, in_tiles;
-  int32_t tile0;               // tiles of earlier items
   int32_t in_major;            // weight stored [in][out] rather than [out][in]
+  // The first `whole` tiles are one workgroup's each; the others' tokens are
+  // cut into `pieces`, a workgroup each.
+  int32_t whole, pieces;
+  int32_t whole0, piece0, cut0;   // whole tiles, pieces and cut tiles of earlier items
 };
 struct LinearArgs {
   Item item[kMaxItems];
+  float* partial;              // a tile of sums for each piece
   int32_t n;
   int32_t first;               // main_grad is written, not added to
+  int32_t whole;               // whole tiles in all
 };
 
 // A tile of kDepth tokens and C columns in LDS: 16-byte units (8 bf16) of a
@@ -467,62 +472,121 @@ __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0
   }
 }
 
+// A tile's place: its first columns of dY and X.  Bands of eight tiles of dY's
+// columns are walked along X's columns.
+struct Place {
+  int64_t o0, i0;
+  bool whole;                  // all its weights are there and in the window
+  __device__ __forceinline__ Place(const Item& it, int tile) {
+    const int band = tile / (8 * it.in_tiles), at = tile - band * 8 * it.in_tiles;
+    const int height = it.out_tiles - 8 * band < 8 ? it.out_tiles - 8 * band : 8;
+    o0 = static_cast<int64_t>(it.out_tile0 + 8 * band + at % height) * kTileOut;
+    i0 = static_cast<int64_t>(it.in_tile0 + at / height) * kTileIn;
+    const int64_t r = it.in_major ? i0 : o0, c = it.in_major ? o0 : i0;
+    const int64_t rows = it.in_major ? it.in : it.out, cols = it.in_major ? it.out : it.in;
+    const int high = it.in_major ? kTileIn : kTileOut, wide = it.in_major ? kTileOut : kTileIn;
+    whole = r + high <= rows && c + wide <= cols && r * cols + c >= it.first &&
+            (r + high - 1) * cols + c + wide <= it.last;
+  }
+};
+
+// kCount of the sixteen sums that a lane has of block (i, j), from the v0-th
+// on, into main_grad: stored rows 8 * (v / 4) + v % 4, one column a lane.
+template <int kCount, typename V>
+__device__ __forceinline__ void put_sums(const Item& it, const Place& at, bool first, int w,
+                                         int lane, int i, int j, int v0, const V& sums) {
+  const int64_t o = at.o0 + (w / kWavesIn) * (32 * kOutBlocks) + 32 * i;
+  const int64_t c = at.i0 + (w % kWavesIn) * (32 * kInBlocks) + 32 * j;
+  const int64_t cols = it.in_major ? it.out : it.in, rows = it.in_major ? it.in : it.out;
+  const int64_t row = (it.in_major ? c : o) + 4 * (lane >> 5);
+  const int64_t col = (it.in_major ? o : c) + (lane & 31);
+  if (at.whole) {
+    float* p = it.grad + row * cols + col;
+    float old[kCount] = {};
+    if (!first) {
+#pragma unroll
+      for (int v = 0; v < kCount; ++v)
+        old[v] = *as_global<float>(p + (8 * ((v0 + v) / 4) + ((v0 + v) & 3)) * cols);
+    }
+#pragma unroll
+    for (int v = 0; v < kCount; ++v)
+      *as_global<float>(p + (8 * ((v0 + v) / 4) + ((v0 + v) & 3)) * cols) = old[v] + sums[v];
+  } else {
+#pragma unroll
+    for (int v = 0; v < kCount; ++v) {
+      const int64_t r = row + 8 * ((v0 + v) / 4) + ((v0 + v) & 3), e = r * cols + col;
+      if (r < rows && col < cols && e >= it.first && e < it.last)
+        it.grad[e] = (first ? 0.0f : it.grad[e]) + sums[v];
+    }
+  }
+}
+
 __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a) {
   __shared__ __align__(16) char lds[2 * kStage];
-  const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
-  // Workgroups go round the eight XCDs; each XCD takes neighbouring tiles.
-  const int total = gridDim.x, per = total / 8, more = total % 8;
-  const int xcd = blockIdx.x % 8;
-  const int id = xcd * per + (xcd < more ? xcd : more) + blockIdx.x / 8;
-  int k = 0;
-  while (k + 1 < a.n && a.item[k + 1].tile0 <= id) ++k;
-  const Item& it = a.item[k];
-  // Bands of eight tiles of dY's columns, walked along X's columns.
-  const int tile = id - it.tile0;
-  const int band = tile / (8 * it.in_tiles), in_band = tile - band * 8 * it.in_tiles;
-  const int height = it.out_tiles - 8 * band < 8 ? it.out_tiles - 8 * band : 8;
-  const int64_t o0 = static_cast<int64_t>(it.out_tile0 + 8 * band + in_band % height) * kTileOut;
-  const int64_t i0 = static_cast<int64_t>(it.in_tile0 + in_band / height) * kTileIn;
-  Acc acc = {};
-  if (it.tokens > 0) {
-    if (it.in_major) tile_sums<true>(it, o0, i0, 0, it.tokens, lds, acc);
-    else tile_sums<false>(it, o0, i0, 0, it.tokens, lds, acc);
+  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
+  // Consecutive workgroups go round the eight XCDs: of the 256 that run at
+  // once, each XCD takes 32 neighbours, which share columns in its L2.
+  const int round = blockIdx.x & ~255;
+  const int now = static_cast<int>(gridDim.x) - round < 256 ? gridDim.x - round : 256;
+  const int xcd = blockIdx.x % 8, more = now % 8;
+  const int id = round + xcd * (now / 8) + (xcd < more ? xcd : more) + (blockIdx.x - round) / 8;
+  int k = 0, tile;
+  int64_t t0 = 0, t1;
+  float* partial = nullptr;
+  if (id < a.whole) {
+    while (k + 1 < a.n && a.item[k + 1].whole0 <= id) ++k;
+    tile = id - a.item[k].whole0;
+    t1 = a.item[k].tokens;
+  } else {
+    const int piece = id - a.whole;
+    while (k + 1 < a.n && a.item[k + 1].piece0 <= piece) ++k;
+    const Item& it = a.item[k];
+    const int cut = it.out_tiles * it.in_tiles - it.whole;
+    const int p = (piece - it.piece0) / cut;
+    tile = it.whole + (piece - it.piece0) % cut;
+    const int64_t steps = (it.tokens + kDepth - 1) / kDepth;
+    t0 = p * steps / it.pieces * kDepth;
+    t1 = p + 1 < it.pieces ? (p + 1) * steps / it.pieces * kDepth : it.tokens;
+    partial = a.partial + static_cast<int64_t>(piece) * (kTileOut * kTileIn);
   }
-  // Stored rows and columns of the wave's blocks.
-  const int64_t r0 = it.in_major ? i0 + (w % kWavesIn) * (32 * kInBlocks)
-                                 : o0 + (w / kWavesIn) * (32 * kOutBlocks);
-  const int64_t c0 = it.in_major ? o0 + (w / kWavesIn) * (32 * kOutBlocks)
-                                 : i0 + (w % kWavesIn) * (32 * kInBlocks);
-  const int64_t rows = it.in_major ? it.in : it.out, cols = it.in_major ? it.out : it.in;
-  const int64_t rb = it.in_major ? kTileIn : kTileOut, cb = it.in_major ? kTileOut : kTileIn;
-  const int64_t tr = it.in_major ? i0 : o0, tc = it.in_major ? o0 : i0;
-  const bool whole = tr + rb <= rows && tc + cb <= cols && tr * cols + tc >= it.first &&
-                     (tr + rb - 1) * cols + tc + cb <= it.last;
+  const Item& it = a.item[k];
+  const Place at(it, tile);
+  Acc acc = {};
+  if (it.in_major) tile_sums<true>(it, at.o0, at.i0, t0, t1, lds, acc);
+  else tile_sums<false>(it, at.o0, at.i0, t0, t1, lds, acc);
 #pragma unroll
   for (int i = 0; i < kOutBlocks; ++i)
 #pragma unroll
     for (int j = 0; j < kInBlocks; ++j) {
-      const int64_t r = r0 + 32 * (it.in_major ? j : i) + 4 * (lane >> 5);
-      const int64_t c = c0 + 32 * (it.in_major ? i : j) + (lane & 31);
-      if (whole) {
-        float* p = it.grad + r * cols + c;
-        float old[16] = {};
-        if (!a.first) {
+      if (partial) {
 #pragma unroll
-          for (int v = 0; v < 16; ++v) old[v] = *as_global<float>(p + (8 * (v / 4) + (v & 3)) * cols);
-        }
-#pragma unroll
-        for (int v = 0; v < 16; ++v)
-          *as_global<float>(p + (8 * (v / 4) + (v & 3)) * cols) = old[v] + acc[i][j][v];
+        for (int v = 0; v < 4; ++v)
+          *as_global<f32x4>(partial + (((i * kInBlocks + j) * 4 + v) * kThreads + tid) * 4) =
+              f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
       } else {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int64_t row = r + 8 * (v / 4) + (v & 3), e = row * cols + c;
-          if (row < rows && c < cols && e >= it.first && e < it.last)
-            it.grad[e] = (a.first ? 0.0f : it.grad[e]) + acc[i][j][v];
-        }
+        put_sums<16>(it, at, a.first, w, lane, i, j, 0, acc[i][j]);
       }
     }
+}
+
+// Adds up the pieces of the cut tiles, in their order: a workgroup for each
+// four rows of each block.
+constexpr int kJoins = kOutBlocks * kInBlocks * 4;
+__global__ __launch_bounds__(kThreads) void linear_join_kernel(const LinearArgs a) {
+  const int tid = threadIdx.x, cut = blockIdx.x / kJoins, part = blockIdx.x % kJoins;
+  int k = 0;
+  while (k + 1 < a.n && a.item[k + 1].cut0 <= cut) ++k;
+  const Item& it = a.item[k];
+  const int tile = cut - it.cut0;
+  const int64_t step = static_cast<int64_t>(it.out_tiles * it.in_tiles - it.whole) * (kTileOut * kTileIn);
+  const float* p = a.partial + (static_cast<int64_t>(it.piece0) + tile) * (kTileOut * kTileIn) +
+                   (part * kThreads + tid) * 4;
+  f32x4 sum = *as_global<f32x4>(p);
+#pragma unroll 8
+  for (int n = 1; n < it.pieces; ++n) sum += *as_global<f32x4>(p + n * step);
+  const int block = part / 4;
+  put_sums<4>(it, Place(it, it.whole + tile), a.first, uniform(tid >> 6), tid & 63,
+              block / kInBlocks, block % kInBlocks, 4 * (part % 4), sum);
 }
 
 zr_status check_rows(const void* codes, const uint8_t* scales, int64_t rows, int64_t cols) {
@@ -609,9 +673,62 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
     it.out_tiles = static_cast<int32_t>(it.in_major ? all : r1 - r0);
     out->push_back(it);
   }
+  // Tiles with most tokens first: the last to start are the shortest.
+  std::stable_sort(out->begin(), out->end(),
+                   [](const Item& a, const Item& b) { return a.tokens > b.tokens; });
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
     return fail(ZR_ERR_INVALID, "param listed twice in one call");
+  return ZR_OK;
+}
+
+// The launch of up to kMaxItems items: which tiles are one workgroup's, and
+// which are cut along their tokens so that the last round of tiles fills the
+// chip's 256 CUs (one workgroup each).  Cutting costs the pieces' writes and
+// reads, about the time of sixteen tiles of tokens when every CU has a piece
+// (256 kB each, 64 MB in all: 25 us against 1.7 us a tile), so it has to save
+// more than that.  Measured, cut and not, over 8192 tokens: 2304 x 768 and
+// 768 x 768 weights (36 tiles, 7 pieces each) 61 and 178 us, 14336 x 4096
+// (896 tiles, the last 128 in 2 pieces) 818 and 865 us; over 4096 tokens 2560
+// x 2560 (100 tiles in 2 pieces) 72 and 95 us.
+constexpr int kCus = 256, kCutCost = 16;
+
+struct Launch {
+  LinearArgs a;
+  int64_t grid = 0, cut = 0, bytes = 0;   // workgroups, cut tiles, workspace
+};
+zr_status plan_launch(const Item* items, size_t n, bool first, Launch* out) {
+  LinearArgs& a = out->a;
+  a = LinearArgs{};
+  a.first = first;
+  a.n = static_cast<int32_t>(n);
+  int64_t tiles = 0;
+  for (size_t k = 0; k < n; ++k) tiles += int64_t(items[k].out_tiles) * items[k].in_tiles;
+  if (tiles > 0x3fffffff) return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
+  const int64_t rest = tiles % kCus;   // tiles of the last round
+  int64_t before = 0, whole = 0, pieces = 0;
+  for (size_t k = 0; k < n; ++k) {
+    Item& it = a.item[k] = items[k];
+    const int64_t count = int64_t(it.out_tiles) * it.in_tiles;
+    const int64_t steps = ceil_div(it.tokens, kDepth);
+    it.pieces = 1;
+    if (rest > 0) it.pieces = static_cast<int32_t>(std::min(kCus / rest, steps / 4));
+    it.whole = static_cast<int32_t>(std::min(count, std::max<int64_t>(0, tiles - rest - before)));
+    if (it.pieces < 2 || steps - ceil_div(steps, it.pieces) < kCutCost) {
+      it.pieces = 1;
+      it.whole = static_cast<int32_t>(count);
+    }
+    it.whole0 = static_cast<int32_t>(whole);
+    it.piece0 = static_cast<int32_t>(pieces);
+    it.cut0 = static_cast<int32_t>(out->cut);
+    before += count;
+    whole += it.whole;
+    out->cut += count - it.whole;
+    pieces += (count - it.whole) * it.pieces;
+  }
+  a.whole = static_cast<int32_t>(whole);
+  out->grid = whole + pieces;
+  out->bytes = pieces * (kTileOut * kTileIn * 4);
   return ZR_OK;
 }
 
@@ -622,20 +739,24 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
     std::vector<Item> todo;
     zr_status st = linear_items(plan, items, n, main_grad, window_base, window_len, first, &todo);
     if (st != ZR_OK) return st;
-    (void)workspace;
-    (void)workspace_bytes;
-    for (size_t b = 0; b < todo.size(); b += kMaxItems) {
-      LinearArgs a{};
-      a.first = first;
-      int64_t tiles = 0;
-      for (size_t k = b; k < todo.size() && k < b + kMaxItems; ++k) {
-        todo[k].tile0 = static_cast<int32_t>(tiles);
-        tiles += int64_t(todo[k].out_tiles) * todo[k].in_tiles;
-        a.item[a.n++] = todo[k];
-      }
-      if (tiles > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
-      linear_kernel<<<tiles, kThreads, 0, stream>>>(a);
+    std::vector<Launch> launches(ceil_div(todo.size(), kMaxItems));
+    for (size_t b = 0; b < launches.size(); ++b) {
+      const size_t k = b * kMaxItems;
+      Launch& l = launches[b];
+      st = plan_launch(&todo[k], std::min<size_t>(kMaxItems, todo.size() - k), first, &l);
+      if (st != ZR_OK) return st;
+      if (l.bytes > 0 && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < l.bytes))
+        return fail(ZR_ERR_INVALID, "workspace is null, not 16-byte aligned or smaller than " +
+                                        std::to_string(l.bytes) + " bytes");
+      l.a.partial = static_cast<float*>(workspace);
+    }
+    for (const Launch& l : launches) {
+      linear_kernel<<<l.grid, kThreads, 0, stream>>>(l.a);
       st = launched("linear gradient launch");
+      if (st != ZR_OK) return st;
+      if (l.cut == 0) continue;
+      linear_join_kernel<<<l.cut * kJoins, kThreads, 0, stream>>>(l.a);
+      st = launched("linear gradient join launch");
       if (st != ZR_OK) return st;
     }
     return ZR_OK;
@@ -692,11 +813,19 @@ extern "C" zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linea
                                              int64_t* bytes) {
   return guarded([&]() -> zr_status {
     if (!bytes) return fail(ZR_ERR_INVALID, "null output pointer");
-    std::vector<Item> todo;
-    const zr_status st = linear_items(plan, items, n, reinterpret_cast<const float*>(4),
-                                      window_base, window_len, true, &todo);
-    if (st != ZR_OK) return st;
     *bytes = 0;
+    for (const bool first : {false, true}) {   // items without tokens are only in one
+      std::vector<Item> todo;
+      zr_status st = linear_items(plan, items, n, reinterpret_cast<const float*>(4), window_base,
+                                  window_len, first, &todo);
+      if (st != ZR_OK) return st;
+      for (size_t k = 0; k < todo.size(); k += kMaxItems) {
+        Launch l;
+        st = plan_launch(&todo[k], std::min<size_t>(kMaxItems, todo.size() - k), first, &l);
+        if (st != ZR_OK) return st;
+        *bytes = std::max(*bytes, l.bytes);
+      }
+    }
     return ZR_OK;
   });
 }
