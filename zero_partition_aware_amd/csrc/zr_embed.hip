@@ -125,37 +125,56 @@ struct EmbedWork {       // the caller's workspace
 struct SortArgs {
   Tokens tokens;
   EmbedWork w;
-  int64_t n, row0, rows;  // the window's rows: [row0, row0 + rows)
+  int64_t n, row0;
+  int32_t rows;           // the window's rows: [row0, row0 + rows)
   int32_t span;           // rows per workgroup
   // first micro-batch only: rows without tokens are zeroed
   float* main_grad;       // null otherwise; where the table's element 0 lies
   int64_t dim, first, last;
 };
 
+// kGroup times 64 ids of a wave's share at once, as rows relative to the
+// window's first; -1 for an id without a row in the window.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t end, int32_t (&r)[kGroup]) {
+  int64_t t[kGroup];
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g)
+    t[g] = i + 64 * g < end ? token_at(a.tokens, i + 64 * g) - a.row0 : -1;
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) r[g] = t[g] >= 0 && t[g] < a.rows ? static_cast<int32_t>(t[g]) : -1;
+}
+
 // Workgroup g sorts the tokens of rows [g*span, (g+1)*span): it counts, over
 // the whole batch, the tokens of earlier rows (its first place in the order)
 // and those of each row of its own, by wave; then every wave places its share
 // of the batch, in order, behind what earlier rows and earlier waves have.
-// Two reads of the ids by each workgroup, which stay in L2, in one launch:
-// measured against the work that follows, the ids are 1/1000 of the bytes.
+// Every workgroup reads all ids twice (from L2), so that one launch sorts and
+// nothing waits for another workgroup.  Lanes of one row find each other by a
+// ballot on each bit of the row: a row that fills the wave costs no more than
+// 64 different ones.
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortArgs a) {
   __shared__ int32_t place[kSortWaves][kSortRows];
   __shared__ int32_t wave_sum[kSortWaves];
   __shared__ int32_t before_s;
   __shared__ uint8_t empty[kSortRows];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.span;
-  const int span = static_cast<int>(a.rows - lo < a.span ? a.rows - lo : a.span);
+  const int lo = blockIdx.x * a.span;
+  const int span = a.rows - lo < a.span ? a.rows - lo : a.span;
   for (int i = tid; i < kSortWaves * kSortRows; i += blockDim.x) (&place[0][0])[i] = 0;
   if (tid == 0) before_s = 0;
   __syncthreads();
   const int64_t share = (a.n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
   const int64_t i0 = w * share, i1 = i0 + share < a.n ? i0 + share : a.n;
   int before = 0;
-  for (int64_t i = i0 + lane; i < i1; i += 64) {
-    const int64_t r = token_at(a.tokens, i) - a.row0;
-    if (r >= 0 && r < lo) ++before;
-    if (r >= lo && r < lo + span) atomicAdd(&place[w][r - lo], 1);
+  for (int64_t i = i0; i < i1; i += 64 * kGroup) {
+    int32_t r[kGroup];
+    load_rows(a, i + lane, i1, r);
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      if (r[g] >= 0 && r[g] < lo) ++before;
+      if (r[g] >= lo && r[g] < lo + span) atomicAdd(&place[w][r[g] - lo], 1);
+    }
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
@@ -182,42 +201,42 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
     at += c;
   }
   __syncthreads();
-  for (int64_t b = i0; b < i1; b += 64) {
-    const int64_t i = b + lane;
-    int64_t r = -1;
-    if (i < i1) r = token_at(a.tokens, i) - a.row0 - lo;
-    const bool mine = r >= 0 && r < span;
-    uint64_t left = __ballot(mine);
-    while (left) {
-      const int row = __builtin_amdgcn_readlane(static_cast<int>(r), __builtin_ctzll(left));
-      const uint64_t same = __ballot(mine && static_cast<int>(r) == row);
-      const int p = place[w][row];
-      if (mine && static_cast<int>(r) == row) {
-        const int q = p + __popcll(same & ((1ull << lane) - 1));
-        a.w.pos[q] = static_cast<int32_t>(i);
-        a.w.row[q] = static_cast<int32_t>(lo) + row;
+  const int bits = 32 - __builtin_clz(a.span);
+  for (int64_t i = i0; i < i1; i += 64 * kGroup) {
+    int32_t r[kGroup];
+    load_rows(a, i + lane, i1, r);
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      const int row = r[g] - lo;
+      const bool mine = r[g] >= lo && row < span;
+      uint64_t same = __ballot(mine);
+      if (same == 0) continue;
+      for (int b = 0; b < bits; ++b) {
+        const bool one = (row >> b) & 1;
+        const uint64_t ones = __ballot(one);
+        same &= one ? ones : ~ones;
       }
-      place[w][row] = p + __popcll(same);
-      left &= ~same;
+      if (mine) {
+        const int p = place[w][row], rank = __popcll(same & ((1ull << lane) - 1));
+        a.w.pos[p + rank] = static_cast<int32_t>(i + 64 * g + lane);
+        a.w.row[p + rank] = r[g];
+        if ((same >> lane) == 1) place[w][row] = p + rank + 1;   // the row's last lane
+      }
     }
   }
   if (!a.main_grad) return;
-  // Zeros for the elements of rows without tokens, four to a lane.
-  const int64_t e0 = (a.row0 + lo) * a.dim;
-  const int64_t b0 = e0 > a.first ? e0 : a.first;
-  const int64_t e1 = (a.row0 + lo + span) * a.dim;
-  const int64_t b1 = e1 < a.last ? e1 : a.last;
-  const int64_t lead = (16 - (reinterpret_cast<uintptr_t>(a.main_grad + b0) & 15)) / 4 % 4;
-  for (int64_t e = b0 - (4 - lead) % 4 + 4 * tid; e < b1; e += 4 * blockDim.x) {
-    const int64_t f = e < b0 ? b0 : e, l = e + 4 < b1 ? e + 4 : b1;
-    const uint32_t rf = static_cast<uint64_t>(f - e0) / a.dim;
-    const uint32_t rl = static_cast<uint64_t>(l - 1 - e0) / a.dim;
-    if (rf == rl && l - f == 4) {
-      if (empty[rf]) *as_global<f32x4_a4>(a.main_grad + f) = f32x4{0, 0, 0, 0};
-    } else {
-      for (int64_t x = f; x < l; ++x)
-        if (empty[static_cast<uint64_t>(x - e0) / a.dim]) a.main_grad[x] = 0.0f;
-    }
+  // Zeros to the rows without tokens, a wave to a row.
+  for (int r = w; r < span; r += kSortWaves) {
+    if (!empty[r]) continue;
+    const int64_t e = (a.row0 + lo + r) * a.dim;
+    const int64_t f = e > a.first ? e : a.first, l = e + a.dim < a.last ? e + a.dim : a.last;
+    float* p = a.main_grad + f;
+    const int n = static_cast<int>(l - f);
+    const int lead = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 4) & 3);   // to 16 bytes
+    if (lane < lead && lane < n) p[lane] = 0.0f;
+    int c = lead + 4 * lane;
+    for (; c + 4 <= n; c += 256) *as_global<f32x4>(p + c) = f32x4{0, 0, 0, 0};
+    for (; c < n; ++c) p[c] = 0.0f;
   }
 }
 
@@ -225,8 +244,8 @@ struct SumArgs {
   const void* dy;
   EmbedWork w;
   float* main_grad;            // where the table's element 0 lies
-  int64_t dy_stride, dim, row0, first, last;
-  int32_t piece, cols;         // positions per piece; columns of a partial sum
+  int64_t dy_stride, row0, first, last;
+  int32_t dim, piece, cols;    // positions per piece; columns of a partial sum
   float scale;
 };
 
@@ -245,73 +264,106 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, 
   }
 }
 
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const T* p, int left);
-template <>
-__device__ __forceinline__ f32x4 load4(const uint16_t* p, int left) {
-  if (left >= 4) {
-    const u32x2 w = *as_global<u32x2_a2>(p);
-    return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
-  }
-  f32x4 x{0, 0, 0, 0};
-  for (int j = 0; j < left; ++j) x[j] = bf16_lo(p[j]);
+// Four columns of a row of dY, `left` of them there.
+__device__ __forceinline__ u32x2 load4(const uint16_t* p, int left) {
+  if (left >= 4) return *as_global<u32x2_a2>(p);
+  u32x2 x{0, 0};
+  for (int j = 0; j < left; ++j) x[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
   return x;
 }
-template <>
 __device__ __forceinline__ f32x4 load4(const float* p, int left) {
   if (left >= 4) return *as_global<f32x4_a4>(p);
   f32x4 x{0, 0, 0, 0};
   for (int j = 0; j < left; ++j) x[j] = p[j];
   return x;
 }
+__device__ __forceinline__ f32x4 widen4(u32x2 w) {
+  return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
+}
+__device__ __forceinline__ f32x4 widen4(f32x4 x) { return x; }
 
-constexpr int kSumVecs = 4;                     // column groups of four per lane
-constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of one wave
+constexpr int kSumVecs = 2;                     // groups of four columns of a lane
+constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of a wave
+constexpr int kSumRows = 8;                     // rows of dY in flight
 
+// One wave sums one piece of the sorted positions over kSumCols columns.  The
+// rows of dY of eight positions, and the rows of main_grad that the runs among
+// them end in, are all asked for before any of them is used: the loads'
+// latency, not their bytes, is what a row-by-row walk waits for.
 template <typename T, bool kFirst>
 __global__ __launch_bounds__(64) void embed_sum_kernel(const SumArgs a) {
+  using Vec = decltype(load4(static_cast<const T*>(nullptr), 4));
   const int lane = threadIdx.x;
   const int count = *a.w.count;
   const int p0 = blockIdx.x * a.piece;
   if (p0 >= count) return;
   const int p1 = p0 + a.piece < count ? p0 + a.piece : count;
   const int c0 = blockIdx.y * kSumCols + 4 * lane;
-  int row = a.w.row[p0];
-  bool head = p0 > 0 && a.w.row[p0 - 1] == row;   // the run began in an earlier piece
+  bool head = p0 > 0 && a.w.row[p0 - 1] == a.w.row[p0];   // the run began in an earlier piece
   f32x4 s[kSumVecs] = {};
-  for (int p = p0; p < p1; ++p) {
-    const int r = a.w.row[p];
-    if (r != row) {
+  for (int p = p0; p < p1; p += kSumRows) {
+    int row[kSumRows + 1];
+    Vec x[kSumRows][kSumVecs];
+    f32x4 old[kSumRows][kSumVecs];
+    bool ends[kSumRows], quick[kSumRows];
+#pragma unroll
+    for (int k = 0; k <= kSumRows; ++k) row[k] = p + k < count ? a.w.row[p + k] : -1;
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k) {
+      // behind the piece the last row is asked for again, unused
+      const int pos = a.w.pos[p + k < p1 ? p + k : p1 - 1];
+      const T* src = static_cast<const T*>(a.dy) + static_cast<int64_t>(pos) * a.dy_stride;
+#pragma unroll
+      for (int u = 0; u < kSumVecs; ++u) {
+        const int c = c0 + 256 * u;
+        x[k][u] = Vec{};
+        if (c < a.dim) x[k][u] = load4(src + c, a.dim - c);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k) {
+      // a run that ends here, and its row if that lies in the window whole
+      ends[k] = p + k < p1 && row[k] != row[k + 1];
+      const int64_t e = (a.row0 + row[k]) * a.dim;
+      quick[k] = ends[k] && e >= a.first && e + a.dim <= a.last;
+      if (!kFirst && quick[k]) {
+#pragma unroll
+        for (int u = 0; u < kSumVecs; ++u) {
+          const int c = c0 + 256 * u;
+          if (c + 4 <= a.dim) old[k][u] = *as_global<f32x4_a4>(a.main_grad + e + c);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kSumRows; ++k) {
+      if (p + k >= p1) break;
+#pragma unroll
+      for (int u = 0; u < kSumVecs; ++u) s[u] += widen4(x[k][u]);
+      if (!ends[k]) continue;
 #pragma unroll
       for (int u = 0; u < kSumVecs; ++u) {
         const int c = c0 + 256 * u;
         if (c < a.dim) {
           if (head)
             *as_global<f32x4>(a.w.partial + int64_t(blockIdx.x) * 2 * a.cols + c) = s[u];
+          else if (quick[k] && c + 4 <= a.dim)
+            *as_global<f32x4_a4>(a.main_grad + (a.row0 + row[k]) * a.dim + c) =
+                (kFirst ? f32x4{0, 0, 0, 0} : old[k][u]) + s[u] * a.scale;
           else
-            put_row<kFirst>(a, row, c, s[u]);
+            put_row<kFirst>(a, row[k], c, s[u]);
         }
         s[u] = f32x4{0, 0, 0, 0};
       }
-      row = r;
       head = false;
     }
-    const T* src = static_cast<const T*>(a.dy) + static_cast<int64_t>(a.w.pos[p]) * a.dy_stride;
-#pragma unroll
-    for (int u = 0; u < kSumVecs; ++u) {
-      const int c = c0 + 256 * u;
-      if (c < a.dim) s[u] += load4<T>(src + c, static_cast<int>(a.dim) - c);
-    }
   }
-  const bool on = p1 < count && a.w.row[p1] == row;   // the run goes on
+  if (p1 == count || a.w.row[p1] != a.w.row[p1 - 1]) return;
+  // The last run goes on behind the piece.
 #pragma unroll
   for (int u = 0; u < kSumVecs; ++u) {
     const int c = c0 + 256 * u;
-    if (c >= a.dim) continue;
-    if (head || on)
+    if (c < a.dim)
       *as_global<f32x4>(a.w.partial + (int64_t(blockIdx.x) * 2 + (head ? 0 : 1)) * a.cols + c) = s[u];
-    else
-      put_row<kFirst>(a, row, c, s[u]);
   }
 }
 
@@ -429,13 +481,14 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     sa.w = w;
     sa.n = n;
     sa.row0 = clip.first / dim;
-    sa.rows = ceil_div(clip.last, dim) - sa.row0;
-    sa.span = static_cast<int32_t>(std::min<int64_t>(kSortRows, ceil_div(sa.rows, 256)));
+    const int64_t rows = ceil_div(clip.last, dim) - sa.row0;
+    if (rows >= (int64_t(1) << 30)) return fail(ZR_ERR_UNSUPPORTED, "2^30 rows or more in the window");
+    sa.rows = static_cast<int32_t>(rows);
+    sa.span = static_cast<int32_t>(std::min<int64_t>(kSortRows, ceil_div(rows, 256)));
     sa.main_grad = first ? table : nullptr;
     sa.dim = dim;
     sa.first = clip.first;
     sa.last = clip.last;
-    if (ceil_div(sa.rows, sa.span) > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "too many rows");
     embed_sort_kernel<<<ceil_div(sa.rows, sa.span), 64 * kSortWaves, 0, stream>>>(sa);
     st = launched("embedding sort launch");
     if (st != ZR_OK || n == 0) return st;
@@ -444,7 +497,7 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     a.w = w;
     a.main_grad = table;
     a.dy_stride = dy_stride;
-    a.dim = dim;
+    a.dim = static_cast<int32_t>(dim);
     a.row0 = sa.row0;
     a.first = clip.first;
     a.last = clip.last;
