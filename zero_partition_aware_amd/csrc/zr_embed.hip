@@ -104,7 +104,7 @@ __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupA
 // main_grad[row] (+)= scale * sum of dY over the tokens with that row's id.
 // 1. sort: the positions of the tokens whose row meets the window, by row and
 //    in their own order within a row;
-// 2. sum: pieces of kPiece sorted positions, each summed by waves of its own
+// 2. sum: pieces of 8 to 64 sorted positions, each summed by waves of its own
 //    in that order.  A row whose tokens lie in one piece is added to
 //    main_grad at once; one that spans pieces leaves a partial sum per piece;
 // 3. join: the partial sums of such a row, added in the order of the pieces.
@@ -136,7 +136,9 @@ struct SortArgs {
 // kGroup times 64 ids of a wave's share at once, as rows relative to the
 // window's first; -1 for an id without a row in the window.
 constexpr int kGroup = 8;
-__device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t end, int32_t (&r)[kGroup]) {
+constexpr int kKept = 4;   // groups that a wave keeps from its count to its placing
+using Rows = int32_t[kGroup];
+__device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t end, Rows& r) {
   int64_t t[kGroup];
 #pragma unroll
   for (int g = 0; g < kGroup; ++g)
@@ -144,15 +146,42 @@ __device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t 
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) r[g] = t[g] >= 0 && t[g] < a.rows ? static_cast<int32_t>(t[g]) : -1;
 }
+__device__ __forceinline__ void count_rows(const Rows& r, int lo, int span, int32_t* place, int* before) {
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) {
+    if (r[g] >= 0 && r[g] < lo) ++*before;
+    if (r[g] >= lo && r[g] < lo + span) atomicAdd(&place[r[g] - lo], 1);
+  }
+}
+// Lanes of one row find each other by a ballot on each bit of the row: a row
+// that fills the wave costs no more than 64 different ones.
+__device__ __forceinline__ void place_rows(const EmbedWork& w, const Rows& r, int64_t i, int lo, int span,
+                                           int bits, int lane, int32_t* place) {
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) {
+    const int row = r[g] - lo;
+    const bool mine = r[g] >= lo && row < span;
+    uint64_t same = __ballot(mine);
+    if (same == 0) continue;
+    for (int b = 0; b < bits; ++b) {
+      const int64_t one = -static_cast<int64_t>((row >> b) & 1);
+      same &= ~(__ballot(one) ^ one);
+    }
+    if (mine) {
+      const int p = place[row], rank = __popcll(same & ((1ull << lane) - 1));
+      w.pos[p + rank] = static_cast<int32_t>(i + 64 * g);
+      w.row[p + rank] = r[g];
+      if ((same >> lane) == 1) place[row] = p + rank + 1;   // the row's last lane
+    }
+  }
+}
 
 // Workgroup g sorts the tokens of rows [g*span, (g+1)*span): it counts, over
 // the whole batch, the tokens of earlier rows (its first place in the order)
 // and those of each row of its own, by wave; then every wave places its share
 // of the batch, in order, behind what earlier rows and earlier waves have.
-// Every workgroup reads all ids twice (from L2), so that one launch sorts and
-// nothing waits for another workgroup.  Lanes of one row find each other by a
-// ballot on each bit of the row: a row that fills the wave costs no more than
-// 64 different ones.
+// Every workgroup reads all ids (from L2), so that one launch sorts and nothing
+// waits for another workgroup.
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortArgs a) {
   __shared__ int32_t place[kSortWaves][kSortRows];
   __shared__ int32_t wave_sum[kSortWaves];
@@ -166,15 +195,17 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
   __syncthreads();
   const int64_t share = (a.n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
   const int64_t i0 = w * share, i1 = i0 + share < a.n ? i0 + share : a.n;
+  constexpr int kStep = 64 * kGroup;
   int before = 0;
-  for (int64_t i = i0; i < i1; i += 64 * kGroup) {
-    int32_t r[kGroup];
-    load_rows(a, i + lane, i1, r);
+  Rows kept[kKept];
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      if (r[g] >= 0 && r[g] < lo) ++before;
-      if (r[g] >= lo && r[g] < lo + span) atomicAdd(&place[w][r[g] - lo], 1);
-    }
+  for (int k = 0; k < kKept; ++k) load_rows(a, i0 + lane + k * kStep, i1, kept[k]);
+#pragma unroll
+  for (int k = 0; k < kKept; ++k) count_rows(kept[k], lo, span, place[w], &before);
+  for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
+    Rows r;
+    load_rows(a, i + lane, i1, r);
+    count_rows(r, lo, span, place[w], &before);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
@@ -202,27 +233,13 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
   }
   __syncthreads();
   const int bits = 32 - __builtin_clz(a.span);
-  for (int64_t i = i0; i < i1; i += 64 * kGroup) {
-    int32_t r[kGroup];
-    load_rows(a, i + lane, i1, r);
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      const int row = r[g] - lo;
-      const bool mine = r[g] >= lo && row < span;
-      uint64_t same = __ballot(mine);
-      if (same == 0) continue;
-      for (int b = 0; b < bits; ++b) {
-        const bool one = (row >> b) & 1;
-        const uint64_t ones = __ballot(one);
-        same &= one ? ones : ~ones;
-      }
-      if (mine) {
-        const int p = place[w][row], rank = __popcll(same & ((1ull << lane) - 1));
-        a.w.pos[p + rank] = static_cast<int32_t>(i + 64 * g + lane);
-        a.w.row[p + rank] = r[g];
-        if ((same >> lane) == 1) place[w][row] = p + rank + 1;   // the row's last lane
-      }
-    }
+  for (int k = 0; k < kKept; ++k)
+    place_rows(a.w, kept[k], i0 + lane + k * kStep, lo, span, bits, lane, place[w]);
+  for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
+    Rows r;
+    load_rows(a, i + lane, i1, r);
+    place_rows(a.w, r, i + lane, lo, span, bits, lane, place[w]);
   }
   if (!a.main_grad) return;
   // Zeros to the rows without tokens, a wave to a row.
@@ -266,13 +283,13 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, 
 
 // Four columns of a row of dY, `left` of them there.
 __device__ __forceinline__ u32x2 load4(const uint16_t* p, int left) {
-  if (left >= 4) return *as_global<u32x2_a2>(p);
+  if (left >= 4) return __builtin_nontemporal_load(as_global<u32x2_a2>(p));
   u32x2 x{0, 0};
   for (int j = 0; j < left; ++j) x[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
   return x;
 }
 __device__ __forceinline__ f32x4 load4(const float* p, int left) {
-  if (left >= 4) return *as_global<f32x4_a4>(p);
+  if (left >= 4) return __builtin_nontemporal_load(as_global<f32x4_a4>(p));
   f32x4 x{0, 0, 0, 0};
   for (int j = 0; j < left; ++j) x[j] = p[j];
   return x;
@@ -284,80 +301,110 @@ __device__ __forceinline__ f32x4 widen4(f32x4 x) { return x; }
 
 constexpr int kSumVecs = 2;                     // groups of four columns of a lane
 constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of a wave
-constexpr int kSumRows = 8;                     // rows of dY in flight
+constexpr int kSumRows = 4;                     // positions of a batch
 
-// One wave sums one piece of the sorted positions over kSumCols columns.  The
-// rows of dY of eight positions, and the rows of main_grad that the runs among
-// them end in, are all asked for before any of them is used: the loads'
-// latency, not their bytes, is what a row-by-row walk waits for.
+// The rows of dY of kSumRows positions, and the rows of main_grad that runs
+// end in among them.
 template <typename T, bool kFirst>
-__global__ __launch_bounds__(64) void embed_sum_kernel(const SumArgs a) {
+struct Batch {
   using Vec = decltype(load4(static_cast<const T*>(nullptr), 4));
-  const int lane = threadIdx.x;
-  const int count = *a.w.count;
+  Vec x[kSumRows][kSumVecs];
+  f32x4 old[kFirst ? 1 : kSumRows][kSumVecs];
+};
+
+// One wave sums one piece (at most 64) of the sorted positions over kSumCols
+// columns.  Its lanes hold the piece's positions and rows; two batches of
+// rows are on their way at any time, main_grad's among them.
+//
+// What bounds it: HBM, with rows of dY in no order.  Rows of dY are read past
+// the caches (they are used once, and main_grad's lines would give way to
+// them), and the waves of a workgroup take neighbouring columns of the same
+// rows.  Measured, 32768 tokens of 4096 bf16 columns, 27000 of them in a
+// window of 16032 rows, sort and join included: 127 us in the _first form, 158
+// with ordinary loads; 138 us added, 142.
+constexpr int kSumWaves = 8;
+template <typename T, bool kFirst>
+__global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs a) {
+  const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
   const int p0 = blockIdx.x * a.piece;
+  const int at = p0 + lane;
+  const int count = *a.w.count;
   if (p0 >= count) return;
-  const int p1 = p0 + a.piece < count ? p0 + a.piece : count;
-  const int c0 = blockIdx.y * kSumCols + 4 * lane;
-  bool head = p0 > 0 && a.w.row[p0 - 1] == a.w.row[p0];   // the run began in an earlier piece
+  const int n = count - p0 < a.piece ? count - p0 : a.piece;
+  const int my_pos = a.w.pos[at < count ? at : count - 1];
+  const int my_row = a.w.row[at < count ? at : count - 1];
+  const int my_next = at + 1 < count ? a.w.row[at + 1] : -1;
+  const uint64_t ends = __ballot(my_row != my_next);       // positions that end a run
+  // and whose rows lie in the window whole
+  const int64_t my_first = (a.row0 + my_row) * a.dim;
+  const uint64_t quick = __ballot(my_first >= a.first && my_first + a.dim <= a.last);
+  bool head = p0 > 0 && a.w.row[p0 - 1] == __builtin_amdgcn_readfirstlane(my_row);   // began earlier
+  const int c0 = (blockIdx.y * (blockDim.x >> 6) + w) * kSumCols + 4 * lane;
   f32x4 s[kSumVecs] = {};
-  for (int p = p0; p < p1; p += kSumRows) {
-    int row[kSumRows + 1];
-    Vec x[kSumRows][kSumVecs];
-    f32x4 old[kSumRows][kSumVecs];
-    bool ends[kSumRows], quick[kSumRows];
-#pragma unroll
-    for (int k = 0; k <= kSumRows; ++k) row[k] = p + k < count ? a.w.row[p + k] : -1;
+
+  auto load = [&](Batch<T, kFirst>& b, int p) {
 #pragma unroll
     for (int k = 0; k < kSumRows; ++k) {
       // behind the piece the last row is asked for again, unused
-      const int pos = a.w.pos[p + k < p1 ? p + k : p1 - 1];
-      const T* src = static_cast<const T*>(a.dy) + static_cast<int64_t>(pos) * a.dy_stride;
+      const int i = p + k < n ? p + k : n - 1;
+      const T* src = static_cast<const T*>(a.dy) +
+                     static_cast<int64_t>(__builtin_amdgcn_readlane(my_pos, i)) * a.dy_stride;
 #pragma unroll
       for (int u = 0; u < kSumVecs; ++u) {
         const int c = c0 + 256 * u;
-        x[k][u] = Vec{};
-        if (c < a.dim) x[k][u] = load4(src + c, a.dim - c);
+        b.x[k][u] = {};
+        if (c < a.dim) b.x[k][u] = load4(src + c, a.dim - c);
       }
-    }
+      if constexpr (!kFirst) {
+        if (p + k < n && ((ends & quick) >> i & 1)) {
+          const float* row = a.main_grad + (a.row0 + __builtin_amdgcn_readlane(my_row, i)) * a.dim;
 #pragma unroll
-    for (int k = 0; k < kSumRows; ++k) {
-      // a run that ends here, and its row if that lies in the window whole
-      ends[k] = p + k < p1 && row[k] != row[k + 1];
-      const int64_t e = (a.row0 + row[k]) * a.dim;
-      quick[k] = ends[k] && e >= a.first && e + a.dim <= a.last;
-      if (!kFirst && quick[k]) {
-#pragma unroll
-        for (int u = 0; u < kSumVecs; ++u) {
-          const int c = c0 + 256 * u;
-          if (c + 4 <= a.dim) old[k][u] = *as_global<f32x4_a4>(a.main_grad + e + c);
+          for (int u = 0; u < kSumVecs; ++u) {
+            const int c = c0 + 256 * u;
+            if (c + 4 <= a.dim) b.old[k][u] = *as_global<f32x4_a4>(row + c);
+          }
         }
       }
     }
+  };
+  auto add = [&](const Batch<T, kFirst>& b, int p) {
 #pragma unroll
     for (int k = 0; k < kSumRows; ++k) {
-      if (p + k >= p1) break;
+      const int i = p + k;
+      if (i < n) {
 #pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) s[u] += widen4(x[k][u]);
-      if (!ends[k]) continue;
+        for (int u = 0; u < kSumVecs; ++u) s[u] += widen4(b.x[k][u]);
+        if (ends >> i & 1) {
+          const int row = __builtin_amdgcn_readlane(my_row, i);
+          const bool whole = quick >> i & 1;
 #pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) {
-        const int c = c0 + 256 * u;
-        if (c < a.dim) {
-          if (head)
-            *as_global<f32x4>(a.w.partial + int64_t(blockIdx.x) * 2 * a.cols + c) = s[u];
-          else if (quick[k] && c + 4 <= a.dim)
-            *as_global<f32x4_a4>(a.main_grad + (a.row0 + row[k]) * a.dim + c) =
-                (kFirst ? f32x4{0, 0, 0, 0} : old[k][u]) + s[u] * a.scale;
-          else
-            put_row<kFirst>(a, row[k], c, s[u]);
+          for (int u = 0; u < kSumVecs; ++u) {
+            const int c = c0 + 256 * u;
+            if (c < a.dim) {
+              if (head)
+                *as_global<f32x4>(a.w.partial + int64_t(blockIdx.x) * 2 * a.cols + c) = s[u];
+              else if (whole && c + 4 <= a.dim)
+                *as_global<f32x4_a4>(a.main_grad + (a.row0 + row) * a.dim + c) =
+                    (kFirst ? f32x4{0, 0, 0, 0} : b.old[kFirst ? 0 : k][u]) + s[u] * a.scale;
+              else
+                put_row<kFirst>(a, row, c, s[u]);
+            }
+            s[u] = f32x4{0, 0, 0, 0};
+          }
+          head = false;
         }
-        s[u] = f32x4{0, 0, 0, 0};
       }
-      head = false;
     }
+  };
+  Batch<T, kFirst> b0, b1;
+  load(b0, 0);
+  for (int p = 0; p < n; p += 2 * kSumRows) {
+    load(b1, p + kSumRows);
+    add(b0, p);
+    load(b0, p + 2 * kSumRows);
+    add(b1, p + kSumRows);
   }
-  if (p1 == count || a.w.row[p1] != a.w.row[p1 - 1]) return;
+  if (ends >> (n - 1) & 1) return;
   // The last run goes on behind the piece.
 #pragma unroll
   for (int u = 0; u < kSumVecs; ++u) {
@@ -367,45 +414,81 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(const SumArgs a) {
   }
 }
 
-// The rows that span pieces: workgroup (piece, columns) adds up the run that
-// starts in its piece and goes on behind it, if there is one.
+// The rows that span pieces: workgroup (piece, kJoinCols columns) adds up the
+// run that starts in its piece and goes on behind it, if there is one: its
+// waves add an eighth of the pieces each, in their order.  With rows of three
+// tokens on average most pieces end inside a run, so what counts is how few
+// loads wait for each other: the run's pieces are counted 64 at a time.
+constexpr int kJoinVecs = 4, kJoinCols = 256 * kJoinVecs, kJoinWaves = 8;
 template <bool kFirst>
-__global__ __launch_bounds__(256) void embed_join_kernel(const SumArgs a) {
-  __shared__ f32x4 part[4][64];
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(const SumArgs a) {
+  __shared__ f32x4 part[kJoinWaves][kJoinVecs][64];
   const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
-  const int count = *a.w.count;
   const int64_t p0 = static_cast<int64_t>(blockIdx.x) * a.piece, p1 = p0 + a.piece;
-  if (p1 >= count) return;
-  const int row = a.w.row[p1];
-  if (a.w.row[p1 - 1] != row || (p0 > 0 && a.w.row[p0 - 1] == row)) return;
-  // The run's last position, by bisection: rows are sorted.
-  int64_t in = p1, out = count;
-  while (in + 1 < out) {
-    const int64_t mid = (in + out) / 2;
-    if (a.w.row[mid] == row) in = mid; else out = mid;
+  // asked for together, though what lies behind the count is not set
+  const int64_t end = static_cast<int64_t>(gridDim.x) * a.piece;   // the last piece's first position
+  const int64_t there = p1 + lane * a.piece;
+  int first_row = a.w.row[there < end ? there : end];
+  const int count = *a.w.count, row = a.w.row[p1], last = a.w.row[p1 - 1];
+  const int before = a.w.row[p0 > 0 ? p0 - 1 : 0];
+  if (p1 >= count || last != row || (p0 > 0 && before == row)) return;
+  int64_t links = 0;   // pieces that follow
+  for (;;) {
+    const int64_t p = p1 + (links + lane) * a.piece;
+    const uint64_t on = __ballot(p < count && first_row == row);
+    const int more = on == ~0ull ? 64 : __builtin_ctzll(~on);
+    links += more;
+    if (more < 64) break;
+    const int64_t q = p1 + (links + lane) * a.piece;
+    first_row = a.w.row[q < end ? q : end];
   }
-  const int64_t links = in / a.piece - blockIdx.x;   // pieces that follow
-  const int c = blockIdx.y * 256 + 4 * lane;
-  f32x4 s{0, 0, 0, 0};
-  if (c < a.dim) {
-    const int64_t each = (links + 3) / 4;
-    const int64_t j1 = (w + 1) * each < links ? (w + 1) * each : links;
-    const float* head = a.w.partial + (blockIdx.x + 1) * int64_t(2) * a.cols + c;
-    if (w == 0) s = *as_global<f32x4>(a.w.partial + (blockIdx.x * int64_t(2) + 1) * a.cols + c);
-#pragma unroll 8
-    for (int64_t j = w * each; j < j1; ++j) s += *as_global<f32x4>(head + j * 2 * a.cols);
+  const int64_t each = (links + kJoinWaves - 1) / kJoinWaves;
+  const int64_t j1 = (w + 1) * each < links ? (w + 1) * each : links;
+  const int c0 = blockIdx.y * kJoinCols + 4 * lane;
+  const float* first = a.w.partial + (blockIdx.x * int64_t(2) + 1) * a.cols;
+  const float* next = first + a.cols;
+  f32x4 s[kJoinVecs] = {};
+  int64_t c_in[kJoinVecs];   // columns behind the last are read as the first, unused
+#pragma unroll
+  for (int u = 0; u < kJoinVecs; ++u) c_in[u] = c0 + 256 * u < a.dim ? c0 + 256 * u : 0;
+  if (w == 0) {
+#pragma unroll
+    for (int u = 0; u < kJoinVecs; ++u) s[u] = *as_global<f32x4>(first + c_in[u]);
   }
-  part[w][lane] = s;
+  constexpr int kDeep = 4;
+  for (int64_t j = w * each; j < j1; j += kDeep) {
+    f32x4 x[kDeep][kJoinVecs];
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d) {
+      const int64_t link = j + d < j1 ? j + d : j1 - 1;
+#pragma unroll
+      for (int u = 0; u < kJoinVecs; ++u) x[d][u] = *as_global<f32x4>(next + link * 2 * a.cols + c_in[u]);
+    }
+#pragma unroll
+    for (int d = 0; d < kDeep; ++d)
+      if (j + d < j1) {
+#pragma unroll
+        for (int u = 0; u < kJoinVecs; ++u) s[u] += x[d][u];
+      }
+  }
+#pragma unroll
+  for (int u = 0; u < kJoinVecs; ++u) part[w][u][lane] = s[u];
   __syncthreads();
-  if (w == 0 && c < a.dim)
-    put_row<kFirst>(a, row, c, ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane]);
+  const int c = c0 + 256 * w;   // a group of columns for each of the first waves
+  if (w < kJoinVecs && c < a.dim) {
+    f32x4 sum = part[0][w][lane];
+#pragma unroll
+    for (int v = 1; v < kJoinWaves; ++v) sum += part[v][w][lane];
+    put_row<kFirst>(a, row, c, sum);
+  }
 }
+static_assert(kJoinVecs <= kJoinWaves, "a wave for each group of columns");
 
 // Positions per piece: enough pieces to fill the chip, and no more partial
 // sums than that takes.
 int64_t piece_of(int64_t n, int64_t dim) {
   const int64_t waves = ceil_div(dim, kSumCols);
-  int64_t piece = 64;
+  int64_t piece = 64;   // positions that a wave's lanes hold
   while (piece > 8 && ceil_div(n, piece) * waves < 2048) piece /= 2;
   return piece;
 }
@@ -446,7 +529,8 @@ zr_status check_tokens(const void* tokens, zr_index type, int64_t n) {
 
 template <typename T, bool kFirst>
 void launch_sum(const SumArgs& a, int64_t pieces, hipStream_t stream) {
-  embed_sum_kernel<T, kFirst><<<dim3(pieces, ceil_div(a.dim, kSumCols)), 64, 0, stream>>>(a);
+  const int64_t waves = ceil_div(a.dim, kSumCols), here = std::min<int64_t>(waves, kSumWaves);
+  embed_sum_kernel<T, kFirst><<<dim3(pieces, ceil_div(waves, here)), 64 * here, 0, stream>>>(a);
 }
 
 zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const void* tokens,
@@ -513,9 +597,9 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     }
     st = launched("embedding sum launch");
     if (st != ZR_OK || s.pieces == 1) return st;
-    const dim3 grid(s.pieces - 1, ceil_div(dim, 256));
-    if (first) embed_join_kernel<true><<<grid, 256, 0, stream>>>(a);
-    else embed_join_kernel<false><<<grid, 256, 0, stream>>>(a);
+    const dim3 grid(s.pieces - 1, ceil_div(dim, kJoinCols));
+    if (first) embed_join_kernel<true><<<grid, 64 * kJoinWaves, 0, stream>>>(a);
+    else embed_join_kernel<false><<<grid, 64 * kJoinWaves, 0, stream>>>(a);
     return launched("embedding join launch");
   });
 }
