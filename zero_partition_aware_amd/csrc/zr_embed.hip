@@ -75,21 +75,23 @@ __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupA
   if ((k + 1) * a.part <= f) ++k;
   if (!valid || f + len <= (k + 1) * a.part) {
     const T* src = valid ? static_cast<const T*>(a.parts[k]) + (f - k * a.part) : nullptr;
-    u32x4 x[4];
+    if (len >= V) {
+      // The last lane of a row that is no multiple of V takes its last V
+      // columns, some of them twice.
+      u32x4 x[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = (u * 64 + lane) * V;
-      x[u] = u32x4{0, 0, 0, 0};
-      if (valid && c + V <= len) x[u] = *as_global<u32x4_a2>(src + c);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = (u * 64 + lane) * V;
-      if (c + V <= len) {
-        *as_global<u32x4_a2>(out + c) = scaled_vec<T>(x[u], a.scale);
-      } else {
-        for (int e = c; e < len; ++e) out[e] = valid ? scaled<T>(src[e], a.scale) : T(0);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t c = (u * 64 + lane) * V, d = c + V <= len ? c : len - V;
+        x[u] = u32x4{0, 0, 0, 0};
+        if (valid && c < len) x[u] = *as_global<u32x4_a2>(src + d);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t c = (u * 64 + lane) * V, d = c + V <= len ? c : len - V;
+        if (c < len) *as_global<u32x4_a2>(out + d) = scaled_vec<T>(x[u], a.scale);
+      }
+    } else if (lane < len) {
+      out[lane] = valid ? scaled<T>(src[lane], a.scale) : T(0);
     }
     return;
   }
@@ -190,7 +192,7 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int lo = blockIdx.x * a.span;
   const int span = a.rows - lo < a.span ? a.rows - lo : a.span;
-  for (int i = tid; i < kSortWaves * kSortRows; i += blockDim.x) (&place[0][0])[i] = 0;
+  for (int i = lane; i < span; i += 64) place[w][i] = 0;
   if (tid == 0) before_s = 0;
   __syncthreads();
   const int64_t share = (a.n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
@@ -213,7 +215,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
   __syncthreads();
   // One thread a row: its count, then an exclusive scan over the rows.
   int count = 0;
-  for (int v = 0; v < kSortWaves; ++v) count += place[v][tid];
+  if (tid < span)
+    for (int v = 0; v < kSortWaves; ++v) count += place[v][tid];
   int scan = count;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -225,12 +228,13 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
   int at = before_s + scan - count;
   for (int v = 0; v < w; ++v) at += wave_sum[v];
   empty[tid] = count == 0;
-  if (blockIdx.x == gridDim.x - 1 && tid == 64 * kSortWaves - 1) *a.w.count = at + count;
-  for (int v = 0; v < kSortWaves; ++v) {
-    const int c = place[v][tid];
-    place[v][tid] = at;
-    at += c;
-  }
+  if (blockIdx.x == gridDim.x - 1 && tid == 64 * kSortWaves - 1) *a.w.count = at;
+  if (tid < span)
+    for (int v = 0; v < kSortWaves; ++v) {
+      const int c = place[v][tid];
+      place[v][tid] = at;
+      at += c;
+    }
   __syncthreads();
   const int bits = 32 - __builtin_clz(a.span);
 #pragma unroll
@@ -242,18 +246,23 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
     place_rows(a.w, r, i + lane, lo, span, bits, lane, place[w]);
   }
   if (!a.main_grad) return;
-  // Zeros to the rows without tokens, a wave to a row.
-  for (int r = w; r < span; r += kSortWaves) {
-    if (!empty[r]) continue;
-    const int64_t e = (a.row0 + lo + r) * a.dim;
-    const int64_t f = e > a.first ? e : a.first, l = e + a.dim < a.last ? e + a.dim : a.last;
-    float* p = a.main_grad + f;
-    const int n = static_cast<int>(l - f);
-    const int lead = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 4) & 3);   // to 16 bytes
-    if (lane < lead && lane < n) p[lane] = 0.0f;
-    int c = lead + 4 * lane;
-    for (; c + 4 <= n; c += 256) *as_global<f32x4>(p + c) = f32x4{0, 0, 0, 0};
-    for (; c < n; ++c) p[c] = 0.0f;
+  // Zeros to the rows without tokens: each wave takes a sixteenth of the rows,
+  // and neighbouring ones together.
+  for (int r = w * span / kSortWaves, end = (w + 1) * span / kSortWaves; r < end;) {
+    int next = r + 1;
+    if (empty[r]) {
+      while (next < end && empty[next]) ++next;
+      const int64_t e = (a.row0 + lo + r) * a.dim, g = (a.row0 + lo + next) * a.dim;
+      const int64_t f = e > a.first ? e : a.first, l = g < a.last ? g : a.last;
+      float* p = a.main_grad + f;
+      const int64_t n = l - f;
+      const int lead = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 4) & 3);   // to 16 bytes
+      if (lane < lead && lane < n) p[lane] = 0.0f;
+      int64_t c = lead + 4 * lane;
+      for (; c + 4 <= n; c += 256) *as_global<f32x4>(p + c) = f32x4{0, 0, 0, 0};
+      for (; c < n; ++c) p[c] = 0.0f;
+    }
+    r = next;
   }
 }
 
@@ -275,29 +284,47 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, 
     auto* p = as_global<f32x4_a4>(a.main_grad + e);
     *p = (kFirst ? f32x4{0, 0, 0, 0} : f32x4(*p)) + s;
   } else {
+    f32x4 old{0, 0, 0, 0};
+#pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (col + j < a.dim && e + j >= a.first && e + j < a.last)
-        a.main_grad[e + j] = (kFirst ? 0.0f : a.main_grad[e + j]) + s[j];
+      if (!kFirst && col + j < a.dim && e + j >= a.first && e + j < a.last) old[j] = a.main_grad[e + j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col + j < a.dim && e + j >= a.first && e + j < a.last) a.main_grad[e + j] = old[j] + s[j];
   }
 }
 
-// Four columns of a row of dY, `left` of them there.
-__device__ __forceinline__ u32x2 load4(const uint16_t* p, int left) {
-  if (left >= 4) return __builtin_nontemporal_load(as_global<u32x2_a2>(p));
+// Four columns of a row of dY, used once.
+__device__ __forceinline__ u32x2 load4(const uint16_t* p) {
+  return __builtin_nontemporal_load(as_global<u32x2_a2>(p));
+}
+__device__ __forceinline__ f32x4 load4(const float* p) {
+  return __builtin_nontemporal_load(as_global<f32x4_a4>(p));
+}
+__device__ __forceinline__ u32x2 load_some(const uint16_t* p, int n) {
   u32x2 x{0, 0};
-  for (int j = 0; j < left; ++j) x[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < n) x[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
   return x;
 }
-__device__ __forceinline__ f32x4 load4(const float* p, int left) {
-  if (left >= 4) return __builtin_nontemporal_load(as_global<f32x4_a4>(p));
+__device__ __forceinline__ f32x4 load_some(const float* p, int n) {
   f32x4 x{0, 0, 0, 0};
-  for (int j = 0; j < left; ++j) x[j] = p[j];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (j < n) x[j] = p[j];
   return x;
 }
 __device__ __forceinline__ f32x4 widen4(u32x2 w) {
   return f32x4{bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])};
 }
 __device__ __forceinline__ f32x4 widen4(f32x4 x) { return x; }
+// The values from the n-th on, n < 4, moved to the front.
+__device__ __forceinline__ f32x4 from(f32x4 x, int n) {
+  if (n & 1) x = f32x4{x[1], x[2], x[3], x[3]};
+  if (n & 2) x = f32x4{x[2], x[3], x[3], x[3]};
+  return x;
+}
 
 constexpr int kSumVecs = 2;                     // groups of four columns of a lane
 constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of a wave
@@ -307,14 +334,15 @@ constexpr int kSumRows = 4;                     // positions of a batch
 // end in among them.
 template <typename T, bool kFirst>
 struct Batch {
-  using Vec = decltype(load4(static_cast<const T*>(nullptr), 4));
+  using Vec = decltype(load4(static_cast<const T*>(nullptr)));
   Vec x[kSumRows][kSumVecs];
   f32x4 old[kFirst ? 1 : kSumRows][kSumVecs];
 };
 
 // One wave sums one piece (at most 64) of the sorted positions over kSumCols
 // columns.  Its lanes hold the piece's positions and rows; two batches of
-// rows are on their way at any time, main_grad's among them.
+// rows are on their way at any time, main_grad's among them.  A lane that the
+// rows' end cuts reads the last four columns and moves its own to the front.
 //
 // What bounds it: HBM, with rows of dY in no order.  Rows of dY are read past
 // the caches (they are used once, and main_grad's lines would give way to
@@ -323,7 +351,7 @@ struct Batch {
 // window of 16032 rows, sort and join included: 127 us in the _first form, 158
 // with ordinary loads; 138 us added, 142.
 constexpr int kSumWaves = 8;
-template <typename T, bool kFirst>
+template <typename T, bool kFirst, bool kTiny>   // kTiny: rows of fewer than four columns
 __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs a) {
   const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
   const int p0 = blockIdx.x * a.piece;
@@ -340,6 +368,13 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
   const uint64_t quick = __ballot(my_first >= a.first && my_first + a.dim <= a.last);
   bool head = p0 > 0 && a.w.row[p0 - 1] == __builtin_amdgcn_readfirstlane(my_row);   // began earlier
   const int c0 = (blockIdx.y * (blockDim.x >> 6) + w) * kSumCols + 4 * lane;
+  int c_in[kSumVecs];
+#pragma unroll
+  for (int u = 0; u < kSumVecs; ++u) {
+    const int c = c0 + 256 * u;
+    c_in[u] = c + 4 <= a.dim ? c : c < a.dim && !kTiny ? a.dim - 4 : 0;
+  }
+  const bool cut = a.dim & 3;
   f32x4 s[kSumVecs] = {};
 
   auto load = [&](Batch<T, kFirst>& b, int p) {
@@ -350,19 +385,13 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
       const T* src = static_cast<const T*>(a.dy) +
                      static_cast<int64_t>(__builtin_amdgcn_readlane(my_pos, i)) * a.dy_stride;
 #pragma unroll
-      for (int u = 0; u < kSumVecs; ++u) {
-        const int c = c0 + 256 * u;
-        b.x[k][u] = {};
-        if (c < a.dim) b.x[k][u] = load4(src + c, a.dim - c);
-      }
-      if constexpr (!kFirst) {
+      for (int u = 0; u < kSumVecs; ++u)
+        b.x[k][u] = kTiny ? load_some(src, a.dim) : load4(src + c_in[u]);
+      if constexpr (!kFirst && !kTiny) {
         if (p + k < n && ((ends & quick) >> i & 1)) {
           const float* row = a.main_grad + (a.row0 + __builtin_amdgcn_readlane(my_row, i)) * a.dim;
 #pragma unroll
-          for (int u = 0; u < kSumVecs; ++u) {
-            const int c = c0 + 256 * u;
-            if (c + 4 <= a.dim) b.old[k][u] = *as_global<f32x4_a4>(row + c);
-          }
+          for (int u = 0; u < kSumVecs; ++u) b.old[k][u] = *as_global<f32x4_a4>(row + c_in[u]);
         }
       }
     }
@@ -373,21 +402,33 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
       const int i = p + k;
       if (i < n) {
 #pragma unroll
-        for (int u = 0; u < kSumVecs; ++u) s[u] += widen4(b.x[k][u]);
+        for (int u = 0; u < kSumVecs; ++u) {
+          const f32x4 x = widen4(b.x[k][u]);
+          s[u] += cut ? from(x, (c0 + 256 * u - c_in[u]) & 3) : x;
+        }
         if (ends >> i & 1) {
           const int row = __builtin_amdgcn_readlane(my_row, i);
-          const bool whole = quick >> i & 1;
+          const bool whole = !kTiny && (quick >> i & 1);
 #pragma unroll
           for (int u = 0; u < kSumVecs; ++u) {
             const int c = c0 + 256 * u;
             if (c < a.dim) {
-              if (head)
+              if (head) {
                 *as_global<f32x4>(a.w.partial + int64_t(blockIdx.x) * 2 * a.cols + c) = s[u];
-              else if (whole && c + 4 <= a.dim)
-                *as_global<f32x4_a4>(a.main_grad + (a.row0 + row) * a.dim + c) =
-                    (kFirst ? f32x4{0, 0, 0, 0} : b.old[kFirst ? 0 : k][u]) + s[u] * a.scale;
-              else
+              } else if (whole) {
+                float* p = a.main_grad + (a.row0 + row) * a.dim + c;
+                const f32x4 o = kFirst ? f32x4{0, 0, 0, 0} : b.old[kFirst ? 0 : k][u];
+                const f32x4 v = (cut ? from(o, (c - c_in[u]) & 3) : o) + s[u] * a.scale;
+                if (c + 4 <= a.dim) {
+                  *as_global<f32x4_a4>(p) = v;
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 3; ++j)
+                    if (c + j < a.dim) p[j] = v[j];
+                }
+              } else {
                 put_row<kFirst>(a, row, c, s[u]);
+              }
             }
             s[u] = f32x4{0, 0, 0, 0};
           }
@@ -530,7 +571,9 @@ zr_status check_tokens(const void* tokens, zr_index type, int64_t n) {
 template <typename T, bool kFirst>
 void launch_sum(const SumArgs& a, int64_t pieces, hipStream_t stream) {
   const int64_t waves = ceil_div(a.dim, kSumCols), here = std::min<int64_t>(waves, kSumWaves);
-  embed_sum_kernel<T, kFirst><<<dim3(pieces, ceil_div(waves, here)), 64 * here, 0, stream>>>(a);
+  const dim3 grid(pieces, ceil_div(waves, here));
+  if (a.dim < 4) embed_sum_kernel<T, kFirst, true><<<grid, 64 * here, 0, stream>>>(a);
+  else embed_sum_kernel<T, kFirst, false><<<grid, 64 * here, 0, stream>>>(a);
 }
 
 zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const void* tokens,
