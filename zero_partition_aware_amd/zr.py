@@ -719,51 +719,74 @@ def zr_all_gather_params(plan, group, parts, out, out_base=0, out_len=None,
 
 # -------------------------------------------------------- layer operators
 
-def _rows(t, name, shape, dtypes):
-    """Checks one matrix of contiguous rows and returns (address, stride):
-    rows x columns as ``shape`` says (None: any), of one of the torch dtypes,
-    on the current device.  Rows may lie apart (a slice of wider rows); a
-    strided or broadcast column axis is refused."""
+# Checks of these calls' tensors.  Each is one condition that holds in every
+# good call; what is wrong is only worked out, and named, when it fails.
+
+_FLOATS = None if torch is None else (torch.bfloat16, torch.float32)
+
+
+def _device():
+    """The current device; before torch has used one there is no device tensor
+    to compare it with (-2: not the -1 of host tensors)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+
+
+def _refuse_device(t, name, dev):
+    if not t.is_cuda:
+        raise ZrError(ZR_ERR_INVALID, f"{name} must be a device tensor")
+    raise ZrError(ZR_ERR_INVALID, f"{name} is on device {t.get_device()}, not on the current one "
+                                  f"({dev})")
+
+
+def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS):
+    """Checks one matrix of contiguous rows (``rows`` x ``cols``, None: any) of
+    one of the torch dtypes on the device ``dev`` and returns (address,
+    stride).  Rows may lie apart (a slice of wider rows); a strided or
+    broadcast column axis is refused."""
     if t.dtype not in dtypes:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 2 or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; the call needs "
-                                      f"{tuple('any' if w is None else w for w in shape)}")
-    _on_device(t, name)
-    rows, cols = t.shape
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and
+                                                                      shape[1] != cols):
+        raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(shape)}; the call needs "
+                                      f"({'any' if rows is None else rows}, "
+                                      f"{'any' if cols is None else cols})")
+    if t.get_device() != dev:
+        _refuse_device(t, name, dev)
     stride, step = t.stride()
-    if rows < 2:
-        stride = max(stride, cols)
-    if (step != 1 and cols > 1) or stride < cols:
+    if shape[0] < 2 and stride < shape[1]:
+        stride = shape[1]
+    if (step != 1 and shape[1] > 1) or stride < shape[1]:
         raise ZrError(ZR_ERR_INVALID, f"{name} must have contiguous rows")
     return t.data_ptr(), stride
 
 
-def _on_device(t, name):
-    if not t.is_cuda:
-        raise ZrError(ZR_ERR_INVALID, f"{name} must be a device tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ZrError(ZR_ERR_INVALID, f"{name} is on device {t.get_device()}, not on the current "
-                                      f"one ({torch.cuda.current_device()})")
-
-
-def _dense(t, name, dtype, min_numel=0):
-    """Address of a contiguous tensor of the current device."""
+def _dense(t, name, dev, dtype, min_numel=0):
+    """Address of a contiguous tensor of the device ``dev``."""
+    if (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and
+            t.numel() >= min_numel):
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be {dtype}, not {t.dtype}")
     if not t.is_contiguous():
         raise ZrError(ZR_ERR_INVALID, f"{name} must be contiguous")
-    _on_device(t, name)
-    if t.numel() < min_numel:
-        raise ZrError(ZR_ERR_INVALID,
-                      f"{name} holds {t.numel()} elements; the call touches {min_numel}")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        _refuse_device(t, name, dev)
+    raise ZrError(ZR_ERR_INVALID,
+                  f"{name} holds {t.numel()} elements; the call touches {min_numel}")
 
 
-def _token_ids(tokens):
+def _stream_of(stream, dev):
+    """The raw handle of ``stream`` or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _token_ids(tokens, dev):
     if tokens.dtype is torch.int64:
-        return _dense(tokens, "tokens", torch.int64), ZR_I64
-    return _dense(tokens, "tokens", torch.int32), ZR_I32
+        return _dense(tokens, "tokens", dev, torch.int64), ZR_I64
+    return _dense(tokens, "tokens", dev, torch.int32), ZR_I32
 
 
 def zr_embedding_lookup(plan, param, dim, parts, tokens, out, scale=1.0, stream=None):
@@ -771,17 +794,19 @@ def zr_embedding_lookup(plan, param, dim, parts, tokens, out, scale=1.0, stream=
     read from the R_g partition tensors ``parts`` (bf16 or fp32, those that
     hold none of the table may be None); ids outside [0, vocab) give zeros.
     tokens: int64 or int32, any shape; out: [tokens.numel(), dim]."""
-    ids, wide = _token_ids(tokens)
-    n, d = tokens.numel(), _i64(dim, "dim")
-    ptr, stride = _rows(out, "out", (n, d), (torch.bfloat16, torch.float32))
-    p = _i64(param, "param")
+    dev = _device()
+    ids, wide = _token_ids(tokens, dev)
+    n, d, p = tokens.numel(), _i64(dim, "dim"), _i64(param, "param")
+    ptr, stride = _rows(out, "out", dev, n, d)
     group = plan.param_groups[p] if 0 <= p < len(plan.param_groups) else 0
     _expect_len(parts, _world(plan, group), "parts")
-    P = _part_numel(plan, group)
-    arr = (c_vp * len(parts))(*[None if t is None else _dense(t, f"parts[{k}]", out.dtype, P)
-                                for k, t in enumerate(parts)])
+    P, dtype = _part_numel(plan, group), out.dtype
+    arr = (c_vp * len(parts))()
+    for k, t in enumerate(parts):
+        if t is not None:
+            arr[k] = _dense(t, "a partition", dev, dtype, P)
     _check(_lib.zr_embedding_lookup(plan.handle, p, d, arr, _dtype_code(out), ids, wide, n,
-                                    scale, ptr, stride, _stream(stream)))
+                                    scale, ptr, stride, _stream_of(stream, dev)))
 
 
 def zr_ipg_embedding_workspace(plan, param, dim, n, window_base, window_len):
@@ -813,14 +838,16 @@ def zr_ipg_accumulate_embedding_first(plan, param, dim, tokens, dy, main_grad, w
 
 def _embedding(fn, plan, param, dim, tokens, dy, main_grad, workspace, window_base, window_len,
                scale, stream):
-    ids, wide = _token_ids(tokens)
+    dev = _device()
+    ids, wide = _token_ids(tokens, dev)
     n, d = tokens.numel(), _i64(dim, "dim")
-    ptr, stride = _rows(dy, "dy", (n, d), (torch.bfloat16, torch.float32))
+    ptr, stride = _rows(dy, "dy", dev, n, d)
     wl = main_grad.numel() if window_len is None else _i64(window_len, "window_len")
     _check(fn(plan.handle, _i64(param, "param"), d, ids, wide, n, scale, ptr, _dtype_code(dy),
-              stride, _dense(main_grad, "main_grad", torch.float32, wl),
-              _i64(window_base, "window_base"), wl, _dense(workspace, "workspace", torch.uint8),
-              workspace.numel(), _stream(stream)))
+              stride, _dense(main_grad, "main_grad", dev, torch.float32, wl),
+              _i64(window_base, "window_base"), wl,
+              _dense(workspace, "workspace", dev, torch.uint8), workspace.numel(),
+              _stream_of(stream, dev)))
 
 
 def zr_act_layout(cols):
@@ -838,54 +865,59 @@ def act_empty(rows, cols, device="cuda"):
             torch.empty((rows, s), dtype=torch.uint8, device=device))
 
 
-def _checkpoint(codes, scales, rows, cols):
+def _checkpoint(codes, scales, dev, rows, cols):
     """Checks a checkpoint's tensors and returns their addresses."""
-    c = -(-cols // 32) * 32
-    for t, name, dtype, want in ((codes, "codes", torch.float8_e4m3fn, (rows, c)),
-                                 (scales, "scales", torch.uint8, (rows, c // 32))):
-        if tuple(t.shape) != want:
-            raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; a checkpoint of "
-                                          f"[{rows}, {cols}] has {want}")
-    return _dense(codes, "codes", torch.float8_e4m3fn), _dense(scales, "scales", torch.uint8)
+    blocks = -(-cols // 32)
+    if codes.shape != (rows, 32 * blocks) or scales.shape != (rows, blocks):
+        raise ZrError(ZR_ERR_INVALID,
+                      f"codes and scales have shapes {tuple(codes.shape)} and "
+                      f"{tuple(scales.shape)}; a checkpoint of [{rows}, {cols}] has "
+                      f"{(rows, 32 * blocks)} and {(rows, blocks)}")
+    return (_dense(codes, "codes", dev, torch.float8_e4m3fn),
+            _dense(scales, "scales", dev, torch.uint8))
 
 
 def zr_act_quantize(x, codes, scales, stream=None):
     """The 8-bit checkpoint of x (bf16 or fp32, [rows, cols]) into the tensors
     of act_empty."""
-    ptr, stride = _rows(x, "x", (None, None), (torch.bfloat16, torch.float32))
+    dev = _device()
+    ptr, stride = _rows(x, "x", dev)
     rows, cols = x.shape
-    c, s = _checkpoint(codes, scales, rows, cols)
-    _check(_lib.zr_act_quantize(ptr, _dtype_code(x), rows, cols, stride, c, s, _stream(stream)))
+    c, s = _checkpoint(codes, scales, dev, rows, cols)
+    _check(_lib.zr_act_quantize(ptr, _dtype_code(x), rows, cols, stride, c, s,
+                                _stream_of(stream, dev)))
 
 
 def zr_act_dequantize(codes, scales, out, stream=None):
     """The activations a checkpoint stands for, into out (bf16 or fp32,
     [rows, cols])."""
-    ptr, stride = _rows(out, "out", (None, None), (torch.bfloat16, torch.float32))
+    dev = _device()
+    ptr, stride = _rows(out, "out", dev)
     rows, cols = out.shape
-    c, s = _checkpoint(codes, scales, rows, cols)
+    c, s = _checkpoint(codes, scales, dev, rows, cols)
     _check(_lib.zr_act_dequantize(c, s, rows, cols, ptr, _dtype_code(out), stride,
-                                  _stream(stream)))
+                                  _stream_of(stream, dev)))
 
 
-def _linear_items(plan, items):
+def _linear_items(plan, items, dev):
     arr = (zr_linear_grad * max(len(items), 1))()
     for k, (param, dy, codes, scales, *in_major) in enumerate(items):
-        p = _i64(param, f"items[{k}].param")
-        ptr, stride = _rows(dy, f"items[{k}].dy", (None, None), (torch.bfloat16,))
+        p = _i64(param, "an item's param")
+        ptr, stride = _rows(dy, "an item's dy", dev, dtypes=(torch.bfloat16,))
         tokens, n_out = dy.shape
         # an out-of-range id is left to the C call's check
         n_in = plan.numels[p] // max(n_out, 1) if 0 <= p < len(plan.numels) else 1
-        c, s = _checkpoint(codes, scales, tokens, max(n_in, 1))
-        arr[k] = zr_linear_grad(p, n_out, n_in, tokens, ptr, stride, c, s,
-                                int(bool(in_major and in_major[0])))
+        c, s = _checkpoint(codes, scales, dev, tokens, max(n_in, 1))
+        arr[k] = (p, n_out, n_in, tokens, ptr, stride, c, s,
+                  1 if in_major and in_major[0] else 0)
     return arr
 
 
 def zr_ipg_linear_workspace(plan, items, window_base, window_len):
     """Bytes of workspace zr_ipg_accumulate_linear needs for these items."""
     v = c_i64()
-    _check(_lib.zr_ipg_linear_workspace(plan.handle, _linear_items(plan, items), len(items),
+    _check(_lib.zr_ipg_linear_workspace(plan.handle, _linear_items(plan, items, _device()),
+                                        len(items),
                                         _i64(window_base, "window_base"),
                                         _i64(window_len, "window_len"), ctypes.byref(v)))
     return v.value
@@ -911,9 +943,11 @@ def zr_ipg_accumulate_linear_first(plan, items, main_grad, workspace, window_bas
 
 
 def _linear(fn, plan, items, main_grad, workspace, window_base, window_len, stream):
+    dev = _device()
     wl = main_grad.numel() if window_len is None else _i64(window_len, "window_len")
-    arr = _linear_items(plan, items)
-    ws = None if workspace is None else _dense(workspace, "workspace", torch.uint8)
+    arr = _linear_items(plan, items, dev)
+    ws = None if workspace is None else _dense(workspace, "workspace", dev, torch.uint8)
     _check(fn(plan.handle, arr, len(items),
-              _dense(main_grad, "main_grad", torch.float32, wl), _i64(window_base, "window_base"),
-              wl, ws, 0 if workspace is None else workspace.numel(), _stream(stream)))
+              _dense(main_grad, "main_grad", dev, torch.float32, wl),
+              _i64(window_base, "window_base"), wl, ws,
+              0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
