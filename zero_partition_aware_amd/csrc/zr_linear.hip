@@ -9,6 +9,7 @@
 // those of bf16 values.  Rows of codes are padded to whole blocks with zeros,
 // so every row of codes starts on 32 bytes whatever cols is.
 
+#include <tuple>
 #include <vector>
 
 #include "zr_layers.h"
@@ -147,21 +148,24 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
 // dW[o, i] = sum over tokens t of dY[t, o] * X^[t, i], added to main_grad.
 // Both operands lie token by token, so the sum runs over their slow axis.  A
 // workgroup of 2 x 4 waves owns 256 x 256 weights, 128 x 64 a wave in the
-// accumulators; tiles of 64 tokens go through registers (X decoded there, once
-// for the workgroup) into one of two LDS buffers, and the transposing LDS read
-// hands each lane of a 32x32x16 MFMA the eight tokens of its column.  The
-// 16-byte units of a staged row are exchanged (xor) by four times the token's
-// number mod 4, so that the four rows that 16 lanes read, and the two blocks
-// that 32 do, lie in different banks: 3.0 cycles a read, 4.0 with half the
-// distance and 8.0 without.  One barrier a tile: while a tile multiplies, the
-// next fragments, the next tile's stores and the loads of the one after it are
-// under way (phase below).
+// accumulators.  Tiles of 64 tokens go into one of two LDS buffers: dY's
+// straight from memory where its rows lie on 16 bytes (through registers
+// otherwise), X's through registers, where it is decoded once for the
+// workgroup.  The transposing LDS read hands each lane of a 32x32x16 MFMA the
+// eight tokens of its column.  The 16-byte units of a staged row are exchanged
+// (xor) by four times the token's number mod 4, so that the four rows that 16
+// lanes read, and the two blocks that 32 do, lie in different banks: 3.0 cycles
+// a read, 4.0 with half the distance and 8.0 without.  One barrier a tile:
+// while a tile multiplies, the next fragments, the next tile's stores and the
+// loads of the one after it are under way (phase below).
 //
-// What bounds it: LDS.  A tile costs 64 kB of stores (13.8 cycles a 1 kB
-// store) and 192 kB of reads a CU, 880 and 1150 cycles against the 2050 of
-// its MFMAs; smaller tiles read and store more for each product.  Measured
-// (4096 x 4096 weights, 8192 tokens): 1234 TFLOP/s; 256 x 128 tiles of four
-// waves, two workgroups a CU, 1042; four waves of 128 x 128 1156.
+// What bounds it: the instructions between the MFMAs.  The MFMAs of a tile
+// take 2050 cycles of a SIMD, the loop about 2900; without the staging of
+// either operand it takes 2400, with dY through registers 3100.  Smaller tiles
+// read and store more for each product.  Measured at 4096 x 4096 weights and
+// 8192 tokens: 1332 TFLOP/s, 1240 with rows that do not lie on 16 bytes; with
+// dY through registers 1207, and of that kind 256 x 128 tiles of four waves,
+// two workgroups a CU, 1042, four waves of 128 x 128 1156.
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using s16x4 = short __attribute__((ext_vector_type(4)));
@@ -186,7 +190,8 @@ struct Item {
   int64_t pitch;               // bytes per row of codes
   int32_t out_tile0, in_tile0; // first tiles that meet the window
   int32_t out_tiles, in_tiles;
-  int32_t in_major;            // weight stored [in][out] rather than [out][in]
+  int16_t in_major;            // weight stored [in][out] rather than [out][in]
+  int16_t direct;              // dY's rows lie on 16 bytes
   // The first `whole` tiles are one workgroup's each; the others' tokens are
   // cut into `pieces`, a workgroup each.
   int32_t whole, pieces;
@@ -202,9 +207,10 @@ struct LinearArgs {
 
 // A tile of kDepth tokens and C columns in LDS: 16-byte units (8 bf16) of a
 // token's row, exchanged by the token's number.
+__device__ __forceinline__ int exchanged(int k, int u) { return u ^ (4 * (k & 3)); }
 template <int C>
 __device__ __forceinline__ int staged(int k, int u) {
-  return k * (C * 2) + ((u ^ (4 * (k & 3))) << 4);
+  return k * (C * 2) + (exchanged(k, u) << 4);
 }
 
 // The eight tokens of one column that a lane of an MFMA takes, from the
@@ -225,9 +231,11 @@ constexpr int kInUnits = kTileIn / 16, kInRows = kThreads / kInUnits;
 constexpr int kInLoads = kDepth / kInRows;
 static_assert(kOutLoads * kOutRows == kDepth && kInLoads * kInRows == kDepth, "staging shape");
 
-struct Staged {
-  u32x4 dy[kOutLoads];
-  u32x4 x[kInLoads];
+struct StagedOut {
+  u32x4 v[kOutLoads];
+};
+struct StagedIn {
+  u32x4 v[kInLoads];
   uint32_t scale[kInLoads];
 };
 
@@ -239,6 +247,7 @@ struct Loader {
   const char* scales;
   int64_t dy_step, x_step, s_step;   // bytes per token
   uint32_t dy_off, x_off, s_off;     // this thread's first unit
+  uint32_t direct_off;               // and that of dY straight into LDS
   int32_t dy_row, x_row, dy_left;    // its rows; dY's columns from its unit on
 
   __device__ __forceinline__ Loader(const Item& it, int64_t o0, int64_t i0, int tid) {
@@ -254,56 +263,69 @@ struct Loader {
     codes = reinterpret_cast<const char*>(it.codes) + i0;
     scales = reinterpret_cast<const char*>(it.scales) + i0 / kBlock;
     dy_off = dy_row * static_cast<uint32_t>(dy_step) + 2 * u;
+    int d = 8 * exchanged(dy_row, tid % kOutUnits);
+    if (o0 + d >= it.out) d = 0;
+    direct_off = dy_row * static_cast<uint32_t>(dy_step) + 2 * d;
     x_off = x_row * static_cast<uint32_t>(x_step) + v;
     s_off = x_row * static_cast<uint32_t>(s_step) + v / kBlock;
     dy_left = static_cast<int>(it.out - o0 < kTileOut ? it.out - o0 : kTileOut) - u;
   }
-  // Loads [j0, j1) of dY and of X for the tokens from t on, all there.  A unit
-  // that the row's end cuts is read whole: it ends in the next row.
+  // The whole tile's tokens from t on, all there.  A unit that the row's end
+  // cuts is read whole: it ends in the next row.
   template <int kJ0, int kJ1>
-  __device__ __forceinline__ void load_dy(Staged& s, int64_t t) const {
+  __device__ __forceinline__ void load_dy(StagedOut& s, int64_t t) const {
     const char* d = dy + t * dy_step;
 #pragma unroll
     for (int j = kJ0; j < kJ1; ++j)
-      s.dy[j] = *as_global<u32x4_a2>(d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step))));
+      s.v[j] = *as_global<u32x4_a2>(d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step))));
   }
-  template <int kJ0, int kJ1>
-  __device__ __forceinline__ void load_x(Staged& s, int64_t t) const {
+  // dY straight into LDS, where a wave's 64 units lie one after the other: the
+  // exchange is made by what each lane reads.  Units on 16 bytes.
+  __device__ __forceinline__ void direct_dy(char* lds, int64_t t, int w) const {
+    const char* d = dy + t * dy_step;
+#pragma unroll
+    for (int j = 0; j < kOutLoads; ++j)
+      __builtin_amdgcn_global_load_lds(
+          (const ZR_GLOBAL_AS void*)(d + (direct_off + j * (kOutRows * static_cast<uint32_t>(dy_step)))),
+          (__attribute__((address_space(3))) void*)(lds + (w * (64 / kOutUnits) + j * kOutRows) * (kTileOut * 2)),
+          16, 0, 0);
+  }
+  __device__ __forceinline__ void load_x(StagedIn& s, int64_t t) const {
     const char* x = codes + t * x_step;
     const char* c = scales + t * s_step;
 #pragma unroll
-    for (int j = kJ0; j < kJ1; ++j) {
-      s.x[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
+    for (int j = 0; j < kInLoads; ++j) {
+      s.v[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
       s.scale[j] = *as_global<uint8_t>(c + (s_off + j * (kInRows * static_cast<uint32_t>(s_step))));
     }
   }
   // The same for `tokens` tokens, fewer than kDepth perhaps, up to the last.
-  __device__ __forceinline__ void load_some(Staged& s, int64_t t, int64_t tokens) const {
+  __device__ __forceinline__ void load_some(StagedOut& o, StagedIn& i, int64_t t, int64_t tokens) const {
     const char* d = dy + t * dy_step;
     const char* x = codes + t * x_step;
     const char* c = scales + t * s_step;
 #pragma unroll
     for (int j = 0; j < kOutLoads; ++j) {
-      s.dy[j] = u32x4{0, 0, 0, 0};
+      o.v[j] = u32x4{0, 0, 0, 0};
       if (dy_row + j * kOutRows < tokens) {
         const char* p = d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step)));
         if (dy_left >= 8) {
-          s.dy[j] = *as_global<u32x4_a2>(p);
+          o.v[j] = *as_global<u32x4_a2>(p);
         } else {
 #pragma unroll
           for (int e = 0; e < 7; ++e)
             if (e < dy_left)
-              s.dy[j][e / 2] |= static_cast<uint32_t>(as_global<uint16_t>(p)[e]) << (16 * (e & 1));
+              o.v[j][e / 2] |= static_cast<uint32_t>(as_global<uint16_t>(p)[e]) << (16 * (e & 1));
         }
       }
     }
 #pragma unroll
     for (int j = 0; j < kInLoads; ++j) {
-      s.x[j] = u32x4{0, 0, 0, 0};
-      s.scale[j] = 127;
+      i.v[j] = u32x4{0, 0, 0, 0};
+      i.scale[j] = 127;
       if (x_row + j * kInRows < tokens) {
-        s.x[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
-        s.scale[j] = *as_global<uint8_t>(c + (s_off + j * (kInRows * static_cast<uint32_t>(s_step))));
+        i.v[j] = *as_global<u32x4>(x + (x_off + j * (kInRows * static_cast<uint32_t>(x_step))));
+        i.scale[j] = *as_global<uint8_t>(c + (s_off + j * (kInRows * static_cast<uint32_t>(s_step))));
       }
     }
   }
@@ -314,31 +336,29 @@ constexpr int kOutBytes = kDepth * kTileOut * 2, kInBytes = kDepth * kTileIn * 2
 constexpr int kStage = kOutBytes + kInBytes;
 
 template <int kJ0, int kJ1>
-__device__ __forceinline__ void store_dy(const Staged& s, char* lds, int tid) {
+__device__ __forceinline__ void store_dy(const StagedOut& s, char* lds, int tid) {
 #pragma unroll
   for (int j = kJ0; j < kJ1; ++j)
     *reinterpret_cast<u32x4*>(lds + staged<kTileOut>(tid / kOutUnits + j * kOutRows, tid % kOutUnits)) =
-        s.dy[j];
+        s.v[j];
 }
-template <int kJ0, int kJ1>
-__device__ __forceinline__ void store_x(const Staged& s, char* lds, int tid) {
-  const int v = tid % kInUnits, half = (tid >> 2) & 1;
+__device__ __forceinline__ void store_x(const StagedIn& s, char* lds, int tid) {
 #pragma unroll
-  for (int j = kJ0; j < kJ1; ++j) {
+  for (int j = 0; j < kInLoads; ++j) {
     const float scale = bits_float(s.scale[j] << 23);
     u32x4 w[2];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       w[e / 2][2 * (e & 1)] = __builtin_bit_cast(
-          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.x[j][e], scale, false));
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.v[j][e], scale, false));
       w[e / 2][2 * (e & 1) + 1] = __builtin_bit_cast(
-          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.x[j][e], scale, true));
+          uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(s.v[j][e], scale, true));
     }
-    // Eight lanes write eight different units of 128 bytes at a time.
-    char* x = lds + kOutBytes;
-    const int k = tid / kInUnits + j * kInRows;
-    *reinterpret_cast<u32x4*>(x + staged<kTileIn>(k, 2 * v + half)) = half ? w[1] : w[0];
-    *reinterpret_cast<u32x4*>(x + staged<kTileIn>(k, 2 * v + 1 - half)) = half ? w[0] : w[1];
+    // Every other unit at a time costs the store two of sixteen cycles; a
+    // choice between the two halves by the lane would cost more.
+    const int k = tid / kInUnits + j * kInRows, u = 2 * (tid % kInUnits);
+    *reinterpret_cast<u32x4*>(lds + staged<kTileIn>(k, u)) = w[0];
+    *reinterpret_cast<u32x4*>(lds + staged<kTileIn>(k, u + 1)) = w[1];
   }
 }
 
@@ -352,7 +372,7 @@ struct Fragments {
   bf16x8 d[kOutBlocks], x[kInBlocks];
 };
 struct Reader {
-  int d[kOutBlocks], x[kInBlocks];   // a lane's places in a staged tile
+  int d[kOutBlocks], x[kInBlocks];   // a lane's places in a staged tile's halves
   __device__ __forceinline__ Reader(int lane, int w) {
     const int g = lane >> 4, q = lane & 15;
     const int k = 8 * (g >> 1) + (q >> 2), c = 16 * (g & 1) + 4 * (q & 3);
@@ -364,14 +384,14 @@ struct Reader {
 #pragma unroll
     for (int b = 0; b < kInBlocks; ++b) {
       const int at = (w % kWavesIn) * (32 * kInBlocks) + 32 * b + c;
-      x[b] = kOutBytes + staged<kTileIn>(k, at / 8) + (at % 8) * 2;
+      x[b] = staged<kTileIn>(k, at / 8) + (at % 8) * 2;
     }
   }
-  __device__ __forceinline__ void read(Fragments& f, const char* lds, int k) const {
+  __device__ __forceinline__ void read(Fragments& f, const char* dy, const char* in, int k) const {
 #pragma unroll
-    for (int b = 0; b < kOutBlocks; ++b) f.d[b] = read_columns<kTileOut>(lds, d[b] + k * (kTileOut * 2));
+    for (int b = 0; b < kOutBlocks; ++b) f.d[b] = read_columns<kTileOut>(dy, d[b] + k * (kTileOut * 2));
 #pragma unroll
-    for (int b = 0; b < kInBlocks; ++b) f.x[b] = read_columns<kTileIn>(lds, x[b] + k * (kTileIn * 2));
+    for (int b = 0; b < kInBlocks; ++b) f.x[b] = read_columns<kTileIn>(in, x[b] + k * (kTileIn * 2));
   }
 };
 
@@ -394,79 +414,125 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// Sixteen tokens of the pipelined loop: the next fragments are read, a third
-// of the next tile is put into LDS and a third of the one after it loaded
-// while these multiply.
-template <bool kInMajor, int kPhase>
-__device__ __forceinline__ void phase(Acc& acc, Fragments (&f)[2], Staged& s, const Loader& in,
-                                      const Reader& reader, char* cur, char* next, int64_t t_load,
-                                      int tid) {
+// What the pipelined loop keeps in registers.
+struct Pipe {
+  StagedOut dy;    // the next tile's, unless dY goes straight into LDS
+  StagedIn x;      // the next tile's
+  Fragments f[2];
+};
+
+// Sixteen tokens of tile n: while they multiply, the next sixteen's fragments
+// are read and a third of tile n + 1 is put into LDS.
+template <bool kInMajor, bool kDirect, int kPhase>
+__device__ __forceinline__ void phase(Acc& acc, Pipe& r, const Loader& in, const Reader& reader,
+                                      const char* cur, char* next_dy, char* next_x, int64_t t1,
+                                      int64_t t2, int tid) {
   constexpr int kPhases = kDepth / 16, kParts = kPhases - 1;
-  static_assert(kPhases == 4, "tile_sums runs four phases");
-  if constexpr (kPhase == kPhases - 1) {
+  static_assert(kPhases == 4, "four phases in step");
+  Fragments& next = r.f[(kPhase + 1) & 1];
+  if constexpr (kPhase == kParts) {
+    if constexpr (kDirect) __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): dY is there
     lds_barrier();
-    reader.read(f[(kPhase + 1) & 1], next, 0);
+    reader.read(next, next_dy, next_x, 0);
+    in.load_x(r.x, t2);
   } else {
-    reader.read(f[(kPhase + 1) & 1], cur, 16 * (kPhase + 1));
-    constexpr int d0 = kOutLoads * kPhase / kParts, d1 = kOutLoads * (kPhase + 1) / kParts;
-    constexpr int x0 = kInLoads * kPhase / kParts, x1 = kInLoads * (kPhase + 1) / kParts;
-    store_dy<d0, d1>(s, next, tid);
-    store_x<x0, x1>(s, next, tid);
-    in.load_dy<d0, d1>(s, t_load);
-    in.load_x<x0, x1>(s, t_load);
+    reader.read(next, cur, cur + kOutBytes, 16 * (kPhase + 1));
+    if constexpr (kDirect) {
+      if constexpr (kPhase == 0) in.direct_dy(next_dy, t1, uniform(tid >> 6));
+    } else {
+      constexpr int d0 = kOutLoads * kPhase / kParts, d1 = kOutLoads * (kPhase + 1) / kParts;
+      store_dy<d0, d1>(r.dy, next_dy, tid);
+      in.load_dy<d0, d1>(r.dy, t2);
+    }
+    // X last: it was asked for after the last barrier
+    if constexpr (kPhase == kParts - 1) store_x(r.x, next_x, tid);
   }
-  multiply<kInMajor>(acc, f[kPhase & 1]);
+  multiply<kInMajor>(acc, r.f[kPhase & 1]);
+  // Three reads behind each of the first MFMAs, and nothing over the phase's
+  // end (measured, 4096 x 4096 weights over 8192 tokens: 208 us; two reads
+  // each 212, one and two in turn 217, the compiler's own order 231).
+  constexpr int kReads = 2 * (kOutBlocks + kInBlocks);
+#pragma unroll
+  for (int i = 0; i < kReads / 3; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // MFMA
+    __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);   // LDS read
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, kOutBlocks * kInBlocks - kReads / 3, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tile n, with the tokens of tiles n + 1 and n + 2 from t1 and t2 on.  The pointers are restricted so that the compiler sees that reads of
+// the current buffer need not wait for what goes into the other.
+template <bool kInMajor, bool kDirect>
+__device__ __forceinline__ void step(Acc& acc, Pipe& r, const Loader& in, const Reader& reader,
+                                     const char* __restrict cur, char* __restrict next_dy,
+                                     char* __restrict next_x, int64_t t1, int64_t t2, int tid) {
+  phase<kInMajor, kDirect, 0>(acc, r, in, reader, cur, next_dy, next_x, t1, t2, tid);
+  phase<kInMajor, kDirect, 1>(acc, r, in, reader, cur, next_dy, next_x, t1, t2, tid);
+  phase<kInMajor, kDirect, 2>(acc, r, in, reader, cur, next_dy, next_x, t1, t2, tid);
+  phase<kInMajor, kDirect, 3>(acc, r, in, reader, cur, next_dy, next_x, t1, t2, tid);
+}
+
+// `steps` whole tiles of tokens from t0 on.
+template <bool kInMajor, bool kDirect>
+__device__ __forceinline__ void whole_tiles(const Loader& in, const Reader& reader, int64_t t0,
+                                            int steps, char* lds, Acc& acc, int tid) {
+  Pipe r;
+  // behind the last tile, the last is loaded and staged again, unused
+  auto tile = [&](int n) { return t0 + static_cast<int64_t>(n < steps ? n : steps - 1) * kDepth; };
+  if constexpr (kDirect) {
+    in.direct_dy(lds, t0, uniform(tid >> 6));
+  } else {
+    in.load_dy<0, kOutLoads>(r.dy, t0);
+    store_dy<0, kOutLoads>(r.dy, lds, tid);
+    in.load_dy<0, kOutLoads>(r.dy, tile(1));
+  }
+  in.load_x(r.x, t0);
+  store_x(r.x, lds + kOutBytes, tid);
+  in.load_x(r.x, tile(1));
+  if constexpr (kDirect) __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+  lds_barrier();
+  reader.read(r.f[0], lds, lds + kOutBytes, 0);
+  int stage = 0;
+#pragma unroll 1
+  for (int n = 0; n < steps; ++n) {
+    const char* cur = lds + stage;
+    stage = kStage - stage;
+    char* next = lds + stage;
+    step<kInMajor, kDirect>(acc, r, in, reader, cur, next, next + kOutBytes, tile(n + 1), tile(n + 2),
+                            tid);
+  }
 }
 
 // The tile's sums over the tokens [t0, t1), added to the MFMAs' accumulators:
 // a block's rows are the weight's stored rows, its columns a row's elements.
-template <bool kInMajor>
+template <bool kInMajor, bool kDirect>
 __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0, int64_t t0,
                                           int64_t t1, char* lds, Acc& acc) {
   const int tid = threadIdx.x;
   const Loader in(it, o0, i0, tid);
   const Reader reader(tid & 63, uniform(tid >> 6));
-  Staged s;
   // Whole tiles of tokens.  The matrix's last row cannot be read past its end,
   // and a row of fewer than eight columns ends behind the next row.
-  int64_t end = it.out % 8 && t1 == it.tokens ? t1 - 1 : t1;
-  const int steps = it.out < 8 ? 0 : static_cast<int>((end - t0) / kDepth);
+  const int64_t end = it.out % 8 && t1 == it.tokens ? t1 - 1 : t1;
+  const int steps = it.out < 8 || end < t0 ? 0 : static_cast<int>((end - t0) / kDepth);
   if (steps > 0) {
-    in.load_dy<0, kOutLoads>(s, t0);
-    in.load_x<0, kInLoads>(s, t0);
-    store_dy<0, kOutLoads>(s, lds, tid);
-    store_x<0, kInLoads>(s, lds, tid);
-    const int64_t last = t0 + static_cast<int64_t>(steps - 1) * kDepth;
-    int64_t t = t0 + kDepth < last ? t0 + kDepth : last;
-    in.load_dy<0, kOutLoads>(s, t);
-    in.load_x<0, kInLoads>(s, t);
-    lds_barrier();
-    Fragments f[2];
-    reader.read(f[0], lds, 0);
-    int stage = 0;
-    for (int n = 0; n < steps; ++n) {
-      char* cur = lds + stage;
-      stage = kStage - stage;
-      char* next = lds + stage;
-      // behind the last tile, the last is loaded and staged again, unused
-      t = t + kDepth < last ? t + kDepth : last;
-      phase<kInMajor, 0>(acc, f, s, in, reader, cur, next, t, tid);
-      phase<kInMajor, 1>(acc, f, s, in, reader, cur, next, t, tid);
-      phase<kInMajor, 2>(acc, f, s, in, reader, cur, next, t, tid);
-      phase<kInMajor, 3>(acc, f, s, in, reader, cur, next, t, tid);
-    }
+    whole_tiles<kInMajor, kDirect>(in, reader, t0, steps, lds, acc, tid);
     t0 += static_cast<int64_t>(steps) * kDepth;
   }
   for (; t0 < t1; t0 += kDepth) {
-    in.load_some(s, t0, t1 - t0);
+    StagedOut dy;
+    StagedIn x;
+    in.load_some(dy, x, t0, t1 - t0);
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0): nothing goes into LDS any more
     lds_barrier();
-    store_dy<0, kOutLoads>(s, lds, tid);
-    store_x<0, kInLoads>(s, lds, tid);
+    store_dy<0, kOutLoads>(dy, lds, tid);
+    store_x(x, lds + kOutBytes, tid);
     lds_barrier();
 #pragma unroll 1
     for (int k = 0; k < kDepth; k += 16) {
       Fragments f;
-      reader.read(f, lds, k);
+      reader.read(f, lds, lds + kOutBytes, k);
       multiply<kInMajor>(acc, f);
     }
   }
@@ -474,6 +540,7 @@ __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0
 
 // A tile's place: its first columns of dY and X.  Bands of eight tiles of dY's
 // columns are walked along X's columns.
+template <bool kInMajor>
 struct Place {
   int64_t o0, i0;
   bool whole;                  // all its weights are there and in the window
@@ -482,9 +549,9 @@ struct Place {
     const int height = it.out_tiles - 8 * band < 8 ? it.out_tiles - 8 * band : 8;
     o0 = static_cast<int64_t>(it.out_tile0 + 8 * band + at % height) * kTileOut;
     i0 = static_cast<int64_t>(it.in_tile0 + at / height) * kTileIn;
-    const int64_t r = it.in_major ? i0 : o0, c = it.in_major ? o0 : i0;
-    const int64_t rows = it.in_major ? it.in : it.out, cols = it.in_major ? it.out : it.in;
-    const int high = it.in_major ? kTileIn : kTileOut, wide = it.in_major ? kTileOut : kTileIn;
+    const int64_t r = kInMajor ? i0 : o0, c = kInMajor ? o0 : i0;
+    const int64_t rows = kInMajor ? it.in : it.out, cols = kInMajor ? it.out : it.in;
+    const int high = kInMajor ? kTileIn : kTileOut, wide = kInMajor ? kTileOut : kTileIn;
     whole = r + high <= rows && c + wide <= cols && r * cols + c >= it.first &&
             (r + high - 1) * cols + c + wide <= it.last;
   }
@@ -492,14 +559,14 @@ struct Place {
 
 // kCount of the sixteen sums that a lane has of block (i, j), from the v0-th
 // on, into main_grad: stored rows 8 * (v / 4) + v % 4, one column a lane.
-template <int kCount, typename V>
-__device__ __forceinline__ void put_sums(const Item& it, const Place& at, bool first, int w,
+template <int kCount, bool kInMajor, typename V>
+__device__ __forceinline__ void put_sums(const Item& it, const Place<kInMajor>& at, bool first, int w,
                                          int lane, int i, int j, int v0, const V& sums) {
   const int64_t o = at.o0 + (w / kWavesIn) * (32 * kOutBlocks) + 32 * i;
   const int64_t c = at.i0 + (w % kWavesIn) * (32 * kInBlocks) + 32 * j;
-  const int64_t cols = it.in_major ? it.out : it.in, rows = it.in_major ? it.in : it.out;
-  const int64_t row = (it.in_major ? c : o) + 4 * (lane >> 5);
-  const int64_t col = (it.in_major ? o : c) + (lane & 31);
+  const int64_t cols = kInMajor ? it.out : it.in, rows = kInMajor ? it.in : it.out;
+  const int64_t row = (kInMajor ? c : o) + 4 * (lane >> 5);
+  const int64_t col = (kInMajor ? o : c) + (lane & 31);
   if (at.whole) {
     float* p = it.grad + row * cols + col;
     float old[kCount] = {};
@@ -521,6 +588,7 @@ __device__ __forceinline__ void put_sums(const Item& it, const Place& at, bool f
   }
 }
 
+template <bool kInMajor, bool kDirect>
 __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a) {
   __shared__ __align__(16) char lds[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
@@ -550,10 +618,9 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a)
     partial = a.partial + static_cast<int64_t>(piece) * (kTileOut * kTileIn);
   }
   const Item& it = a.item[k];
-  const Place at(it, tile);
+  const Place<kInMajor> at(it, tile);
   Acc acc = {};
-  if (it.in_major) tile_sums<true>(it, at.o0, at.i0, t0, t1, lds, acc);
-  else tile_sums<false>(it, at.o0, at.i0, t0, t1, lds, acc);
+  tile_sums<kInMajor, kDirect>(it, at.o0, at.i0, t0, t1, lds, acc);
 #pragma unroll
   for (int i = 0; i < kOutBlocks; ++i)
 #pragma unroll
@@ -572,6 +639,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a)
 // Adds up the pieces of the cut tiles, in their order: a workgroup for each
 // four rows of each block.
 constexpr int kJoins = kOutBlocks * kInBlocks * 4;
+template <bool kInMajor>
 __global__ __launch_bounds__(kThreads) void linear_join_kernel(const LinearArgs a) {
   const int tid = threadIdx.x, cut = blockIdx.x / kJoins, part = blockIdx.x % kJoins;
   int k = 0;
@@ -585,7 +653,7 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(const LinearArgs 
 #pragma unroll 8
   for (int n = 1; n < it.pieces; ++n) sum += *as_global<f32x4>(p + n * step);
   const int block = part / 4;
-  put_sums<4>(it, Place(it, it.whole + tile), a.first, uniform(tid >> 6), tid & 63,
+  put_sums<4>(it, Place<kInMajor>(it, it.whole + tile), a.first, uniform(tid >> 6), tid & 63,
               block / kInBlocks, block % kInBlocks, 4 * (part % 4), sum);
 }
 
@@ -662,6 +730,7 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
     it.in = z.n_in;
     it.pitch = ceil_div(z.n_in, kBlock) * kBlock;
     it.in_major = z.in_major != 0;
+    it.direct = aligned_to(z.dy, 16) && z.dy_stride % 8 == 0;
     // Tiles of the stored rows that meet the window; within a row, all.
     const int64_t row = it.in_major ? it.out : it.in;
     const int64_t high = it.in_major ? kTileIn : kTileOut, wide = it.in_major ? kTileOut : kTileIn;
@@ -673,13 +742,26 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
     it.out_tiles = static_cast<int32_t>(it.in_major ? all : r1 - r0);
     out->push_back(it);
   }
-  // Tiles with most tokens first: the last to start are the shortest.
-  std::stable_sort(out->begin(), out->end(),
-                   [](const Item& a, const Item& b) { return a.tokens > b.tokens; });
+  // One kernel's items together, and tiles with most tokens first: the last to
+  // start are the shortest.
+  std::stable_sort(out->begin(), out->end(), [](const Item& a, const Item& b) {
+    return std::make_tuple(a.in_major, a.direct, b.tokens) <
+           std::make_tuple(b.in_major, b.direct, a.tokens);
+  });
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
     return fail(ZR_ERR_INVALID, "param listed twice in one call");
   return ZR_OK;
+}
+
+// The items that one launch takes from the k-th on: of one kernel, and at most
+// kMaxItems.
+size_t launch_end(const std::vector<Item>& items, size_t k) {
+  size_t e = k + 1;
+  while (e < items.size() && e < k + kMaxItems && items[e].in_major == items[k].in_major &&
+         items[e].direct == items[k].direct)
+    ++e;
+  return e;
 }
 
 // The launch of up to kMaxItems items: which tiles are one workgroup's, and
@@ -739,11 +821,12 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
     std::vector<Item> todo;
     zr_status st = linear_items(plan, items, n, main_grad, window_base, window_len, first, &todo);
     if (st != ZR_OK) return st;
-    std::vector<Launch> launches(ceil_div(todo.size(), kMaxItems));
-    for (size_t b = 0; b < launches.size(); ++b) {
-      const size_t k = b * kMaxItems;
-      Launch& l = launches[b];
-      st = plan_launch(&todo[k], std::min<size_t>(kMaxItems, todo.size() - k), first, &l);
+    std::vector<Launch> launches;
+    for (size_t k = 0, e; k < todo.size(); k = e) {
+      e = launch_end(todo, k);
+      launches.emplace_back();
+      Launch& l = launches.back();
+      st = plan_launch(&todo[k], e - k, first, &l);
       if (st != ZR_OK) return st;
       if (l.bytes > 0 && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < l.bytes))
         return fail(ZR_ERR_INVALID, "workspace is null, not 16-byte aligned or smaller than " +
@@ -751,11 +834,15 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
       l.a.partial = static_cast<float*>(workspace);
     }
     for (const Launch& l : launches) {
-      linear_kernel<<<l.grid, kThreads, 0, stream>>>(l.a);
+      const bool in_major = l.a.item[0].in_major, direct = l.a.item[0].direct;
+      auto* kernel = in_major ? (direct ? linear_kernel<true, true> : linear_kernel<true, false>)
+                              : (direct ? linear_kernel<false, true> : linear_kernel<false, false>);
+      kernel<<<l.grid, kThreads, 0, stream>>>(l.a);
       st = launched("linear gradient launch");
       if (st != ZR_OK) return st;
       if (l.cut == 0) continue;
-      linear_join_kernel<<<l.cut * kJoins, kThreads, 0, stream>>>(l.a);
+      auto* join = in_major ? linear_join_kernel<true> : linear_join_kernel<false>;
+      join<<<l.cut * kJoins, kThreads, 0, stream>>>(l.a);
       st = launched("linear gradient join launch");
       if (st != ZR_OK) return st;
     }
@@ -819,9 +906,10 @@ extern "C" zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linea
       zr_status st = linear_items(plan, items, n, reinterpret_cast<const float*>(4), window_base,
                                   window_len, first, &todo);
       if (st != ZR_OK) return st;
-      for (size_t k = 0; k < todo.size(); k += kMaxItems) {
+      for (size_t k = 0, e; k < todo.size(); k = e) {
+        e = launch_end(todo, k);
         Launch l;
-        st = plan_launch(&todo[k], std::min<size_t>(kMaxItems, todo.size() - k), first, &l);
+        st = plan_launch(&todo[k], e - k, first, &l);
         if (st != ZR_OK) return st;
         *bytes = std::max(*bytes, l.bytes);
       }
