@@ -104,8 +104,9 @@ __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupA
 // -------------------------------------------------------------- gradient ---
 //
 // main_grad[row] (+)= scale * sum of dY over the tokens with that row's id.
-// 1. sort: the positions of the tokens whose row meets the window, by row and
-//    in their own order within a row;
+// 1. sort: the positions of the tokens whose row meets the window, row after
+//    row (in no particular order of the rows) and in their own order within a
+//    row;
 // 2. sum: pieces of 8 to 64 sorted positions, each summed by waves of its own
 //    in that order.  A row whose tokens lie in one piece is added to
 //    main_grad at once; one that spans pieces leaves a partial sum per piece;
@@ -129,7 +130,7 @@ struct SortArgs {
   EmbedWork w;
   int64_t n, row0;
   int32_t rows;           // the window's rows: [row0, row0 + rows)
-  int32_t span;           // rows per workgroup
+  int32_t shift;          // 2^shift workgroups
   // first micro-batch only: rows without tokens are zeroed
   float* main_grad;       // null otherwise; where the table's element 0 lies
   int64_t dim, first, last;
@@ -148,50 +149,67 @@ __device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t 
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) r[g] = t[g] >= 0 && t[g] < a.rows ? static_cast<int32_t>(t[g]) : -1;
 }
-__device__ __forceinline__ void count_rows(const Rows& r, int lo, int span, int32_t* place, int* before) {
+__device__ __forceinline__ void count_rows(const Rows& r, int shift, int32_t* place, int* before) {
+  const int mask = (1 << shift) - 1, mine = blockIdx.x;
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    if (r[g] >= 0 && r[g] < lo) ++*before;
-    if (r[g] >= lo && r[g] < lo + span) atomicAdd(&place[r[g] - lo], 1);
+    if (r[g] >= 0 && (r[g] & mask) < mine) ++*before;
+    if (r[g] >= 0 && (r[g] & mask) == mine) atomicAdd(&place[r[g] >> shift], 1);
   }
 }
-// Lanes of one row find each other by a ballot on each bit of the row: a row
-// that fills the wave costs no more than 64 different ones.
-__device__ __forceinline__ void place_rows(const EmbedWork& w, const Rows& r, int64_t i, int lo, int span,
+// Puts 64 positions at a time where their rows' next ones belong.  Lanes of
+// one row find each other by a ballot for the first lane's row, and the next
+// one's; where more than kTries rows meet, by a ballot for each bit of the row.
+constexpr int kTries = 3;
+__device__ __forceinline__ void place_rows(const EmbedWork& w, const Rows& r, int64_t i, int shift,
                                            int bits, int lane, int32_t* place) {
+  const int mask = (1 << shift) - 1, own = blockIdx.x;
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    const int row = r[g] - lo;
-    const bool mine = r[g] >= lo && row < span;
-    uint64_t same = __ballot(mine);
-    if (same == 0) continue;
-    for (int b = 0; b < bits; ++b) {
-      const int64_t one = -static_cast<int64_t>((row >> b) & 1);
-      same &= ~(__ballot(one) ^ one);
-    }
-    if (mine) {
-      const int p = place[row], rank = __popcll(same & ((1ull << lane) - 1));
-      w.pos[p + rank] = static_cast<int32_t>(i + 64 * g);
-      w.row[p + rank] = r[g];
-      if ((same >> lane) == 1) place[row] = p + rank + 1;   // the row's last lane
+    const int row = r[g] >> shift;
+    bool left = r[g] >= 0 && (r[g] & mask) == own;
+    uint64_t todo = __ballot(left);
+    for (int t = 0; todo; ++t) {
+      uint64_t same = todo;
+      bool mine = left;
+      if (t < kTries) {
+        const int one = __builtin_amdgcn_readlane(row, __builtin_ctzll(todo));
+        mine = left && row == one;
+        same = __ballot(mine);
+      } else {
+        for (int b = 0; b < bits; ++b) {
+          const int64_t bit = -static_cast<int64_t>((row >> b) & 1);
+          same &= ~(__ballot(bit) ^ bit);
+        }
+      }
+      if (mine) {
+        const int p = place[row], rank = __popcll(same & ((1ull << lane) - 1));
+        w.pos[p + rank] = static_cast<int32_t>(i + 64 * g);
+        w.row[p + rank] = r[g];
+        if ((same >> lane) == 1) place[row] = p + rank + 1;   // the row's last lane
+        left = false;
+      }
+      todo = t < kTries ? todo & ~same : 0;
     }
   }
 }
 
-// Workgroup g sorts the tokens of rows [g*span, (g+1)*span): it counts, over
-// the whole batch, the tokens of earlier rows (its first place in the order)
-// and those of each row of its own, by wave; then every wave places its share
-// of the batch, in order, behind what earlier rows and earlier waves have.
-// Every workgroup reads all ids (from L2), so that one launch sorts and nothing
-// waits for another workgroup.
+// Workgroup g sorts the tokens of the rows r with r mod 2^shift = g (the
+// commonest ids are often neighbours: taken apart, no workgroup has many of
+// them).  It counts, over the whole batch, the tokens of earlier workgroups
+// (its first place in the order) and those of each row of its own, by wave;
+// then every wave places its share of the batch, in order, behind what earlier
+// rows and earlier waves have.  Every workgroup reads all ids (from L2), so
+// that one launch sorts and nothing waits for another workgroup.  Measured,
+// 32768 ids over 16032 rows: TIME us, 31 with neighbouring rows together.
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortArgs a) {
   __shared__ int32_t place[kSortWaves][kSortRows];
   __shared__ int32_t wave_sum[kSortWaves];
   __shared__ int32_t before_s;
   __shared__ uint8_t empty[kSortRows];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const int lo = blockIdx.x * a.span;
-  const int span = a.rows - lo < a.span ? a.rows - lo : a.span;
+  const int own = blockIdx.x;
+  const int span = (a.rows - own + (1 << a.shift) - 1) >> a.shift;   // its rows
   for (int i = lane; i < span; i += 64) place[w][i] = 0;
   if (tid == 0) before_s = 0;
   __syncthreads();
@@ -203,11 +221,11 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
 #pragma unroll
   for (int k = 0; k < kKept; ++k) load_rows(a, i0 + lane + k * kStep, i1, kept[k]);
 #pragma unroll
-  for (int k = 0; k < kKept; ++k) count_rows(kept[k], lo, span, place[w], &before);
+  for (int k = 0; k < kKept; ++k) count_rows(kept[k], a.shift, place[w], &before);
   for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
     Rows r;
     load_rows(a, i + lane, i1, r);
-    count_rows(r, lo, span, place[w], &before);
+    count_rows(r, a.shift, place[w], &before);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
@@ -236,33 +254,28 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
       at += c;
     }
   __syncthreads();
-  const int bits = 32 - __builtin_clz(a.span);
+  const int bits = 32 - __builtin_clz(span);
 #pragma unroll
   for (int k = 0; k < kKept; ++k)
-    place_rows(a.w, kept[k], i0 + lane + k * kStep, lo, span, bits, lane, place[w]);
+    place_rows(a.w, kept[k], i0 + lane + k * kStep, a.shift, bits, lane, place[w]);
   for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
     Rows r;
     load_rows(a, i + lane, i1, r);
-    place_rows(a.w, r, i + lane, lo, span, bits, lane, place[w]);
+    place_rows(a.w, r, i + lane, a.shift, bits, lane, place[w]);
   }
   if (!a.main_grad) return;
-  // Zeros to the rows without tokens: each wave takes a sixteenth of the rows,
-  // and neighbouring ones together.
-  for (int r = w * span / kSortWaves, end = (w + 1) * span / kSortWaves; r < end;) {
-    int next = r + 1;
-    if (empty[r]) {
-      while (next < end && empty[next]) ++next;
-      const int64_t e = (a.row0 + lo + r) * a.dim, g = (a.row0 + lo + next) * a.dim;
-      const int64_t f = e > a.first ? e : a.first, l = g < a.last ? g : a.last;
-      float* p = a.main_grad + f;
-      const int64_t n = l - f;
-      const int lead = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 4) & 3);   // to 16 bytes
-      if (lane < lead && lane < n) p[lane] = 0.0f;
-      int64_t c = lead + 4 * lane;
-      for (; c + 4 <= n; c += 256) *as_global<f32x4>(p + c) = f32x4{0, 0, 0, 0};
-      for (; c < n; ++c) p[c] = 0.0f;
-    }
-    r = next;
+  // Zeros to the rows without tokens, a wave to a row.
+  for (int r = w; r < span; r += kSortWaves) {
+    if (!empty[r]) continue;
+    const int64_t e = (a.row0 + own + (static_cast<int64_t>(r) << a.shift)) * a.dim;
+    const int64_t f = e > a.first ? e : a.first, l = e + a.dim < a.last ? e + a.dim : a.last;
+    float* p = a.main_grad + f;
+    const int n = static_cast<int>(l - f);
+    const int lead = static_cast<int>(-(reinterpret_cast<uintptr_t>(p) / 4) & 3);   // to 16 bytes
+    if (lane < lead && lane < n) p[lane] = 0.0f;
+    int c = lead + 4 * lane;
+    for (; c + 4 <= n; c += 256) *as_global<f32x4>(p + c) = f32x4{0, 0, 0, 0};
+    for (; c < n; ++c) p[c] = 0.0f;
   }
 }
 
@@ -611,12 +624,15 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     const int64_t rows = ceil_div(clip.last, dim) - sa.row0;
     if (rows >= (int64_t(1) << 30)) return fail(ZR_ERR_UNSUPPORTED, "2^30 rows or more in the window");
     sa.rows = static_cast<int32_t>(rows);
-    sa.span = static_cast<int32_t>(std::min<int64_t>(kSortRows, ceil_div(rows, 256)));
+    // as many workgroups as the chip has CUs, where each has a row and none too many
+    sa.shift = 0;
+    while ((int64_t(1) << sa.shift) < 256 && (int64_t(2) << sa.shift) <= rows) ++sa.shift;
+    while ((rows >> sa.shift) >= kSortRows) ++sa.shift;
     sa.main_grad = first ? table : nullptr;
     sa.dim = dim;
     sa.first = clip.first;
     sa.last = clip.last;
-    embed_sort_kernel<<<ceil_div(sa.rows, sa.span), 64 * kSortWaves, 0, stream>>>(sa);
+    embed_sort_kernel<<<1 << sa.shift, 64 * kSortWaves, 0, stream>>>(sa);
     st = launched("embedding sort launch");
     if (st != ZR_OK || n == 0) return st;
     SumArgs a{};
