@@ -134,6 +134,18 @@ def test_gradient_without_a_valid_token(first):
     _grad_case(9, 12, 2, 0, 0, False, first, 1, t[:0], dy[:0], 1.0)
 
 
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("n", [700, 9000, 40000])
+def test_gradient_of_ids_that_one_workgroup_sorts(n, first):
+    """Ids a power of two apart, so that the rows dealt out to one workgroup
+    meet within every 64 tokens; and batches longer than a wave keeps."""
+    rng = np.random.default_rng(n)
+    t = 256 * rng.integers(0, 60, n) + rng.integers(0, 2, n)
+    t[::7] = rng.integers(0, 15500, t[::7].size)
+    dy = rng.integers(-50, 51, (n, 12)).astype(np.float32)
+    _grad_case(15500, 12, 1, 0, n, True, first, None, t, dy, 1.0, exact=True)
+
+
 def test_gradient_has_the_same_bits_on_every_run():
     rng = np.random.default_rng(8)
     t = _ids(rng, 500, 20000)

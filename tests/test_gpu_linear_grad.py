@@ -16,7 +16,8 @@ from tests._layers import Window, check_window, checkpoint, rows, workspace  # n
 SIZES = [  # outputs, inputs, tokens
     (1, 1, 1), (7, 5, 3), (128, 128, 64), (130, 97, 65), (300, 70, 63), (64, 513, 17),
     (257, 256, 300), (96, 40, 0), (1000, 33, 129), (33, 1000, 16), (640, 384, 1025), (2, 3, 5000),
-    (129, 127, 4100), (513, 511, 7),
+    (129, 127, 4100), (513, 511, 7), (264, 512, 4096), (512, 264, 3001), (8, 40, 191),
+    (776, 300, 128),
 ]
 
 
@@ -109,6 +110,21 @@ def test_long_sums_and_few_weights():
                 win = Window(n_out * n_in, 3)
                 _run(plan, [(0, *item)], win, 0, first)
                 check_window(win, 0, g, np.zeros_like(size) if whole else size, tokens, first)
+
+
+@pytest.mark.parametrize("in_major", [False, True])
+def test_rows_of_dy_on_and_off_sixteen_bytes_in_one_call(in_major):
+    """Layers of both kinds, and a weight cut along its tokens among them."""
+    rng = np.random.default_rng(21)
+    shapes = [(256, 130, 4500, 0), (256, 130, 4500, 1), (40, 70, 600, 8), (41, 70, 600, 0)]
+    plan = zr.zr_plan_buckets([a * b for a, b, _, _ in shapes], [0] * 4, [(1, 1)], 1 << 40)
+    layers = [_layer(rng, a, b, t, pad, whole=True) for a, b, t, pad in shapes]
+    grads = [linear_grad_oracle(dy, x, in_major)[0] for _, dy, x in layers]
+    for first in (False, True):
+        win = Window(sum(a * b for a, b, _, _ in shapes), 1)
+        _run(plan, [(k, *item, in_major) for k, (item, _, _) in enumerate(layers)], win, 0, first)
+        g = np.concatenate([g.ravel() for g in grads])
+        check_window(win, 0, g, np.zeros_like(g), 4500, first)
 
 
 def test_small_and_large_scales():
