@@ -725,16 +725,21 @@ def zr_all_gather_params(plan, group, parts, out, out_base=0, out_len=None,
 _FLOATS = None if torch is None else (torch.bfloat16, torch.float32)
 
 
-def _device():
-    """The current device; before torch has used one there is no device tensor
-    to compare it with (-2: not the -1 of host tensors)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+def _device_of(t, name):
+    """The device of a call's first tensor, which has to be the current one; -2
+    (no tensor's) for a host tensor, which the checks that follow refuse."""
+    dev = t.get_device()
+    if dev < 0:
+        return -2
+    if dev != torch._C._cuda_getDevice():
+        _refuse_device(t, name, torch.cuda.current_device())
+    return dev
 
 
 def _refuse_device(t, name, dev):
     if not t.is_cuda:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be a device tensor")
-    raise ZrError(ZR_ERR_INVALID, f"{name} is on device {t.get_device()}, not on the current one "
+    raise ZrError(ZR_ERR_INVALID, f"{name} is on device {t.get_device()}, not on the call's "
                                   f"({dev})")
 
 
@@ -794,7 +799,7 @@ def zr_embedding_lookup(plan, param, dim, parts, tokens, out, scale=1.0, stream=
     read from the R_g partition tensors ``parts`` (bf16 or fp32, those that
     hold none of the table may be None); ids outside [0, vocab) give zeros.
     tokens: int64 or int32, any shape; out: [tokens.numel(), dim]."""
-    dev = _device()
+    dev = _device_of(tokens, "tokens")
     ids, wide = _token_ids(tokens, dev)
     n, d, p = tokens.numel(), _i64(dim, "dim"), _i64(param, "param")
     ptr, stride = _rows(out, "out", dev, n, d)
@@ -838,7 +843,7 @@ def zr_ipg_accumulate_embedding_first(plan, param, dim, tokens, dy, main_grad, w
 
 def _embedding(fn, plan, param, dim, tokens, dy, main_grad, workspace, window_base, window_len,
                scale, stream):
-    dev = _device()
+    dev = _device_of(tokens, "tokens")
     ids, wide = _token_ids(tokens, dev)
     n, d = tokens.numel(), _i64(dim, "dim")
     ptr, stride = _rows(dy, "dy", dev, n, d)
@@ -880,7 +885,7 @@ def _checkpoint(codes, scales, dev, rows, cols):
 def zr_act_quantize(x, codes, scales, stream=None):
     """The 8-bit checkpoint of x (bf16 or fp32, [rows, cols]) into the tensors
     of act_empty."""
-    dev = _device()
+    dev = _device_of(x, "x")
     ptr, stride = _rows(x, "x", dev)
     rows, cols = x.shape
     c, s = _checkpoint(codes, scales, dev, rows, cols)
@@ -891,7 +896,7 @@ def zr_act_quantize(x, codes, scales, stream=None):
 def zr_act_dequantize(codes, scales, out, stream=None):
     """The activations a checkpoint stands for, into out (bf16 or fp32,
     [rows, cols])."""
-    dev = _device()
+    dev = _device_of(out, "out")
     ptr, stride = _rows(out, "out", dev)
     rows, cols = out.shape
     c, s = _checkpoint(codes, scales, dev, rows, cols)
@@ -899,9 +904,12 @@ def zr_act_dequantize(codes, scales, out, stream=None):
                                   _stream_of(stream, dev)))
 
 
-def _linear_items(plan, items, dev):
+def _linear_items(plan, items, dev=None):
+    """The items as the C call takes them, on one device (None: the first's)."""
     arr = (zr_linear_grad * max(len(items), 1))()
     for k, (param, dy, codes, scales, *in_major) in enumerate(items):
+        if dev is None:
+            dev = _device_of(dy, "an item's dy")
         p = _i64(param, "an item's param")
         ptr, stride = _rows(dy, "an item's dy", dev, dtypes=(torch.bfloat16,))
         tokens, n_out = dy.shape
@@ -916,7 +924,7 @@ def _linear_items(plan, items, dev):
 def zr_ipg_linear_workspace(plan, items, window_base, window_len):
     """Bytes of workspace zr_ipg_accumulate_linear needs for these items."""
     v = c_i64()
-    _check(_lib.zr_ipg_linear_workspace(plan.handle, _linear_items(plan, items, _device()),
+    _check(_lib.zr_ipg_linear_workspace(plan.handle, _linear_items(plan, items),
                                         len(items),
                                         _i64(window_base, "window_base"),
                                         _i64(window_len, "window_len"), ctypes.byref(v)))
@@ -943,7 +951,7 @@ def zr_ipg_accumulate_linear_first(plan, items, main_grad, workspace, window_bas
 
 
 def _linear(fn, plan, items, main_grad, workspace, window_base, window_len, stream):
-    dev = _device()
+    dev = _device_of(main_grad, "main_grad")
     wl = main_grad.numel() if window_len is None else _i64(window_len, "window_len")
     arr = _linear_items(plan, items, dev)
     ws = None if workspace is None else _dense(workspace, "workspace", dev, torch.uint8)
