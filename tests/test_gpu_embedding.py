@@ -23,7 +23,7 @@ def _ids(rng, vocab, n, masked=0.1):
     """Ids whose frequency falls with their rank; some outside the table."""
     t = np.minimum(np.exp(rng.random(n) * np.log(vocab + 1)).astype(np.int64) - 1, vocab - 1)
     out = rng.random(n) < masked
-    t[out] = rng.choice([-100, -1, vocab, vocab + 5, 2 ** 31 - 1], int(out.sum()))
+    t[out] = rng.choice([-100, -1, vocab, vocab + 5, 2 ** 31 - 1, -2 ** 31], int(out.sum()))
     return t
 
 
@@ -132,6 +132,17 @@ def test_gradient_without_a_valid_token(first):
     t = np.full(50, -100)
     _grad_case(9, 12, 2, 0, 50, False, first, None, t, dy, 1.0)
     _grad_case(9, 12, 2, 0, 0, False, first, 1, t[:0], dy[:0], 1.0)
+
+
+def test_ids_at_the_ends_of_64_bits():
+    t = np.array([-2 ** 63, 2 ** 63 - 1, 3, -2 ** 63 + 5, 2 ** 62, 2 ** 32 + 3])
+    dy = np.full((6, 8), np.nan, np.float32)
+    dy[2] = 2.0
+    for part in (0, 1):
+        _grad_case(9, 8, 2, 0, 6, False, True, part, t, dy, 1.0)
+    plan, out = _plan([72], 1), torch.empty(6, 8, device="cuda")
+    zr.zr_embedding_lookup(plan, 0, 8, [torch.ones(72, device="cuda")], torch.from_numpy(t).cuda(), out)
+    assert out.sum(1).tolist() == [0, 0, 8, 0, 0, 0]
 
 
 @pytest.mark.parametrize("first", [False, True])

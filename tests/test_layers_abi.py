@@ -109,7 +109,7 @@ def test_workspace_queries():
     (dict(x=None), "x is null"), (dict(x=A + 1), "x is null"), (dict(dtype=7), "dtype"),
     (dict(rows=-1), "rows"), (dict(cols=0), "cols"), (dict(cols=1 << 30, stride=1 << 30), "2^30"),
     (dict(stride=9), "stride"), (dict(codes=None), "codes"), (dict(codes=A + 8), "codes"),
-    (dict(scales=None), "scales"),
+    (dict(scales=None), "scales"), (dict(rows=1 << 62), "too many"),
 ])
 def test_checkpoint_refusals(change, words):
     v = dict(x=A, dtype=zr.ZR_BF16, rows=4, cols=10, stride=10, codes=A, scales=A)
@@ -136,6 +136,7 @@ def _item(**change):
 
 @pytest.mark.parametrize("first", [False, True])
 @pytest.mark.parametrize("items,call,words", [
+    ([_item(tokens=1 << 31)], {}, "2^31"), ([_item(dy_stride=1 << 24)], {}, "2^24"),
     ([_item(param=4)], {}, "param id"), ([_item(param=-1)], {}, "param id"),
     ([_item(), _item()], {}, "twice"),
     ([_item(), _item(param=3, n_out=3, n_in=4)], {}, "share a group"),

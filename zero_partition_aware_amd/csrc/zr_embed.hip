@@ -150,8 +150,9 @@ __device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t 
     t[g] = as_global<Id>(a.tokens.ids)[i + 64 * g < end ? i + 64 * g : a.n - 1];
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    const int64_t row = static_cast<int64_t>(t[g]) - a.row0;
-    r[g] = i + 64 * g < end && row >= 0 && row < a.rows ? static_cast<int32_t>(row) : -1;
+    const int64_t id = t[g];
+    const bool in = i + 64 * g < end && id >= a.row0 && id < a.row0 + a.rows;
+    r[g] = in ? static_cast<int32_t>(id - a.row0) : -1;
   }
 }
 __device__ __forceinline__ void count_rows(const Rows& r, int shift, int32_t* place, int* before) {

@@ -673,8 +673,7 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(const LinearArgs 
 
 zr_status check_rows(const void* codes, const uint8_t* scales, int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 1) return fail(ZR_ERR_INVALID, "rows must be >= 0 and cols >= 1");
-  if (cols >= (int64_t(1) << 30) || rows >= (int64_t(1) << 40))
-    return fail(ZR_ERR_UNSUPPORTED, "2^30 columns or 2^40 rows or more");
+  if (cols >= (int64_t(1) << 30)) return fail(ZR_ERR_UNSUPPORTED, "2^30 columns or more");
   if (rows > 0 && (!codes || !aligned_to(codes, 16) || !scales))
     return fail(ZR_ERR_INVALID, "codes or scales is null, or codes is not 16-byte aligned");
   return ZR_OK;
@@ -693,9 +692,10 @@ zr_status act_args(const void* x, zr_dtype dtype, int64_t rows, int64_t cols, in
   a->cols = cols;
   a->stride = stride;
   a->row_groups = static_cast<int32_t>(ceil_div(cols, kBlock) * (kBlock / 8));
+  if (rows > int64_t(0x7fffffff) * kActThreads / a->row_groups)
+    return fail(ZR_ERR_UNSUPPORTED, "too many elements for one call");
   a->total = rows * a->row_groups;
   *grid = ceil_div(a->total, kActThreads);
-  if (*grid > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "too many elements for one call");
   return ZR_OK;
 }
 
@@ -725,8 +725,10 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
       return fail(ZR_ERR_INVALID, "n_out * n_in must be the param's elements");
     st = check_rows(z.codes, z.scales, z.tokens, z.n_in);
     if (st != ZR_OK) return st;
-    if (z.n_in >= (int64_t(1) << 24) || z.dy_stride >= (int64_t(1) << 24))
-      return fail(ZR_ERR_UNSUPPORTED, "n_in or dy_stride of 2^24 or more");   // 32-bit offsets in a tile
+    // 32-bit offsets in a tile, and tiles counted in 32 bits
+    if (z.n_in >= (int64_t(1) << 24) || z.dy_stride >= (int64_t(1) << 24) ||
+        z.tokens >= (int64_t(1) << 31))
+      return fail(ZR_ERR_UNSUPPORTED, "n_in or dy_stride of 2^24, or tokens of 2^31, or more");
     if (z.dy_stride < z.n_out) return fail(ZR_ERR_INVALID, "dy_stride must be >= n_out");
     if (z.tokens > 0 && (!z.dy || !aligned_to(z.dy, 2)))
       return fail(ZR_ERR_INVALID, "dy is null or not element-aligned");
