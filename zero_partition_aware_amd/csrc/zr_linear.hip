@@ -593,11 +593,24 @@ __device__ __forceinline__ void put_sums(const Item& it, const Place<kInMajor>& 
     for (int v = 0; v < kCount; ++v)
       *as_global<float>(p + (8 * ((v0 + v) / 4) + ((v0 + v) & 3)) * cols) = old[v] + sums[v];
   } else {
+    auto place = [&](int v) { return (row + 8 * ((v0 + v) / 4) + ((v0 + v) & 3)) * cols + col; };
+    auto there = [&](int v) {
+      return row + 8 * ((v0 + v) / 4) + ((v0 + v) & 3) < rows && col < cols &&
+             place(v) >= it.first && place(v) < it.last;
+    };
+    if (first) {
 #pragma unroll
-    for (int v = 0; v < kCount; ++v) {
-      const int64_t r = row + 8 * ((v0 + v) / 4) + ((v0 + v) & 3), e = r * cols + col;
-      if (r < rows && col < cols && e >= it.first && e < it.last)
-        it.grad[e] = (first ? 0.0f : it.grad[e]) + sums[v];
+      for (int v = 0; v < kCount; ++v)
+        if (there(v)) it.grad[place(v)] = 0.0f + sums[v];
+    } else {   // all asked for before the first is used
+      float old[kCount] = {};
+      bool in[kCount];
+#pragma unroll
+      for (int v = 0; v < kCount; ++v)
+        if ((in[v] = there(v))) old[v] = it.grad[place(v)];
+#pragma unroll
+      for (int v = 0; v < kCount; ++v)
+        if (in[v]) it.grad[place(v)] = old[v] + sums[v];
     }
   }
 }
@@ -780,17 +793,29 @@ size_t launch_end(const std::vector<Item>& items, size_t k) {
   return e;
 }
 
-// The launch of up to kMaxItems items: which tiles are one workgroup's, and
-// which are cut along their tokens so that the last round of tiles fills the
-// chip's 256 CUs (one workgroup each).  Cutting costs the pieces' writes and
-// reads, about the time of sixteen tiles of tokens when every CU has a piece
-// (256 kB each, 64 MB in all: 25 us against 1.7 us a tile), so it has to save
-// more than that.  Measured, cut and not, over 8192 tokens: 2304 x 768 and
-// 768 x 768 weights (36 tiles, 7 pieces each) 61 and 178 us, 14336 x 4096
-// (896 tiles, the last 128 in 2 pieces) 818 and 865 us; over 4096 tokens 2560
-// x 2560 (100 tiles in 2 pieces) 72 and 95 us.
-constexpr int kCus = 256, kCutCost = 16;
+// How many pieces the tokens of a tile in the last round are cut into, where
+// `rest` tiles are left for the chip's 256 CUs (one workgroup each): the number
+// with the least time in the model below, in 256ths of the time that a tile of
+// tokens takes (1.6 us).  Cutting costs the join's launch and the pieces'
+// writes and reads, 256 kB each: 3 tiles, and 13 more when every CU has a
+// piece.  Measured, cut and not: 2304 x 768 and 768 x 768 weights over 8192
+// tokens (36 tiles, 7 pieces each; with 5 and 4 pieces 1 us less and 3 more)
+// 56 and 160 us; 2560 x 2560 over 4096 (100 tiles, 2 pieces) 66 and 85; 1024 x
+// 1024 over 2048 (16 tiles, 6 pieces) 28 and 44; 160 x 2451 over 1164 (10
+// tiles, 4 pieces) 22 and 44; 14336 x 4096 over 8192 (896 tiles, the last 128
+// in 2 pieces) 777 and 833 us.
+constexpr int kCus = 256;
+int32_t pieces_of(int64_t steps, int64_t rest) {
+  int64_t best = 1, least = 256 * steps;
+  for (int64_t p = 2; p * rest <= kCus && 2 * p <= steps; ++p) {
+    const int64_t cost = 256 * ceil_div(steps, p) + 3 * 256 + 13 * rest * p;
+    if (cost < least) best = p, least = cost;
+  }
+  return static_cast<int32_t>(best);
+}
 
+// The launch of up to kMaxItems items: which tiles are one workgroup's, and
+// which are cut along their tokens so that the last round fills the chip.
 struct Launch {
   LinearArgs a;
   int64_t grid = 0, cut = 0, bytes = 0;   // workgroups, cut tiles, workspace
@@ -809,13 +834,9 @@ zr_status plan_launch(const Item* items, size_t n, bool first, Launch* out) {
     Item& it = a.item[k] = items[k];
     const int64_t count = int64_t(it.out_tiles) * it.in_tiles;
     const int64_t steps = ceil_div(it.tokens, kDepth);
-    it.pieces = 1;
-    if (rest > 0) it.pieces = static_cast<int32_t>(std::min(kCus / rest, steps / 4));
-    it.whole = static_cast<int32_t>(std::min(count, std::max<int64_t>(0, tiles - rest - before)));
-    if (it.pieces < 2 || steps - ceil_div(steps, it.pieces) < kCutCost) {
-      it.pieces = 1;
-      it.whole = static_cast<int32_t>(count);
-    }
+    it.pieces = rest > 0 ? pieces_of(steps, rest) : 1;
+    it.whole = static_cast<int32_t>(
+        it.pieces > 1 ? std::min(count, std::max<int64_t>(0, tiles - rest - before)) : count);
     it.whole0 = static_cast<int32_t>(whole);
     it.piece0 = static_cast<int32_t>(pieces);
     it.cut0 = static_cast<int32_t>(out->cut);
