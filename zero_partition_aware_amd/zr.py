@@ -748,22 +748,25 @@ def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS):
     one of the torch dtypes on the device ``dev`` and returns (address,
     stride).  Rows may lie apart (a slice of wider rows); a strided or
     broadcast column axis is refused."""
+    shape = t.shape
+    if len(shape) == 2 and t.dtype in dtypes and t.get_device() == dev:
+        n, c = shape
+        stride, step = t.stride()
+        if n < 2 and stride < c:
+            stride = c
+        if ((rows is None or n == rows) and (cols is None or c == cols) and stride >= c and
+                (step == 1 or c < 2)):
+            return t.data_ptr(), stride
     if t.dtype not in dtypes:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be one of {dtypes}, not {t.dtype}")
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and
-                                                                      shape[1] != cols):
+    if len(shape) != 2 or shape[0] != (shape[0] if rows is None else rows) or \
+            shape[1] != (shape[1] if cols is None else cols):
         raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(shape)}; the call needs "
                                       f"({'any' if rows is None else rows}, "
                                       f"{'any' if cols is None else cols})")
     if t.get_device() != dev:
         _refuse_device(t, name, dev)
-    stride, step = t.stride()
-    if shape[0] < 2 and stride < shape[1]:
-        stride = shape[1]
-    if (step != 1 and shape[1] > 1) or stride < shape[1]:
-        raise ZrError(ZR_ERR_INVALID, f"{name} must have contiguous rows")
-    return t.data_ptr(), stride
+    raise ZrError(ZR_ERR_INVALID, f"{name} must have contiguous rows")
 
 
 def _dense(t, name, dev, dtype, min_numel=0):
@@ -808,10 +811,16 @@ def zr_embedding_lookup(plan, param, dim, parts, tokens, out, scale=1.0, stream=
     P, dtype = _part_numel(plan, group), out.dtype
     arr = (c_vp * len(parts))()
     for k, t in enumerate(parts):
-        if t is not None:
-            arr[k] = _dense(t, "a partition", dev, dtype, P)
-    _check(_lib.zr_embedding_lookup(plan.handle, p, d, arr, _dtype_code(out), ids, wide, n,
-                                    scale, ptr, stride, _stream_of(stream, dev)))
+        if t is None:
+            continue
+        if not (t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and
+                t.numel() >= P):
+            _dense(t, f"parts[{k}]", dev, dtype, P)
+        arr[k] = t.data_ptr()
+    status = _lib.zr_embedding_lookup(plan.handle, p, d, arr, dtype is torch.bfloat16, ids, wide,
+                                      n, scale, ptr, stride, _stream_of(stream, dev))
+    if status:
+        _check(status)
 
 
 def zr_ipg_embedding_workspace(plan, param, dim, n, window_base, window_len):
@@ -870,16 +879,23 @@ def act_empty(rows, cols, device="cuda"):
             torch.empty((rows, s), dtype=torch.uint8, device=device))
 
 
+_E4M3 = None if torch is None else torch.float8_e4m3fn
+_U8 = None if torch is None else torch.uint8
+
+
 def _checkpoint(codes, scales, dev, rows, cols):
     """Checks a checkpoint's tensors and returns their addresses."""
-    blocks = -(-cols // 32)
+    blocks = (cols + 31) >> 5
+    if (codes.shape == (rows, 32 * blocks) and scales.shape == (rows, blocks) and
+            codes.dtype is _E4M3 and scales.dtype is _U8 and codes.get_device() == dev and
+            scales.get_device() == dev and codes.is_contiguous() and scales.is_contiguous()):
+        return codes.data_ptr(), scales.data_ptr()
     if codes.shape != (rows, 32 * blocks) or scales.shape != (rows, blocks):
         raise ZrError(ZR_ERR_INVALID,
                       f"codes and scales have shapes {tuple(codes.shape)} and "
                       f"{tuple(scales.shape)}; a checkpoint of [{rows}, {cols}] has "
                       f"{(rows, 32 * blocks)} and {(rows, blocks)}")
-    return (_dense(codes, "codes", dev, torch.float8_e4m3fn),
-            _dense(scales, "scales", dev, torch.uint8))
+    return _dense(codes, "codes", dev, _E4M3), _dense(scales, "scales", dev, _U8)
 
 
 def zr_act_quantize(x, codes, scales, stream=None):
@@ -889,8 +905,10 @@ def zr_act_quantize(x, codes, scales, stream=None):
     ptr, stride = _rows(x, "x", dev)
     rows, cols = x.shape
     c, s = _checkpoint(codes, scales, dev, rows, cols)
-    _check(_lib.zr_act_quantize(ptr, _dtype_code(x), rows, cols, stride, c, s,
-                                _stream_of(stream, dev)))
+    status = _lib.zr_act_quantize(ptr, x.dtype is torch.bfloat16, rows, cols, stride, c, s,
+                                  _stream_of(stream, dev))
+    if status:
+        _check(status)
 
 
 def zr_act_dequantize(codes, scales, out, stream=None):
@@ -900,8 +918,10 @@ def zr_act_dequantize(codes, scales, out, stream=None):
     ptr, stride = _rows(out, "out", dev)
     rows, cols = out.shape
     c, s = _checkpoint(codes, scales, dev, rows, cols)
-    _check(_lib.zr_act_dequantize(c, s, rows, cols, ptr, _dtype_code(out), stride,
-                                  _stream_of(stream, dev)))
+    status = _lib.zr_act_dequantize(c, s, rows, cols, ptr, out.dtype is torch.bfloat16, stride,
+                                    _stream_of(stream, dev))
+    if status:
+        _check(status)
 
 
 def _linear_items(plan, items, dev=None):
