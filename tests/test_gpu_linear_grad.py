@@ -144,6 +144,22 @@ def test_small_and_large_scales():
         check_window(win, 0, g, size, 48, True)
 
 
+@pytest.mark.parametrize("dy,x,want", [
+    (2.0 ** -133, 2.0 ** 110, 2.0 ** -21),      # the least bf16 number
+    (2.0 ** -60, 2.0 ** -88, 2.0 ** -146),      # a subnormal sum
+    (2.0 ** -20, float.fromhex("0x1.fep127"), float("inf")),   # coded up to 2^128
+])
+def test_ends_of_the_number_range(dy, x, want):
+    """Four equal products of powers of two: exact, subnormals included."""
+    codes, scales = zr.act_empty(4, 32)
+    zr.zr_act_quantize(torch.full((4, 32), x, device="cuda"), codes, scales)
+    plan = zr.zr_plan_buckets([16 * 32], [0], [(1, 1)], 1 << 40)
+    grad = torch.empty(512, device="cuda")
+    item = (0, torch.full((4, 16), dy, device="cuda").bfloat16(), codes, scales)
+    zr.zr_ipg_accumulate_linear_first(plan, [item], grad, None)
+    assert (grad == want).all()
+
+
 def test_a_nan_stays_in_its_row_and_column():
     rng = np.random.default_rng(13)
     item, dy, x = _layer(rng, 140, 70, 30)
