@@ -370,15 +370,17 @@ __device__ __forceinline__ f32x4 from(f32x4 x, int n) {
 
 constexpr int kSumVecs = 2;                     // groups of four columns of a lane
 constexpr int kSumCols = 64 * 4 * kSumVecs;     // columns of a wave
-constexpr int kSumRows = 4;                     // positions of a batch
+// Positions of a batch; with main_grad's rows in flight too, as many as leave
+// room for a second workgroup on a CU (128 registers).
+template <bool kFirst> constexpr int kSumRows = kFirst ? 4 : 3;
 
-// The rows of dY of kSumRows positions, and the rows of main_grad that runs
+// The rows of dY of a batch of positions, and the rows of main_grad that runs
 // end in among them.
 template <typename T, bool kFirst>
 struct Batch {
   using Vec = decltype(load4(static_cast<const T*>(nullptr)));
-  Vec x[kSumRows][kSumVecs];
-  f32x4 old[kFirst ? 1 : kSumRows][kSumVecs];
+  Vec x[kSumRows<kFirst>][kSumVecs];
+  f32x4 old[kFirst ? 1 : kSumRows<kFirst>][kSumVecs];
 };
 
 // One wave sums one piece (at most 64) of the sorted positions over kSumCols
@@ -389,12 +391,15 @@ struct Batch {
 // What bounds it: HBM, with rows of dY in no order.  Rows of dY are read past
 // the caches (they are used once, and main_grad's lines would give way to
 // them), and the waves of a workgroup take neighbouring columns of the same
-// rows.  Measured, 32768 tokens of 4096 bf16 columns, 27000 of them in a
-// window of 16032 rows, sort and join included: 127 us in the _first form, 158
-// with ordinary loads; 138 us added, 142.
+// rows.  Measured, 32768 tokens of 4096 bf16 columns of which 27000 lie in a
+// window of 16032 rows, sort and join included: 110 us in the _first form, 138
+// with ordinary loads, 112 with workgroups of one wave; 123 us added, 126 with
+// ordinary loads, 125 with four positions a batch.  Every row twice, in no
+// order: 115 and 143; 148, 193 and 157 us.
 constexpr int kSumWaves = 8;
 template <typename T, bool kFirst, bool kTiny>   // kTiny: rows of fewer than four columns
 __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs a) {
+  constexpr int kRows = kSumRows<kFirst>;
   const int lane = threadIdx.x & 63, w = uniform(static_cast<int>(threadIdx.x >> 6));
   const int p0 = blockIdx.x * a.piece;
   const int at = p0 + lane;
@@ -421,7 +426,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
 
   auto load = [&](Batch<T, kFirst>& b, int p) {
 #pragma unroll
-    for (int k = 0; k < kSumRows; ++k) {
+    for (int k = 0; k < kRows; ++k) {
       // behind the piece the last row is asked for again, unused
       const int i = p + k < n ? p + k : n - 1;
       const T* src = static_cast<const T*>(a.dy) +
@@ -440,7 +445,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
   };
   auto add = [&](const Batch<T, kFirst>& b, int p) {
 #pragma unroll
-    for (int k = 0; k < kSumRows; ++k) {
+    for (int k = 0; k < kRows; ++k) {
       const int i = p + k;
       if (i < n) {
 #pragma unroll
@@ -481,11 +486,11 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
   };
   Batch<T, kFirst> b0, b1;
   load(b0, 0);
-  for (int p = 0; p < n; p += 2 * kSumRows) {
-    load(b1, p + kSumRows);
+  for (int p = 0; p < n; p += 2 * kRows) {
+    load(b1, p + kRows);
     add(b0, p);
-    load(b0, p + 2 * kSumRows);
-    add(b1, p + kSumRows);
+    load(b0, p + 2 * kRows);
+    add(b1, p + kRows);
   }
   if (ends >> (n - 1) & 1) return;
   // The last run goes on behind the piece.
@@ -659,7 +664,7 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     while ((rows >> sa.shift) >= kSortRows) ++sa.shift;
     sa.main_grad = first ? table : nullptr;
     // Zeroing rows that the tokens will write again costs less than waiting
-    // for the ids' count, where there are few tokens: 333 tokens of 16800 rows
+    // for the ids' count, where there are few tokens: 333 tokens of 16753 rows
     // of 1001 columns 13 us against 21, 8192 of 50257 of 768 26 against 30.
     sa.zero_all = n <= rows / 4;
     sa.dim = dim;
