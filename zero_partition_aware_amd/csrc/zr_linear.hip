@@ -475,8 +475,9 @@ __device__ __forceinline__ void phase(Acc& acc, Pipe& r, const Loader& in, const
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Tile n, with the tokens of tiles n + 1 and n + 2 from t1 and t2 on.  The pointers are restricted so that the compiler sees that reads of
-// the current buffer need not wait for what goes into the other.
+// Tile n, with the tokens of tiles n + 1 and n + 2 from t1 and t2 on.  The
+// pointers are restricted so that the compiler sees that reads of the current
+// buffer need not wait for what goes into the other.
 template <bool kInMajor, bool kDirect>
 __device__ __forceinline__ void step(Acc& acc, Pipe& r, const Loader& in, const Reader& reader,
                                      const char* __restrict cur, char* __restrict next_dy,
