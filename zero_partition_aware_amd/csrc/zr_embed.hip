@@ -137,68 +137,105 @@ struct SortArgs {
   int32_t zero_all;       // every row first, those with tokens too
 };
 
-// kGroup times 64 ids of a wave's share at once, as rows relative to the
-// window's first; -1 for an id without a row in the window.
+// kGroup times 64 ids of a wave's share at once.  A row r of the window is kept
+// as r mod 2^shift (its workgroup) above r / 2^shift (its place there), less
+// the first such number of the workgroup that reads it: below the count of that
+// workgroup's rows for its own.  Every workgroup handles every id, so the
+// instructions for each are what the sort takes: whole groups need no check of
+// their ends, and what the wave has in common is counted by its scalar unit.
 constexpr int kGroup = 8;
-constexpr int kKept = 4;   // groups that a wave keeps from its count to its placing
-using Rows = int32_t[kGroup];
+constexpr int kAhead = 4;   // groups that a wave loads at once
+constexpr int kHits = 512;  // tokens of its workgroup's rows that a wave keeps
+using Rows = uint32_t[kGroup];
 template <typename Id>
-__device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t end, Rows& r) {
+__device__ __forceinline__ void load_rows(const SortArgs& a, int64_t i, int64_t end, int lane,
+                                          uint32_t base, Rows& r) {
+  const auto* ids = as_global<Id>(a.tokens.ids) + i;
+  // Positions fit in 32 bits.  A 64-bit comparison here, taken by a branch and
+  // by a select, is compiled (ROCm 7.2) to a select on another condition.
+  const int count = min(static_cast<int>(end - i), 64 * kGroup);
   Id t[kGroup];
+  if (count == 64 * kGroup) {
 #pragma unroll
-  for (int g = 0; g < kGroup; ++g)   // behind the end the last id, unused
-    t[g] = as_global<Id>(a.tokens.ids)[i + 64 * g < end ? i + 64 * g : a.n - 1];
+    for (int g = 0; g < kGroup; ++g) t[g] = ids[lane + 64 * g];
+  } else {   // behind the end the last id, unused
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) t[g] = ids[min(lane + 64 * g, count - 1)];
+  }
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    const int64_t id = t[g];
-    const bool in = i + 64 * g < end && id >= a.row0 && id < a.row0 + a.rows;
-    r[g] = in ? static_cast<int32_t>(id - a.row0) : -1;
+    const uint64_t row = static_cast<uint64_t>(static_cast<int64_t>(t[g])) - static_cast<uint64_t>(a.row0);
+    const bool in = row < static_cast<uint32_t>(a.rows) && lane + 64 * g < count;
+    r[g] = (in ? __builtin_rotateright32(static_cast<uint32_t>(row), a.shift) : ~0u) - base;   // ~0 is no row's
   }
 }
-__device__ __forceinline__ void count_rows(const Rows& r, int shift, int32_t* place, int* before) {
-  const int mask = (1 << shift) - 1, mine = blockIdx.x;
-#pragma unroll
-  for (int g = 0; g < kGroup; ++g) {
-    if (r[g] >= 0 && (r[g] & mask) < mine) ++*before;
-    if (r[g] >= 0 && (r[g] & mask) == mine) atomicAdd(&place[r[g] >> shift], 1);
-  }
+__device__ __forceinline__ int lanes_before(uint64_t lanes, int lane) {
+  return __popcll(lanes & ((1ull << lane) - 1));
 }
-// Puts 64 positions at a time where their rows' next ones belong.  Lanes of
-// one row find each other by a ballot for the first lane's row, and the next
-// one's; where more than kTries rows meet, by a ballot for each bit of the row.
-constexpr int kTries = 3;
-__device__ __forceinline__ void place_rows(const EmbedWork& w, const Rows& r, int64_t i, int shift,
-                                           int bits, int lane, int32_t* place) {
-  const int mask = (1 << shift) - 1, own = blockIdx.x;
+
+// What a wave keeps of its share: the tokens of its workgroup's rows, in order.
+struct Hits {
+  int32_t pos[kHits];
+  uint16_t row[kHits];     // in the workgroup's order
+};
+
+// Counts each row of this workgroup, with the row of the first such lane at
+// once (one token may fill half the batch), and the tokens of earlier ones.
+__device__ __forceinline__ void count_rows(const Rows& r, int64_t i, uint32_t base, uint32_t span, int lane,
+                                           int32_t* place, Hits& hits, int* found, int* before) {
 #pragma unroll
   for (int g = 0; g < kGroup; ++g) {
-    const int row = r[g] >> shift;
-    bool left = r[g] >= 0 && (r[g] & mask) == own;
-    uint64_t todo = __ballot(left);
-    for (int t = 0; todo; ++t) {
-      uint64_t same = todo;
-      bool mine = left;
-      if (t < kTries) {
-        const int one = __builtin_amdgcn_readlane(row, __builtin_ctzll(todo));
-        mine = left && row == one;
-        same = __ballot(mine);
-      } else {
-        for (int b = 0; b < bits; ++b) {
-          const int64_t bit = -static_cast<int64_t>((row >> b) & 1);
-          same &= ~(__ballot(bit) ^ bit);
-        }
+    *before += __popcll(__ballot(r[g] > ~base));
+    const bool mine = r[g] < span;
+    const uint64_t all = __ballot(mine);
+    if (!all) continue;
+    const int leader = __builtin_ctzll(all);
+    const uint32_t one = __builtin_amdgcn_readlane(static_cast<int>(r[g]), leader);
+    const int same = __popcll(__ballot(r[g] == one));
+    if (mine) {
+      if (lane == leader) atomicAdd(&place[one], same);
+      else if (r[g] != one) atomicAdd(&place[r[g]], 1);
+      const int at = *found + lanes_before(all, lane);
+      if (at < kHits) {
+        hits.pos[at] = static_cast<int32_t>(i) + 64 * g + lane;
+        hits.row[at] = static_cast<uint16_t>(r[g]);
       }
-      if (mine) {
-        const int p = place[row], rank = __popcll(same & ((1ull << lane) - 1));
-        w.pos[p + rank] = static_cast<int32_t>(i + 64 * g);
-        w.row[p + rank] = r[g];
-        if ((same >> lane) == 1) place[row] = p + rank + 1;   // the row's last lane
-        left = false;
-      }
-      // the next lanes read what these wrote: in order in a wave, no wait needed
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      todo = t < kTries ? todo & ~same : 0;
     }
+    *found += __popcll(all);
+  }
+}
+// Puts the positions of 64 lanes where their rows' next ones belong; a lane
+// with row >= span has none.  Lanes of one row find each other by a ballot for
+// the first lane's row, and the next one's; where more than kTries rows meet,
+// by a ballot for each bit of the row.
+constexpr int kTries = 3;
+__device__ __forceinline__ void place_rows(const EmbedWork& w, uint32_t row, int32_t pos, int shift,
+                                           uint32_t span, int bits, int lane, int32_t* place) {
+  bool left = row < span;
+  uint64_t todo = __ballot(left);
+  for (int t = 0; todo; ++t) {
+    uint64_t same = todo;
+    bool mine = left;
+    if (t < kTries) {
+      const uint32_t one = __builtin_amdgcn_readlane(static_cast<int>(row), __builtin_ctzll(todo));
+      mine = left && row == one;
+      same = __ballot(mine);
+    } else {
+      for (int b = 0; b < bits; ++b) {
+        const int64_t bit = -static_cast<int64_t>((row >> b) & 1);
+        same &= ~(__ballot(bit) ^ bit);
+      }
+    }
+    if (mine) {
+      const int p = place[row], rank = lanes_before(same, lane);
+      w.pos[p + rank] = pos;
+      w.row[p + rank] = static_cast<int32_t>(row << shift) + static_cast<int>(blockIdx.x);
+      if ((same >> lane) == 1) place[row] = p + rank + 1;   // the row's last lane
+      left = false;
+    }
+    // the next lanes read what these wrote: in order in a wave, no wait needed
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    todo = t < kTries ? todo & ~same : 0;
   }
 }
 
@@ -223,42 +260,49 @@ __device__ __forceinline__ void zero_window(const SortArgs& a, int w, int lane) 
 // Workgroup g sorts the tokens of the rows r with r mod 2^shift = g (the
 // commonest ids are often neighbours: taken apart, no workgroup has many of
 // them).  It counts, over the whole batch, the tokens of earlier workgroups
-// (its first place in the order) and those of each row of its own, by wave;
-// then every wave places its share of the batch, in order, behind what earlier
-// rows and earlier waves have.  Every workgroup reads all ids (from L2), so
-// that one launch sorts and nothing waits for another workgroup.  Measured,
-// 32768 ids over 16032 rows: 21 us, 24 with neighbouring rows together.
+// (its first place in the order) and those of each row of its own, by wave,
+// and keeps these; then every wave places what it kept, in order, behind what
+// earlier rows and earlier waves have.  Every workgroup reads all ids (from
+// L2), so that one launch sorts and nothing waits for another workgroup.  What
+// bounds it: three chains of LDS accesses, one after the other.  Measured,
+// launch included, 32768 ids over 16032 rows, a 17th of them the same: 15 us
+// (7 for the loads, 4 to count, 5 to place), 20 where every 64 ids are looked
+// through again to be placed; all the same 26 (42); neighbouring rows together
+// cost 3 us more.
 template <typename Id>
 __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortArgs a) {
   __shared__ int32_t place[kSortWaves][kSortRows];
   __shared__ int32_t wave_sum[kSortWaves];
   __shared__ int32_t before_s;
   __shared__ uint8_t empty[kSortRows];
+  __shared__ Hits hits[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int own = blockIdx.x;
-  const int span = (a.rows - own + (1 << a.shift) - 1) >> a.shift;   // its rows
+  const uint32_t span = (a.rows - own + (1 << a.shift) - 1) >> a.shift;   // its rows
   for (int i = lane; i < span; i += 64) place[w][i] = 0;
   if (tid == 0) before_s = 0;
   __syncthreads();
   const int64_t share = (a.n + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
   const int64_t i0 = w * share, i1 = i0 + share < a.n ? i0 + share : a.n;
   constexpr int kStep = 64 * kGroup;
-  int before = 0;
-  Rows kept[kKept];
+  const uint32_t base = a.shift ? static_cast<uint32_t>(own) << (32 - a.shift) : 0;
+  int before = 0, found = 0;
+  {
+    Rows r[kAhead];
 #pragma unroll
-  for (int k = 0; k < kKept; ++k)
-    if (i0 + k * kStep < i1) load_rows<Id>(a, i0 + lane + k * kStep, i1, kept[k]);
-  if (a.main_grad && a.zero_all) zero_window(a, w, lane);
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kStep < i1) load_rows<Id>(a, i0 + k * kStep, i1, lane, base, r[k]);
+    if (a.main_grad && a.zero_all) zero_window(a, w, lane);
 #pragma unroll
-  for (int k = 0; k < kKept; ++k)
-    if (i0 + k * kStep < i1) count_rows(kept[k], a.shift, place[w], &before);
-  for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
-    Rows r;
-    load_rows<Id>(a, i + lane, i1, r);
-    count_rows(r, a.shift, place[w], &before);
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kStep < i1)
+        count_rows(r[k], i0 + k * kStep, base, span, lane, place[w], hits[w], &found, &before);
   }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) before += __shfl_xor(before, d);
+  for (int64_t i = i0 + kAhead * kStep; i < i1; i += kStep) {
+    Rows r;
+    load_rows<Id>(a, i, i1, lane, base, r);
+    count_rows(r, i, base, span, lane, place[w], hits[w], &found, &before);
+  }
   if (lane == 0) atomicAdd(&before_s, before);
   __syncthreads();
   // One thread a row: its count, then an exclusive scan over the rows.
@@ -285,14 +329,20 @@ __global__ __launch_bounds__(64 * kSortWaves) void embed_sort_kernel(const SortA
     }
   __syncthreads();
   const int bits = 32 - __builtin_clz(span);
+  if (found <= kHits) {
+    for (int h = 0; h < found; h += 64) {
+      const int k = min(h + lane, found - 1);
+      const uint32_t row = h + lane < found ? hits[w].row[k] : ~0u;
+      place_rows(a.w, row, hits[w].pos[k], a.shift, span, bits, lane, place[w]);
+    }
+  } else {   // more than it keeps: its share again
+    for (int64_t i = i0; i < i1; i += kStep) {
+      Rows r;
+      load_rows<Id>(a, i, i1, lane, base, r);
 #pragma unroll
-  for (int k = 0; k < kKept; ++k)
-    if (i0 + k * kStep < i1)
-      place_rows(a.w, kept[k], i0 + lane + k * kStep, a.shift, bits, lane, place[w]);
-  for (int64_t i = i0 + kKept * kStep; i < i1; i += kStep) {
-    Rows r;
-    load_rows<Id>(a, i + lane, i1, r);
-    place_rows(a.w, r, i + lane, a.shift, bits, lane, place[w]);
+      for (int g = 0; g < kGroup; ++g)
+        place_rows(a.w, r[g], static_cast<int32_t>(i) + 64 * g + lane, a.shift, span, bits, lane, place[w]);
+    }
   }
   if (!a.main_grad || a.zero_all) return;
   // Zeros to the rows without tokens, a wave to a row.
