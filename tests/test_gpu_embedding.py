@@ -79,6 +79,7 @@ GRAD = [  # vocab, dim, world, lead, n
     (1, 1, 1, 0, 1), (5, 3, 2, 1, 9), (3, 4, 1, 0, 200), (40, 64, 3, 5, 65), (2000, 8, 8, 0, 1000),
     (7, 1001, 2, 2, 40), (300, 1024, 4, 64, 513), (9, 2050, 2, 0, 100), (50000, 2, 1, 3, 3000),
     (1, 260, 1, 0, 700), (1100, 33, 1, 0, 4097), (262143, 1, 1, 0, 3000), (600001, 2, 1, 3, 4000),
+    (2, 5, 1, 0, 20001), (700, 3, 2, 1, 40001),
 ]
 
 
