@@ -678,8 +678,17 @@ __global__ __launch_bounds__(kThreads) void linear_join_kernel(const LinearArgs 
   const float* p = a.partial + (static_cast<int64_t>(it.piece0) + tile) * (kTileOut * kTileIn) +
                    (part * kThreads + tid) * 4;
   f32x4 sum = *as_global<f32x4>(p);
-#pragma unroll 8
-  for (int n = 1; n < it.pieces; ++n) sum += *as_global<f32x4>(p + n * step);
+  // Four pieces at a time are asked for before the first is added (seven of 36
+  // tiles: 1.4 us less than one after the other; eight at a time no better).
+  for (int n = 1; n < it.pieces; n += 4) {
+    f32x4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (n + u < it.pieces) x[u] = *as_global<f32x4>(p + (n + u) * step);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (n + u < it.pieces) sum += x[u];
+  }
   const int block = part / 4;
   put_sums<4>(it, Place<kInMajor>(it, it.whole + tile), a.first, uniform(tid >> 6), tid & 63,
               block / kInBlocks, block % kInBlocks, 4 * (part % 4), sum);
