@@ -444,10 +444,11 @@ struct Batch {
 // the caches (they are used once, and main_grad's lines would give way to
 // them), and the waves of a workgroup take neighbouring columns of the same
 // rows.  Measured, 32768 tokens of 4096 bf16 columns of which 27000 lie in a
-// window of 16032 rows, sort and join included: 110 us in the _first form, 138
-// with ordinary loads, 112 with workgroups of one wave; 123 us added, 126 with
-// ordinary loads, 125 with four positions a batch.  Every row twice, in no
-// order: 115 and 143; 148, 193 and 157 us.
+// window of 16032 rows, sort and join included: 107 us in the _first form, 135
+// with ordinary loads, 111 with workgroups of one wave; 117 us added, 119 with
+// ordinary loads or four positions a batch.  Every row twice, in no order: 113
+// us in the _first form (141 with ordinary loads), 146 added (189, and 154 with
+// four positions).
 constexpr int kSumWaves = 8;
 template <typename T, bool kFirst, bool kTiny>   // kTiny: rows of fewer than four columns
 __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs a) {
@@ -721,8 +722,9 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     while ((rows >> sa.shift) >= kSortRows) ++sa.shift;
     sa.main_grad = first ? table : nullptr;
     // Zeroing rows that the tokens will write again costs less than waiting
-    // for the ids' count, where there are few tokens: 333 tokens of 16753 rows
-    // of 1001 columns 13 us against 21, 8192 of 50257 of 768 26 against 30.
+    // for the ids' count, where there are few tokens.  The whole call: 333
+    // tokens of 16753 rows of 1001 columns 19.2 us against 20.8, 8192 of 50257
+    // rows of 768 46 both ways, 16384 of them 45.7 against 44.5 (back to back).
     sa.zero_all = n <= rows / 4;
     sa.dim = dim;
     sa.first = clip.first;
