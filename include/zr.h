@@ -486,7 +486,8 @@ zr_status zr_ring_ag_step(float* const* rank_bufs, int32_t n_ranks,
  *   tokens[n]   device array of ids.  An id outside [0, vocab) -- padding --
  *               gives a row of zeros.
  * The product is one fp32 operation, rounded once to dtype (scale 1: a copy
- * of the values; NaNs come out quiet).  out must not overlap parts. */
+ * of the values; NaNs come out quiet).  out must not overlap parts.
+ * ZR_ERR_UNSUPPORTED: dim of 2^24, or 2^26 pieces of a row's 4 kB, or more. */
 zr_status zr_embedding_lookup(const zr_plan* plan, int64_t param, int64_t dim,
                               const void* const* parts, zr_dtype dtype,
                               const void* tokens, zr_index token_type, int64_t n,
@@ -507,7 +508,9 @@ zr_status zr_ipg_embedding_workspace(const zr_plan* plan, int64_t param, int64_t
  * product and one add.  Tokens outside [0, vocab) or the window add nothing,
  * and their rows of dY are not read.  Elements of rows without tokens are not
  * touched; the _first form writes 0 to them.
- *   dy   device rows of dim elements of dy_dtype, one per token. */
+ *   dy   device rows of dim elements of dy_dtype, one per token.
+ * ZR_ERR_UNSUPPORTED: dim of 2^24, 2^28 tokens, or 2^30 rows in the window, or
+ * more. */
 zr_status zr_ipg_accumulate_embedding(const zr_plan* plan, int64_t param, int64_t dim,
                                       const void* tokens, zr_index token_type,
                                       int64_t n, float scale, const void* dy,
@@ -534,7 +537,9 @@ zr_status zr_ipg_accumulate_embedding_first(const zr_plan* plan, int64_t param, 
  * and the number of blocks); the codes behind the last column are 0. */
 zr_status zr_act_layout(int64_t cols, int64_t* code_pitch, int64_t* scale_pitch);
 
-/* zr_act_quantize -- the checkpoint of x.  codes must be 16-byte aligned. */
+/* zr_act_quantize -- the checkpoint of x.  codes must be 16-byte aligned.
+ * ZR_ERR_UNSUPPORTED, here and restoring: cols of 2^30, or 2^35 values in whole
+ * blocks, or more. */
 zr_status zr_act_quantize(const void* x, zr_dtype dtype, int64_t rows, int64_t cols,
                           int64_t x_stride, uint8_t* codes, uint8_t* scales,
                           hipStream_t stream);

@@ -92,6 +92,21 @@ def test_embedding_gradient_outside_the_window_needs_no_gpu():
                                            zr.ZR_FP32, 6, A, 0, 90, A, 1 << 20, None) == zr.ZR_OK
 
 
+def test_calls_of_more_threads_than_a_launch_holds():
+    """A launch holds fewer than 2^32 threads along an axis."""
+    plan = _plan()
+    parts = (ctypes.c_void_p * 2)(A, A)
+    for n in (1 << 27, 1 << 28):
+        assert lib.zr_embedding_lookup(plan.handle, 1, 6, parts, zr.ZR_BF16, A, zr.ZR_I32, n, 1.0,
+                                       A, 6, None) == zr.ZR_ERR_UNSUPPORTED
+    for fn in (lib.zr_ipg_accumulate_embedding_first, lib.zr_ipg_accumulate_embedding):
+        assert fn(plan.handle, 1, 6, A, zr.ZR_I64, 1 << 28, 1.0, A, zr.ZR_FP32, 6, A, 0, 90, A,
+                  1 << 60, None) == zr.ZR_ERR_UNSUPPORTED
+    rows = 1 << 30      # of 32 columns, four threads a row
+    assert lib.zr_act_quantize(A, zr.ZR_FP32, rows, 32, 32, A, A, None) == zr.ZR_ERR_UNSUPPORTED
+    assert lib.zr_act_dequantize(A, A, rows, 32, A, zr.ZR_BF16, 32, None) == zr.ZR_ERR_UNSUPPORTED
+
+
 def test_workspace_queries():
     plan = _plan()
     small = zr.zr_ipg_embedding_workspace(plan, 1, 6, 1, 0, 90)

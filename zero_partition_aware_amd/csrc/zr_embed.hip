@@ -662,7 +662,8 @@ zr_status check_table(const zr_plan* plan, int64_t param, int64_t dim, int64_t n
     return fail(ZR_ERR_INVALID, "dim must be >= 1 and divide the param's elements");
   if (dim >= (int64_t(1) << 24)) return fail(ZR_ERR_UNSUPPORTED, "dim of 2^24 or more");
   if (n < 0) return fail(ZR_ERR_INVALID, "n must be >= 0");
-  if (n >= (int64_t(1) << 31) - 64 * kSortWaves) return fail(ZR_ERR_UNSUPPORTED, "2^31 tokens or more");
+  // positions in 32 bits, and the sum's and the join's threads within a launch
+  if (n >= (int64_t(1) << 28)) return fail(ZR_ERR_UNSUPPORTED, "2^28 tokens or more");
   return ZR_OK;
 }
 
@@ -803,7 +804,8 @@ extern "C" zr_status zr_embedding_lookup(const zr_plan* plan, int64_t param, int
     const int64_t cols = dtype == ZR_BF16 ? kLookupCols<uint16_t> : kLookupCols<float>;
     a.chunks = static_cast<int32_t>(ceil_div(dim, cols));
     const int64_t grid = ceil_div(n * a.chunks, kLookupWaves);
-    if (grid > 0x7fffffff) return fail(ZR_ERR_UNSUPPORTED, "too many rows for one call");
+    if (!fits_launch(grid, 64 * kLookupWaves))
+      return fail(ZR_ERR_UNSUPPORTED, "too many rows for one call");
     if (dtype == ZR_BF16) lookup_kernel<uint16_t><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
     else lookup_kernel<float><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
     return launched("embedding lookup launch");

@@ -68,6 +68,9 @@ inline int64_t dtype_size(zr_dtype d) { return d == ZR_BF16 ? 2 : 4; }
 inline bool aligned_to(const void* p, int64_t s) { return reinterpret_cast<uintptr_t>(p) % s == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A launch holds fewer than 2^32 threads along an axis.
+inline bool fits_launch(int64_t blocks, int64_t threads) { return blocks <= 0xffffffffll / threads; }
+
 inline zr_status launched(const char* what) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return fail(ZR_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));

@@ -715,7 +715,8 @@ zr_status act_args(const void* x, zr_dtype dtype, int64_t rows, int64_t cols, in
   a->cols = cols;
   a->stride = stride;
   a->row_groups = static_cast<int32_t>(ceil_div(cols, kBlock) * (kBlock / 8));
-  if (rows > int64_t(0x7fffffff) * kActThreads / a->row_groups)
+  if (rows > (int64_t(1) << 32) / a->row_groups ||
+      !fits_launch(ceil_div(rows * a->row_groups, kActThreads), kActThreads))
     return fail(ZR_ERR_UNSUPPORTED, "too many elements for one call");
   a->total = rows * a->row_groups;
   *grid = ceil_div(a->total, kActThreads);
