@@ -484,7 +484,7 @@ zr_status zr_ring_ag_step(float* const* rank_bufs, int32_t n_ranks,
  *               and may not be null.  A gathered flat vector serves too:
  *               parts[k] = flat + k * P_g.
  *   tokens[n]   device array of ids.  An id outside [0, vocab) -- padding --
- *               gives a row of zeros.
+ *               gives a row of +0, whatever the scale.
  * The product is one fp32 operation, rounded once to dtype (scale 1: a copy
  * of the values; NaNs come out quiet).  out must not overlap parts.
  * ZR_ERR_UNSUPPORTED: dim of 2^24, or 2^26 pieces of a row's 4 kB, or more. */

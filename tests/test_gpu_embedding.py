@@ -204,3 +204,24 @@ def test_gradient_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(grad, want) and want.abs().max() > 1
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("dim", [1, 3, 7, 8, 130, 1001, 4101])
+@pytest.mark.parametrize("scale", [-1.0, -0.0, float("inf"), float("nan")])
+def test_lookup_of_padding_is_plus_zero_whatever_the_scale(scale, dim, bf16):
+    """An id outside the table reads nothing and is scaled by nothing: +0 in
+    rows of every width, beside rows of the table that the scale makes
+    negative, infinite or NaN."""
+    plan = _plan([5 * dim], 2)
+    P = zr.zr_plan_group_info(plan, 0)[2]
+    table = torch.rand(2 * P, device="cuda") + 0.5
+    table = table.bfloat16() if bf16 else table
+    ids = torch.tensor([-1, 3, 5, 0, 2 ** 62, 4, -2 ** 63], device="cuda")
+    out = torch.full((7, dim), 7.5, dtype=table.dtype, device="cuda")
+    zr.zr_embedding_lookup(plan, 0, dim, list(table.split(P)), ids, out, scale=scale)
+    bits = out.view(torch.int16 if bf16 else torch.int32).cpu()
+    assert (bits[[0, 2, 4, 6]] == 0).all()
+    want = (table[:5 * dim].view(5, dim)[[3, 0, 4]].float() * scale).to(table.dtype)
+    assert torch.equal(out[[1, 3, 5]].isnan(), want.isnan())
+    assert np.isnan(scale) or torch.equal(out[[1, 3, 5]], want)

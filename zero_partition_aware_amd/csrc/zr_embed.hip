@@ -55,7 +55,7 @@ __device__ __forceinline__ u32x4 scaled_vec(u32x4 w, float s) {
 // up to kLookupCols columns of one row, 16 bytes a lane and four loads in
 // flight; the partition that holds the piece is found once a wave, and only
 // a piece that a partition border cuts goes element by element.  An id
-// outside [0, vocab) gives a row of zeros and reads nothing.
+// outside [0, vocab) gives a row of +0 and reads nothing.
 template <typename T>
 __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupArgs a) {
   constexpr int V = kVec<T>, C = kLookupCols<T>;
@@ -88,7 +88,8 @@ __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupA
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t c = (u * 64 + lane) * V, d = c + V <= len ? c : len - V;
-        if (c < len) *as_global<u32x4_a2>(out + d) = scaled_vec<T>(x[u], a.scale);
+        // zeros are not scaled: -0 or NaN would come of a negative or infinite scale
+        if (c < len) *as_global<u32x4_a2>(out + d) = valid ? scaled_vec<T>(x[u], a.scale) : u32x4{0, 0, 0, 0};
       }
     } else if (lane < len) {
       out[lane] = valid ? scaled<T>(src[lane], a.scale) : T(0);
