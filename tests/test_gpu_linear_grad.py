@@ -211,3 +211,28 @@ def test_captured_and_replayed():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(grad, want) and want.abs().max() > 1
+
+
+def _bits(plan, items, length, first, before):
+    """main_grad after one call on `before`, with NaN behind the _first form."""
+    grad = torch.full((length,), float("nan"), device="cuda") if first else before.clone()
+    ws = workspace(zr.zr_ipg_linear_workspace(plan, items, 0, length))
+    (zr.zr_ipg_accumulate_linear_first if first else zr.zr_ipg_accumulate_linear)(plan, items, grad, ws)
+    return grad
+
+
+@pytest.mark.parametrize("in_major", [False, True])
+def test_first_gives_the_bits_of_the_plain_form_on_zeros(in_major):
+    """Also beside a layer without tokens, whose weights only the _first form
+    writes: the other layer's sums are cut into the same pieces."""
+    rng = np.random.default_rng(31)
+    plan = zr.zr_plan_buckets([512 * 640, 640 * 512], [0, 0], [(1, 1)], 1 << 40)
+    full, _, _ = _layer(rng, 512, 640, 2048)
+    none, _, _ = _layer(rng, 640, 512, 0)
+    items, n = [(0, *full, in_major), (1, *none, in_major)], 2 * 512 * 640
+    first = _bits(plan, items, n, True, None)
+    added = _bits(plan, items, n, False, torch.zeros(n, device="cuda"))
+    assert torch.equal(first, added) and (first[n // 2:] == 0).all()
+    # nor does the layer without tokens matter to the other one's sums
+    alone = _bits(plan, items[:1], n, True, None)
+    assert torch.equal(first[:n // 2], alone[:n // 2]) and alone[n // 2:].isnan().all()

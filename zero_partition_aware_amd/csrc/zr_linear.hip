@@ -836,16 +836,23 @@ zr_status plan_launch(const Item* items, size_t n, bool first, Launch* out) {
   a = LinearArgs{};
   a.first = first;
   a.n = static_cast<int32_t>(n);
-  int64_t tiles = 0;
-  for (size_t k = 0; k < n; ++k) tiles += int64_t(items[k].out_tiles) * items[k].in_tiles;
-  if (tiles > 0x3fffffff) return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
-  const int64_t rest = tiles % kCus;   // tiles of the last round
+  int64_t all = 0, tiles = 0;   // tiles, and those with tokens
+  for (size_t k = 0; k < n; ++k) {
+    const int64_t count = int64_t(items[k].out_tiles) * items[k].in_tiles;
+    all += count;
+    if (items[k].tokens > 0) tiles += count;
+  }
+  if (all > 0x3fffffff) return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
+  // Tiles of the last round.  Those without tokens, which come last and which
+  // only the first micro-batch's form writes, do not count: the other tiles'
+  // sums are cut into the same pieces in both forms.
+  const int64_t rest = tiles % kCus;
   int64_t before = 0, whole = 0, pieces = 0;
   for (size_t k = 0; k < n; ++k) {
     Item& it = a.item[k] = items[k];
     const int64_t count = int64_t(it.out_tiles) * it.in_tiles;
     const int64_t steps = ceil_div(it.tokens, kDepth);
-    it.pieces = rest > 0 ? pieces_of(steps, rest) : 1;
+    it.pieces = rest > 0 ? pieces_of(steps, rest) : 1;   // one without tokens
     it.whole = static_cast<int32_t>(
         it.pieces > 1 ? std::min(count, std::max<int64_t>(0, tiles - rest - before)) : count);
     it.whole0 = static_cast<int32_t>(whole);
