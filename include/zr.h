@@ -470,8 +470,9 @@ zr_status zr_ring_ag_step(float* const* rank_bufs, int32_t n_ranks,
  *     zr_ipg_accumulate, and a `_first` form writes what the plain form
  *     gives on a window zeroed at the start of the step, to every element of
  *     the parameter in the window, without reading it.
- *   - Sums are fp32 in an order that depends on the sizes alone: the same
- *     inputs give the same bits on every run.
+ *   - Sums are fp32 in an order fixed by the sizes, the window and the ids,
+ *     not by addresses, alignment or the form: the same inputs give the same
+ *     bits on every run and wherever they lie.
  */
 
 /* zr_embedding_lookup -- rows of a [vocab, dim] table that lies in the ranks'
@@ -568,7 +569,8 @@ typedef struct {
 } zr_linear_grad;
 
 /* Workspace bytes of zr_ipg_accumulate_linear and its _first form for these
- * items (device pointers are checked, not read). */
+ * items.  Device pointers are checked, not read, and do not matter to the
+ * bytes: the items of the call may lie elsewhere. */
 zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linear_grad* items,
                                   int64_t n, int64_t window_base, int64_t window_len,
                                   int64_t* bytes);

@@ -236,3 +236,28 @@ def test_first_gives_the_bits_of_the_plain_form_on_zeros(in_major):
     # nor does the layer without tokens matter to the other one's sums
     alone = _bits(plan, items[:1], n, True, None)
     assert torch.equal(first[:n // 2], alone[:n // 2]) and alone[n // 2:].isnan().all()
+
+
+@pytest.mark.parametrize("in_major", [False, True])
+def test_bits_do_not_depend_on_where_dy_lies(in_major):
+    """Layers' rows of dY on 16 bytes, off them, or some on and some off: the
+    sums have the same order."""
+    rng = np.random.default_rng(32)
+    shapes = [(512, 640, 2048), (264, 512, 3001), (96, 300, 700)]
+    plan = zr.zr_plan_buckets([a * b for a, b, _ in shapes], [0] * 3, [(1, 1)], 1 << 40)
+    layers = [_layer(rng, *s)[0] for s in shapes]
+    n = sum(a * b for a, b, _ in shapes)
+
+    def off(dy):
+        """The same rows, each 2 bytes off 16."""
+        wide = torch.empty(dy.shape[0] * dy.shape[1] + 1, dtype=dy.dtype, device="cuda")[1:].view(dy.shape)
+        return wide.copy_(dy)
+
+    want, need = None, None
+    for places in ((0, 0, 0), (1, 1, 1), (1, 0, 0), (0, 1, 0), (1, 0, 1)):
+        items = [(k, off(dy) if p else dy, c, s, in_major)
+                 for k, (p, (dy, c, s)) in enumerate(zip(places, layers))]
+        got = _bits(plan, items, n, True, None)
+        size = zr.zr_ipg_linear_workspace(plan, items, 0, n)
+        want, need = (got, size) if want is None else (want, need)
+        assert torch.equal(got, want) and size == need, places

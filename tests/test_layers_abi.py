@@ -174,6 +174,26 @@ def test_linear_gradient_refusals(first, items, call, words):
     assert st in (zr.ZR_ERR_INVALID, zr.ZR_ERR_UNSUPPORTED) and words in zr.zr_last_error()
 
 
+def test_linear_workspace_depends_on_sizes_alone():
+    """Neither on where dY lies nor on layers without tokens."""
+    plan = zr.zr_plan_buckets([512 * 640, 640 * 512], [0, 0], [(1, 1)], 1 << 40)
+
+    def need(*changes):
+        v = [dict(param=0, n_out=512, n_in=640, dy_stride=512, tokens=2048),
+             dict(param=1, n_out=640, n_in=512, dy_stride=640, tokens=2048)][:len(changes)]
+        arr = (zr.zr_linear_grad * len(v))(*[_item(**{**a, **c}) for a, c in zip(v, changes)])
+        out = ctypes.c_int64()
+        assert lib.zr_ipg_linear_workspace(plan.handle, arr, len(v), 0, 2 * 512 * 640,
+                                           ctypes.byref(out)) == zr.ZR_OK
+        return out.value
+
+    both = need({}, {})
+    assert both > 0
+    for dy, stride in ((A + 2, 640), (A, 641), (A + 14, 648)):
+        assert need({}, dict(dy=dy, dy_stride=stride)) == both
+    assert need({}, dict(tokens=0, dy=None, codes=None, scales=None)) == need({}) > 0
+
+
 def test_linear_gradient_of_nothing_needs_no_gpu():
     plan = _plan()
     arr = (zr.zr_linear_grad * 1)(_item(tokens=0, dy=None, codes=None, scales=None))

@@ -521,7 +521,7 @@ __device__ __forceinline__ void whole_tiles(const Loader& in, const Reader& read
 
 // The tile's sums over the tokens [t0, t1), added to the MFMAs' accumulators:
 // a block's rows are the weight's stored rows, its columns a row's elements.
-template <bool kInMajor, bool kDirect>
+template <bool kInMajor>
 __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0, int64_t t0,
                                           int64_t t1, char* lds, Acc& acc) {
   const int tid = threadIdx.x;
@@ -532,7 +532,8 @@ __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0
   const int64_t end = it.out % 8 && t1 == it.tokens ? t1 - 1 : t1;
   const int steps = it.out < 8 || end < t0 ? 0 : static_cast<int>((end - t0) / kDepth);
   if (steps > 0) {
-    whole_tiles<kInMajor, kDirect>(in, reader, t0, steps, lds, acc, tid);
+    if (it.direct) whole_tiles<kInMajor, true>(in, reader, t0, steps, lds, acc, tid);
+    else whole_tiles<kInMajor, false>(in, reader, t0, steps, lds, acc, tid);
     t0 += static_cast<int64_t>(steps) * kDepth;
   }
   for (; t0 < t1; t0 += kDepth) {
@@ -616,7 +617,7 @@ __device__ __forceinline__ void put_sums(const Item& it, const Place<kInMajor>& 
   }
 }
 
-template <bool kInMajor, bool kDirect>
+template <bool kInMajor>
 __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a) {
   __shared__ __align__(16) char lds[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
@@ -648,7 +649,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a)
   const Item& it = a.item[k];
   const Place<kInMajor> at(it, tile);
   Acc acc = {};
-  tile_sums<kInMajor, kDirect>(it, at.o0, at.i0, t0, t1, lds, acc);
+  tile_sums<kInMajor>(it, at.o0, at.i0, t0, t1, lds, acc);
 #pragma unroll
   for (int i = 0; i < kOutBlocks; ++i)
 #pragma unroll
@@ -782,11 +783,10 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
     it.out_tiles = static_cast<int32_t>(it.in_major ? all : r1 - r0);
     out->push_back(it);
   }
-  // One kernel's items together, and tiles with most tokens first: the last to
-  // start are the shortest.
+  // One storage order's items together, and tiles with most tokens first: the
+  // last to start are the shortest.
   std::stable_sort(out->begin(), out->end(), [](const Item& a, const Item& b) {
-    return std::make_tuple(a.in_major, a.direct, b.tokens) <
-           std::make_tuple(b.in_major, b.direct, a.tokens);
+    return std::make_tuple(a.in_major, b.tokens) < std::make_tuple(b.in_major, a.tokens);
   });
   std::sort(seen.begin(), seen.end());
   if (std::adjacent_find(seen.begin(), seen.end()) != seen.end())
@@ -794,13 +794,14 @@ zr_status linear_items(const zr_plan* plan, const zr_linear_grad* items, int64_t
   return ZR_OK;
 }
 
-// The items that one launch takes from the k-th on: of one kernel, and at most
-// kMaxItems.
+// The items that one launch takes from the k-th on: of one storage order, and at
+// most kMaxItems.  Where rows of dY lie does not matter, or it would show in how
+// the sums are cut; and two kinds in one launch fill the chip together (768 x 768
+// and 2304 x 768 weights over 8192 tokens, one of each kind: 57 us, 76 in a
+// launch each).
 size_t launch_end(const std::vector<Item>& items, size_t k) {
   size_t e = k + 1;
-  while (e < items.size() && e < k + kMaxItems && items[e].in_major == items[k].in_major &&
-         items[e].direct == items[k].direct)
-    ++e;
+  while (e < items.size() && e < k + kMaxItems && items[e].in_major == items[k].in_major) ++e;
   return e;
 }
 
@@ -889,9 +890,8 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
       l.a.partial = static_cast<float*>(workspace);
     }
     for (const Launch& l : launches) {
-      const bool in_major = l.a.item[0].in_major, direct = l.a.item[0].direct;
-      auto* kernel = in_major ? (direct ? linear_kernel<true, true> : linear_kernel<true, false>)
-                              : (direct ? linear_kernel<false, true> : linear_kernel<false, false>);
+      const bool in_major = l.a.item[0].in_major;
+      auto* kernel = in_major ? linear_kernel<true> : linear_kernel<false>;
       kernel<<<l.grid, kThreads, 0, stream>>>(l.a);
       st = launched("linear gradient launch");
       if (st != ZR_OK) return st;
@@ -956,18 +956,16 @@ extern "C" zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linea
   return guarded([&]() -> zr_status {
     if (!bytes) return fail(ZR_ERR_INVALID, "null output pointer");
     *bytes = 0;
-    for (const bool first : {false, true}) {   // items without tokens are only in one
-      std::vector<Item> todo;
-      zr_status st = linear_items(plan, items, n, reinterpret_cast<const float*>(4), window_base,
-                                  window_len, first, &todo);
+    std::vector<Item> todo;
+    zr_status st = linear_items(plan, items, n, reinterpret_cast<const float*>(4), window_base,
+                                window_len, true, &todo);
+    if (st != ZR_OK) return st;
+    for (size_t k = 0, e; k < todo.size(); k = e) {
+      e = launch_end(todo, k);
+      Launch l;
+      st = plan_launch(&todo[k], e - k, true, &l);
       if (st != ZR_OK) return st;
-      for (size_t k = 0, e; k < todo.size(); k = e) {
-        e = launch_end(todo, k);
-        Launch l;
-        st = plan_launch(&todo[k], e - k, first, &l);
-        if (st != ZR_OK) return st;
-        *bytes = std::max(*bytes, l.bytes);
-      }
+      *bytes = std::max(*bytes, l.bytes);
     }
     return ZR_OK;
   });
