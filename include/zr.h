@@ -585,7 +585,8 @@ zr_status zr_ipg_linear_workspace(const zr_plan* plan, const zr_linear_grad* ite
  * host array; all params must be in one group and none twice; an item
  * without tokens (an expert nobody was routed to) adds nothing.  dY and X
  * should be finite: a NaN or infinity spreads as in the formula.
- * ZR_ERR_UNSUPPORTED: n_in or dy_stride of 2^24, or tokens of 2^31, or more. */
+ * ZR_ERR_UNSUPPORTED: n_in or dy_stride of 2^24, or tokens of 2^31, or more;
+ * weights that meet the window in 2^23 tiles of 256 x 256, less 256, or more. */
 zr_status zr_ipg_accumulate_linear(const zr_plan* plan, const zr_linear_grad* items,
                                    int64_t n, float* main_grad, int64_t window_base,
                                    int64_t window_len, void* workspace,

@@ -174,6 +174,23 @@ def test_linear_gradient_refusals(first, items, call, words):
     assert st in (zr.ZR_ERR_INVALID, zr.ZR_ERR_UNSUPPORTED) and words in zr.zr_last_error()
 
 
+def test_linear_gradient_of_more_threads_than_a_launch_holds():
+    """512 a tile of 256 x 256 weights: 2^23 tiles are refused, of one weight or
+    of several in a launch."""
+    for numels, shapes in (([1 << 40], [(1 << 20, 1 << 20)]),
+                           ([1 << 38] * 2, [(1 << 19, 1 << 19)] * 2)):
+        plan = zr.zr_plan_buckets(numels, [0] * len(numels), [(1, 1)], 1 << 50)
+        arr = (zr.zr_linear_grad * len(shapes))(*[
+            _item(param=k, n_out=o, n_in=i, dy_stride=o) for k, (o, i) in enumerate(shapes)])
+        for fn in (lib.zr_ipg_accumulate_linear_first, lib.zr_ipg_accumulate_linear):
+            assert fn(plan.handle, arr, len(shapes), A, 0, sum(numels), A, 1 << 40,
+                      None) == zr.ZR_ERR_UNSUPPORTED
+            assert "too large" in zr.zr_last_error()
+        out = ctypes.c_int64()
+        assert lib.zr_ipg_linear_workspace(plan.handle, arr, len(shapes), 0, sum(numels),
+                                           ctypes.byref(out)) == zr.ZR_ERR_UNSUPPORTED
+
+
 def test_linear_workspace_depends_on_sizes_alone():
     """Neither on where dY lies nor on layers without tokens."""
     plan = zr.zr_plan_buckets([512 * 640, 640 * 512], [0, 0], [(1, 1)], 1 << 40)

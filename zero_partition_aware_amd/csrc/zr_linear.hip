@@ -843,7 +843,9 @@ zr_status plan_launch(const Item* items, size_t n, bool first, Launch* out) {
     all += count;
     if (items[k].tokens > 0) tiles += count;
   }
-  if (all > 0x3fffffff) return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
+  // a workgroup each, and no more pieces than CUs
+  if (!fits_launch(all + kCus, kThreads))
+    return fail(ZR_ERR_UNSUPPORTED, "weights too large for one call");
   // Tiles of the last round.  Those without tokens, which come last and which
   // only the first micro-batch's form writes, do not count: the other tiles'
   // sums are cut into the same pieces in both forms.
