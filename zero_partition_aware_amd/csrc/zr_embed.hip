@@ -83,13 +83,13 @@ __global__ __launch_bounds__(64 * kLookupWaves) void lookup_kernel(const LookupA
       for (int u = 0; u < 4; ++u) {
         const int64_t c = (u * 64 + lane) * V, d = c + V <= len ? c : len - V;
         x[u] = u32x4{0, 0, 0, 0};
-        if (valid && c < len) x[u] = *as_global<u32x4_a2>(src + d);
+        if (valid && c < len) x[u] = load_at<u32x4, sizeof(T)>(src + d);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t c = (u * 64 + lane) * V, d = c + V <= len ? c : len - V;
         // zeros are not scaled: -0 or NaN would come of a negative or infinite scale
-        if (c < len) *as_global<u32x4_a2>(out + d) = valid ? scaled_vec<T>(x[u], a.scale) : u32x4{0, 0, 0, 0};
+        if (c < len) store_at<sizeof(T)>(out + d, valid ? scaled_vec<T>(x[u], a.scale) : u32x4{0, 0, 0, 0});
       }
     } else if (lane < len) {
       out[lane] = valid ? scaled<T>(src[lane], a.scale) : T(0);
@@ -376,8 +376,8 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, 
   const int64_t e = (a.row0 + row) * a.dim + col;
   s *= a.scale;
   if (col + 4 <= a.dim && e >= a.first && e + 4 <= a.last) {
-    auto* p = as_global<f32x4_a4>(a.main_grad + e);
-    *p = (kFirst ? f32x4{0, 0, 0, 0} : f32x4(*p)) + s;
+    float* p = a.main_grad + e;
+    store_at<4>(p, (kFirst ? f32x4{0, 0, 0, 0} : load_at<f32x4, 4>(p)) + s);
   } else {
     f32x4 old{0, 0, 0, 0};
 #pragma unroll
@@ -391,10 +391,10 @@ __device__ __forceinline__ void put_row(const SumArgs& a, int64_t row, int col, 
 
 // Four columns of a row of dY, used once.
 __device__ __forceinline__ u32x2 load4(const uint16_t* p) {
-  return __builtin_nontemporal_load(as_global<u32x2_a2>(p));
+  return load_once_at<u32x2, 2>(p);
 }
 __device__ __forceinline__ f32x4 load4(const float* p) {
-  return __builtin_nontemporal_load(as_global<f32x4_a4>(p));
+  return load_once_at<f32x4, 4>(p);
 }
 __device__ __forceinline__ u32x2 load_some(const uint16_t* p, int n) {
   u32x2 x{0, 0};
@@ -494,7 +494,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
         if (p + k < n && ((ends & quick) >> i & 1)) {
           const float* row = a.main_grad + (a.row0 + __builtin_amdgcn_readlane(my_row, i)) * a.dim;
 #pragma unroll
-          for (int u = 0; u < kSumVecs; ++u) b.old[k][u] = *as_global<f32x4_a4>(row + c_in[u]);
+          for (int u = 0; u < kSumVecs; ++u) b.old[k][u] = load_at<f32x4, 4>(row + c_in[u]);
         }
       }
     }
@@ -523,7 +523,7 @@ __global__ __launch_bounds__(64 * kSumWaves) void embed_sum_kernel(const SumArgs
                 const f32x4 o = kFirst ? f32x4{0, 0, 0, 0} : b.old[kFirst ? 0 : k][u];
                 const f32x4 v = (cut ? from(o, (c - c_in[u]) & 3) : o) + s[u] * a.scale;
                 if (c + 4 <= a.dim) {
-                  *as_global<f32x4_a4>(p) = v;
+                  store_at<4>(p, v);
                 } else {
 #pragma unroll
                   for (int j = 0; j < 3; ++j)
@@ -679,8 +679,8 @@ template <typename T, bool kFirst>
 void launch_sum(const SumArgs& a, int64_t pieces, hipStream_t stream) {
   const int64_t waves = ceil_div(a.dim, kSumCols), here = std::min<int64_t>(waves, kSumWaves);
   const dim3 grid(pieces, ceil_div(waves, here));
-  if (a.dim < 4) embed_sum_kernel<T, kFirst, true><<<grid, 64 * here, 0, stream>>>(a);
-  else embed_sum_kernel<T, kFirst, false><<<grid, 64 * here, 0, stream>>>(a);
+  if (a.dim < 4) ZR_LAUNCH(grid, 64 * here, stream, a, embed_sum_kernel<T, kFirst, true>);
+  else ZR_LAUNCH(grid, 64 * here, stream, a, embed_sum_kernel<T, kFirst, false>);
 }
 
 zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const void* tokens,
@@ -732,7 +732,7 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     sa.first = clip.first;
     sa.last = clip.last;
     auto* sort = token_type == ZR_I64 ? embed_sort_kernel<int64_t> : embed_sort_kernel<int32_t>;
-    sort<<<1 << sa.shift, 64 * kSortWaves, 0, stream>>>(sa);
+    ZR_LAUNCH(1 << sa.shift, 64 * kSortWaves, stream, sa, sort);
     st = launched("embedding sort launch");
     if (st != ZR_OK || n == 0) return st;
     SumArgs a{};
@@ -757,8 +757,8 @@ zr_status run_embedding(const zr_plan* plan, int64_t param, int64_t dim, const v
     st = launched("embedding sum launch");
     if (st != ZR_OK || s.pieces == 1) return st;
     const dim3 grid(s.pieces - 1, ceil_div(dim, kJoinCols));
-    if (first) embed_join_kernel<true><<<grid, 64 * kJoinWaves, 0, stream>>>(a);
-    else embed_join_kernel<false><<<grid, 64 * kJoinWaves, 0, stream>>>(a);
+    if (first) ZR_LAUNCH(grid, 64 * kJoinWaves, stream, a, embed_join_kernel<true>);
+    else ZR_LAUNCH(grid, 64 * kJoinWaves, stream, a, embed_join_kernel<false>);
     return launched("embedding join launch");
   });
 }
@@ -807,8 +807,8 @@ extern "C" zr_status zr_embedding_lookup(const zr_plan* plan, int64_t param, int
     const int64_t grid = ceil_div(n * a.chunks, kLookupWaves);
     if (!fits_launch(grid, 64 * kLookupWaves))
       return fail(ZR_ERR_UNSUPPORTED, "too many rows for one call");
-    if (dtype == ZR_BF16) lookup_kernel<uint16_t><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
-    else lookup_kernel<float><<<grid, 64 * kLookupWaves, 0, stream>>>(a);
+    if (dtype == ZR_BF16) ZR_LAUNCH(grid, 64 * kLookupWaves, stream, a, lookup_kernel<uint16_t>);
+    else ZR_LAUNCH(grid, 64 * kLookupWaves, stream, a, lookup_kernel<float>);
     return launched("embedding lookup launch");
   });
 }

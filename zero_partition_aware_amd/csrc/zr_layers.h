@@ -17,15 +17,13 @@ using u32x4 = uint32_t __attribute__((ext_vector_type(4)));
 using f32x4 = float __attribute__((ext_vector_type(4)));
 using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 
-// Vector accesses that assume no more than the elements' own alignment: the
-// GPU's global loads and stores take any address, so rows of an odd number
-// of elements need no path of their own.
-typedef u32x2 u32x2_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a2 __attribute__((aligned(2)));
-typedef u32x4 u32x4_a4 __attribute__((aligned(4)));
-typedef f32x4 f32x4_a4 __attribute__((aligned(4)));
-
+// Address spaces, and the launch of kernel __VA_ARGS__ over `grid` workgroups of
+// `block` lanes.  A CPU build of these files, for bounds checking, has its own.
+#ifndef ZR_GLOBAL_AS
 #define ZR_GLOBAL_AS __attribute__((address_space(1)))
+#define ZR_LDS_AS __attribute__((address_space(3)))
+#define ZR_LAUNCH(grid, block, stream, args, ...) __VA_ARGS__<<<(grid), (block), 0, (stream)>>>(args)
+#endif
 
 // Global-memory pointers (rather than generic ones): no flat instructions.
 template <typename T>
@@ -35,6 +33,26 @@ __device__ __forceinline__ const ZR_GLOBAL_AS T* as_global(const void* p) {
 template <typename T>
 __device__ __forceinline__ ZR_GLOBAL_AS T* as_global(void* p) {
   return (ZR_GLOBAL_AS T*)p;
+}
+
+// Vector accesses that assume no more than kAlign bytes' alignment, the
+// elements' own: the GPU's global loads and stores take any address, so rows of
+// an odd number of elements need no path of their own.  (An aligned type would
+// lose its alignment as a template argument.)
+template <typename V, int kAlign>
+__device__ __forceinline__ V load_at(const void* p) {
+  typedef V __attribute__((aligned(kAlign))) U;
+  return *(const ZR_GLOBAL_AS U*)p;
+}
+template <typename V, int kAlign>
+__device__ __forceinline__ V load_once_at(const void* p) {   // past the caches
+  typedef V __attribute__((aligned(kAlign))) U;
+  return __builtin_nontemporal_load((const ZR_GLOBAL_AS U*)p);
+}
+template <int kAlign, typename V>
+__device__ __forceinline__ void store_at(void* p, V v) {
+  typedef V __attribute__((aligned(kAlign))) U;
+  *(ZR_GLOBAL_AS U*)p = v;
 }
 
 __device__ __forceinline__ float bits_float(uint32_t u) { return __builtin_bit_cast(float, u); }

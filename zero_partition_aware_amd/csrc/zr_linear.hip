@@ -47,7 +47,7 @@ __device__ __forceinline__ bool act_group(const ActArgs& a, int64_t* row, int* c
 
 __device__ __forceinline__ void load8(const uint16_t* p, int left, float* x) {
   if (left >= 8) {
-    const u32x4 w = *as_global<u32x4_a2>(p);
+    const u32x4 w = load_at<u32x4, 2>(p);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(w[i]), x[2 * i + 1] = bf16_hi(w[i]);
   } else {
@@ -57,7 +57,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, int left, float* x) {
 }
 __device__ __forceinline__ void load8(const float* p, int left, float* x) {
   if (left >= 8) {
-    const f32x4 u = *as_global<f32x4_a4>(p), v = *as_global<f32x4_a4>(p + 4);
+    const f32x4 u = load_at<f32x4, 4>(p), v = load_at<f32x4, 4>(p + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = u[i], x[4 + i] = v[i];
   } else {
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
     if (left >= 8) {
-      *as_global<u32x4_a2>(out) = v;
+      store_at<2>(out, v);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -147,8 +147,8 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
     }
   } else {
     if (left >= 8) {
-      *as_global<f32x4_a4>(out) = f32x4{x[0], x[1], x[2], x[3]};
-      *as_global<f32x4_a4>(out + 4) = f32x4{x[4], x[5], x[6], x[7]};
+      store_at<4>(out, f32x4{x[0], x[1], x[2], x[3]});
+      store_at<4>(out + 4, f32x4{x[4], x[5], x[6], x[7]});
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -231,7 +231,7 @@ __device__ __forceinline__ int staged(int k, int u) {
 // 16-token, 32-column block whose place `at` the lane has.
 template <int C>
 __device__ __forceinline__ bf16x8 read_columns(const char* lds, int at) {
-  using lds_s16x4 = __attribute__((address_space(3))) s16x4;
+  using lds_s16x4 = ZR_LDS_AS s16x4;
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at + 4 * (C * 2)));
   return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -291,7 +291,7 @@ struct Loader {
     const char* d = dy + t * dy_step;
 #pragma unroll
     for (int j = kJ0; j < kJ1; ++j)
-      s.v[j] = *as_global<u32x4_a2>(d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step))));
+      s.v[j] = load_at<u32x4, 2>(d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step))));
   }
   // dY straight into LDS, where a wave's 64 units lie one after the other: the
   // exchange is made by what each lane reads.  Units on 16 bytes.
@@ -301,7 +301,7 @@ struct Loader {
     for (int j = 0; j < kOutLoads; ++j)
       __builtin_amdgcn_global_load_lds(
           (const ZR_GLOBAL_AS void*)(d + (direct_off + j * (kOutRows * static_cast<uint32_t>(dy_step)))),
-          (__attribute__((address_space(3))) void*)(lds + (w * (64 / kOutUnits) + j * kOutRows) * (kTileOut * 2)),
+          (ZR_LDS_AS void*)(lds + (w * (64 / kOutUnits) + j * kOutRows) * (kTileOut * 2)),
           16, 0, 0);
   }
   __device__ __forceinline__ void load_x(StagedIn& s, int64_t t) const {
@@ -324,7 +324,7 @@ struct Loader {
       if (dy_row + j * kOutRows < tokens) {
         const char* p = d + (dy_off + j * (kOutRows * static_cast<uint32_t>(dy_step)));
         if (dy_left >= 8) {
-          o.v[j] = *as_global<u32x4_a2>(p);
+          o.v[j] = load_at<u32x4, 2>(p);
         } else {
 #pragma unroll
           for (int e = 0; e < 7; ++e)
@@ -894,12 +894,12 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
     for (const Launch& l : launches) {
       const bool in_major = l.a.item[0].in_major;
       auto* kernel = in_major ? linear_kernel<true> : linear_kernel<false>;
-      kernel<<<l.grid, kThreads, 0, stream>>>(l.a);
+      ZR_LAUNCH(l.grid, kThreads, stream, l.a, kernel);
       st = launched("linear gradient launch");
       if (st != ZR_OK) return st;
       if (l.cut == 0) continue;
       auto* join = in_major ? linear_join_kernel<true> : linear_join_kernel<false>;
-      join<<<l.cut * kJoins, kThreads, 0, stream>>>(l.a);
+      ZR_LAUNCH(l.cut * kJoins, kThreads, stream, l.a, join);
       st = launched("linear gradient join launch");
       if (st != ZR_OK) return st;
     }
@@ -930,8 +930,8 @@ extern "C" zr_status zr_act_quantize(const void* x, zr_dtype dtype, int64_t rows
     if (st != ZR_OK || rows == 0) return st;
     a.x = x;
     a.out = codes;
-    if (dtype == ZR_BF16) act_quantize_kernel<uint16_t><<<grid, kActThreads, 0, stream>>>(a);
-    else act_quantize_kernel<float><<<grid, kActThreads, 0, stream>>>(a);
+    if (dtype == ZR_BF16) ZR_LAUNCH(grid, kActThreads, stream, a, act_quantize_kernel<uint16_t>);
+    else ZR_LAUNCH(grid, kActThreads, stream, a, act_quantize_kernel<float>);
     return launched("activation quantize launch");
   });
 }
@@ -946,8 +946,8 @@ extern "C" zr_status zr_act_dequantize(const uint8_t* codes, const uint8_t* scal
     if (st != ZR_OK || rows == 0) return st;
     a.x = codes;
     a.out = out;
-    if (dtype == ZR_BF16) act_dequantize_kernel<uint16_t><<<grid, kActThreads, 0, stream>>>(a);
-    else act_dequantize_kernel<float><<<grid, kActThreads, 0, stream>>>(a);
+    if (dtype == ZR_BF16) ZR_LAUNCH(grid, kActThreads, stream, a, act_dequantize_kernel<uint16_t>);
+    else ZR_LAUNCH(grid, kActThreads, stream, a, act_dequantize_kernel<float>);
     return launched("activation dequantize launch");
   });
 }
