@@ -225,3 +225,45 @@ def test_lookup_of_padding_is_plus_zero_whatever_the_scale(scale, dim, bf16):
     want = (table[:5 * dim].view(5, dim)[[3, 0, 4]].float() * scale).to(table.dtype)
     assert torch.equal(out[[1, 3, 5]].isnan(), want.isnan())
     assert np.isnan(scale) or torch.equal(out[[1, 3, 5]], want)
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("vocab,dim,n", [(7, 4097, 40), (40, 4100, 300), (5, 8192, 200), (3, 8203, 70),
+                                         (2, 20001, 30)])
+def test_gradient_of_rows_wider_than_a_workgroup(vocab, dim, n, bf16, first):
+    """Several workgroups share a row's columns; nothing is written behind the
+    workspace."""
+    rng = np.random.default_rng(vocab + dim)
+    t = _ids(rng, vocab, n)
+    dy = rng.integers(-50, 51, (n, dim)).astype(np.float32)
+    dy[(t < 0) | (t >= vocab)] = np.nan
+    for part in (None, 0, 1):
+        _grad_case(vocab, dim, 2, 3, n, bf16, first, part, t, dy, 2.0, pad=part == 0, exact=True)
+    plan = _plan([vocab * dim], 1)
+    size = zr.zr_ipg_embedding_workspace(plan, 0, dim, n, 0, vocab * dim)
+    ws = torch.full((size + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    rows_, _ = rows(dy, bf16)
+    zr.zr_ipg_accumulate_embedding_first(plan, 0, dim, torch.from_numpy(t).cuda(), rows_,
+                                         torch.empty(vocab * dim, device="cuda"), ws[:size])
+    assert (ws[size:] == 0xA5).all()
+
+
+@pytest.mark.parametrize("vocab,dim,n", [(300, 96, 5000), (9, 1001, 700), (5000, 130, 900), (4, 3, 3000)])
+def test_gradient_bits_do_not_depend_on_the_form_or_on_where_dy_lies(vocab, dim, n):
+    rng = np.random.default_rng(n)
+    plan, t = _plan([vocab * dim], 1), torch.from_numpy(_ids(rng, vocab, n)).cuda()
+    values = rng.standard_normal((n, dim)).astype(np.float32)
+    values[::3] *= -0.0
+    ws = workspace(zr.zr_ipg_embedding_workspace(plan, 0, dim, n, 0, vocab * dim))
+    for bf16 in (False, True):
+        got = []
+        for pad, offset in ((0, 0), (0, 1), (5, 3)):
+            dy, _ = rows(values, bf16, pad, offset)
+            grad = torch.full((vocab * dim,), float("nan"), device="cuda")
+            zr.zr_ipg_accumulate_embedding_first(plan, 0, dim, t, dy, grad, ws, scale=-1.3)
+            added = torch.zeros(vocab * dim, device="cuda")
+            zr.zr_ipg_accumulate_embedding(plan, 0, dim, t, dy, added, ws, scale=-1.3)
+            got += [host_f32(grad), host_f32(added)]
+        for other in got[1:]:
+            assert_bits_equal(other, got[0], "sums")

@@ -261,3 +261,36 @@ def test_bits_do_not_depend_on_where_dy_lies(in_major):
         size = zr.zr_ipg_linear_workspace(plan, items, 0, n)
         want, need = (got, size) if want is None else (want, need)
         assert torch.equal(got, want) and size == need, places
+
+
+@pytest.mark.parametrize("first", [False, True])
+@pytest.mark.parametrize("in_major", [False, True])
+@pytest.mark.parametrize("shapes", [
+    [(4352, 4096, 640)],                                    # 272 tiles: 16 cut
+    [(2048, 4096, 700), (2304, 4000, 643)],                 # the second partly whole, partly cut
+    [(4100, 2050, 330), (515, 8200, 326), (2049, 260, 0)],  # 252 tiles and 18 without tokens
+    [(9000, 520, 1300), (300, 33000, 60)],                  # more than a round whose tokens differ
+])
+def test_more_tiles_than_cus(shapes, in_major, first):
+    """Whole numbers, whose sums are exact, in weights of several rounds of
+    tiles; nothing is written behind the workspace."""
+    gen = torch.Generator("cuda").manual_seed(len(shapes) * 10 + in_major)
+    plan = zr.zr_plan_buckets([a * b for a, b, _ in shapes], [0] * len(shapes), [(1, 1)], 1 << 40)
+    items, want = [], []
+    for k, (n_out, n_in, tokens) in enumerate(shapes):
+        dy = torch.randint(-8, 9, (tokens, n_out), device="cuda", generator=gen).bfloat16()
+        x = torch.randint(-8, 9, (tokens, n_in), device="cuda", generator=gen).float()
+        codes, scales = zr.act_empty(tokens, n_in)
+        zr.zr_act_quantize(x, codes, scales)
+        items.append((k, dy, codes, scales, in_major))
+        a, b = (x.double(), dy.double()) if in_major else (dy.double(), x.double())
+        want.append((a.t().contiguous() @ b).flatten())
+    want = torch.cat(want).float()
+    n = want.numel()
+    grad = torch.full((n + 64,), 3.0, device="cuda")
+    need = zr.zr_ipg_linear_workspace(plan, items, 0, n)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    call = zr.zr_ipg_accumulate_linear_first if first else zr.zr_ipg_accumulate_linear
+    call(plan, items, grad[:n], ws[:need])
+    assert torch.equal(grad[:n], want if first else want + 3.0)
+    assert (grad[n:] == 3.0).all() and (ws[need:] == 0xA5).all()
