@@ -59,7 +59,8 @@ REQUIRED = ([f"lookup_kernel<{t}>" for t in ("float", "unsigned short")] +
             [f"embed_sum_kernel<{t}, {first}, {tiny}>" for t in ("float", "unsigned short")
              for first in ("false", "true") for tiny in ("false", "true")] +
             [f"act_{k}_kernel<{t}>" for k in ("quantize", "dequantize") for t in ("float", "unsigned short")] +
-            [f"{k}_kernel<{b}>" for k in ("embed_join", "linear", "linear_join") for b in ("false", "true")])
+            [f"{k}_kernel<{b}>" for k in ("embed_join", "linear_join") for b in ("false", "true")] +
+            [f"linear_kernel<{b}, {d}>" for b in ("false", "true") for d in ("false", "true")])
 
 
 def test_layer_kernels_on_cpu_under_asan_ubsan(tmp_path):

@@ -179,7 +179,8 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
 // read and store more for each product.  Measured at 4096 x 4096 weights and
 // 8192 tokens: 1332 TFLOP/s, 1240 with rows that do not lie on 16 bytes; with
 // dY through registers 1207, and of that kind 256 x 128 tiles of four waves,
-// two workgroups a CU, 1042, four waves of 128 x 128 1156.
+// two workgroups a CU, 1042, four waves of 128 x 128 1156.  (One full round of
+// tiles: weights of few tiles or few tokens were not compared.)
 
 using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
 using s16x4 = short __attribute__((ext_vector_type(4)));
@@ -521,7 +522,7 @@ __device__ __forceinline__ void whole_tiles(const Loader& in, const Reader& read
 
 // The tile's sums over the tokens [t0, t1), added to the MFMAs' accumulators:
 // a block's rows are the weight's stored rows, its columns a row's elements.
-template <bool kInMajor>
+template <bool kInMajor, bool kDirect>
 __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0, int64_t t0,
                                           int64_t t1, char* lds, Acc& acc) {
   const int tid = threadIdx.x;
@@ -532,7 +533,7 @@ __device__ __forceinline__ void tile_sums(const Item& it, int64_t o0, int64_t i0
   const int64_t end = it.out % 8 && t1 == it.tokens ? t1 - 1 : t1;
   const int steps = it.out < 8 || end < t0 ? 0 : static_cast<int>((end - t0) / kDepth);
   if (steps > 0) {
-    if (it.direct) whole_tiles<kInMajor, true>(in, reader, t0, steps, lds, acc, tid);
+    if (kDirect || it.direct) whole_tiles<kInMajor, true>(in, reader, t0, steps, lds, acc, tid);
     else whole_tiles<kInMajor, false>(in, reader, t0, steps, lds, acc, tid);
     t0 += static_cast<int64_t>(steps) * kDepth;
   }
@@ -617,7 +618,8 @@ __device__ __forceinline__ void put_sums(const Item& it, const Place<kInMajor>& 
   }
 }
 
-template <bool kInMajor>
+// kDirect: every item's dY lies on 16 bytes.
+template <bool kInMajor, bool kDirect>
 __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a) {
   __shared__ __align__(16) char lds[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
@@ -649,7 +651,7 @@ __global__ __launch_bounds__(kThreads, 2) void linear_kernel(const LinearArgs a)
   const Item& it = a.item[k];
   const Place<kInMajor> at(it, tile);
   Acc acc = {};
-  tile_sums<kInMajor>(it, at.o0, at.i0, t0, t1, lds, acc);
+  tile_sums<kInMajor, kDirect>(it, at.o0, at.i0, t0, t1, lds, acc);
 #pragma unroll
   for (int i = 0; i < kOutBlocks; ++i)
 #pragma unroll
@@ -810,12 +812,12 @@ size_t launch_end(const std::vector<Item>& items, size_t k) {
 // with the least time in the model below, in 256ths of the time that a tile of
 // tokens takes (1.6 us).  Cutting costs the join's launch and the pieces'
 // writes and reads, 256 kB each: 3 tiles, and 13 more when every CU has a
-// piece.  Measured, cut and not: 2304 x 768 and 768 x 768 weights over 8192
-// tokens (36 tiles, 7 pieces each; with 5 and 4 pieces 1 us less and 3 more)
-// 56 and 160 us; 2560 x 2560 over 4096 (100 tiles, 2 pieces) 66 and 85; 1024 x
-// 1024 over 2048 (16 tiles, 6 pieces) 28 and 44; 160 x 2451 over 1164 (10
-// tiles, 4 pieces) 22 and 44; 14336 x 4096 over 8192 (896 tiles, the last 128
-// in 2 pieces) 777 and 833 us.
+// piece.  Measured, cut and not, back to back: 2304 x 768 and 768 x 768 weights
+// over 8192 tokens (36 tiles, 7 pieces each; with 5 and 4 pieces 1 us less and 3
+// more) 59 and 162 us; 2560 x 2560 over 4096 (100 tiles, 2 pieces) 71 and 88;
+// 1024 x 1024 over 2048 (16 tiles, 6 pieces) 30 and 45; 160 x 2451 over 1164 (10
+// tiles, 4 pieces) 22 and 36; 14336 x 4096 over 8192 (896 tiles, the last 128
+// in 2 pieces) 793 and 825 us.
 constexpr int kCus = 256;
 int32_t pieces_of(int64_t steps, int64_t rest) {
   int64_t best = 1, least = 256 * steps;
@@ -893,7 +895,12 @@ zr_status run_linear(const zr_plan* plan, const zr_linear_grad* items, int64_t n
     }
     for (const Launch& l : launches) {
       const bool in_major = l.a.item[0].in_major;
-      auto* kernel = in_major ? linear_kernel<true> : linear_kernel<false>;
+      // Where all of dY lies on 16 bytes, a kernel without the other kind's loop
+      // spills no registers: 33.3 us for two weights of 1024 x 1024 over 2048
+      // tokens (33.7), 11.3 for 2048 x 2048 over 64 (11.8).
+      const bool direct = std::all_of(l.a.item, l.a.item + l.a.n, [](const Item& it) { return it.direct; });
+      auto* kernel = in_major ? (direct ? linear_kernel<true, true> : linear_kernel<true, false>)
+                              : (direct ? linear_kernel<false, true> : linear_kernel<false, false>);
       ZR_LAUNCH(l.grid, kThreads, stream, l.a, kernel);
       st = launched("linear gradient launch");
       if (st != ZR_OK) return st;
