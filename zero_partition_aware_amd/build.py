@@ -37,9 +37,10 @@ HIP_FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
 
 
 # Per-kernel fingerprints of the device code: for every kernel in the gfx950
-# code object of the reduction path (the kernels bench.py measures), a hash of its instruction bytes (.text) and of its kernel
-# descriptor (.rodata, register and segment sizes), written beside the
-# library at build time as {demangled kernel name: hash}.  The code holds no
+# code object of the reduction path (the kernels that bench.py measures; the
+# layer operators' have none), a hash of its instruction bytes (.text) and of
+# its kernel descriptor (.rodata, register and segment sizes), written beside
+# the library at build time as {demangled kernel name: hash}.  The code holds no
 # relocations or PC-relative references, so a kernel's bytes do not depend on
 # where it sits; the descriptor's code-entry offset, which does, is zeroed
 # before hashing.  A counter measurement stays tied to exactly the kernel it
