@@ -596,6 +596,61 @@ zr_status zr_ipg_accumulate_linear_first(const zr_plan* plan, const zr_linear_gr
                                          int64_t window_len, void* workspace,
                                          int64_t workspace_bytes, hipStream_t stream);
 
+/* Losses over a vocabulary's logits, with their gradients.  A row z of `vocab`
+ * logits (dtype), q = softmax(z / temperature) over it.  Each row has its own
+ * loss; their sum's gradient dL/dz goes to dlogits, rows of the same dtype,
+ * rounded once: the dy of the layer that made the logits (zr_linear_input_grad,
+ * zr_linear_grad).  dlogits may be null (losses only), or be logits itself,
+ * pointer and stride, which it then replaces; otherwise outputs must not
+ * overlap inputs.  Sums are as above; logarithms, ratios and losses 64-bit,
+ * stored in fp32.
+ *   weight[rows]   each row's factor (a mask, one over the tokens of the step);
+ *                  null: 1.  Weight 0 gives a loss and a gradient of 0.
+ * A row that nothing is asked of (no entry in the vocabulary; logits that are
+ * all -inf) gives a loss, a log-probability and a gradient of 0.  Elsewhere NaN
+ * and +inf spread as in the formulas; logits of -inf have q = 0, and logits of
+ * the type's lowest value are numbers like others.
+ * The workspace (zr_loss_workspace; top 1 for the policy loss) may be 0 bytes
+ * and null.
+ * ZR_ERR_UNSUPPORTED: vocab of 2^30, more than 1024 entries, or 2^22 rows or
+ * more. */
+zr_status zr_loss_workspace(int64_t rows, int64_t vocab, int64_t top, zr_dtype dtype,
+                            int64_t* bytes);
+
+/* zr_distill_loss -- distillation from a teacher's top logits:
+ *   p = softmax(t / temperature) over the row's entries,
+ *   loss = weight * temperature^2 * sum_j p_j * (log p_j - log q[id_j]),
+ *   dlogits[v] = weight * temperature * (q[v] - sum_{j: id_j = v} p_j).
+ *   ids, teacher   device rows of `top` columns and their logits t.  An id
+ *                  outside [0, vocab), or a t of -inf, is no entry; ids may
+ *                  repeat.  With one entry a row this is the cross-entropy
+ *                  (times temperature^2). */
+zr_status zr_distill_loss(const void* logits, zr_dtype dtype, int64_t rows, int64_t vocab,
+                          int64_t logits_stride, const void* ids, zr_index ids_type,
+                          int64_t ids_stride, const void* teacher, zr_dtype teacher_dtype,
+                          int64_t teacher_stride, int64_t top, const float* weight,
+                          double temperature, float* loss, void* dlogits,
+                          int64_t dlogits_stride, void* workspace, int64_t workspace_bytes,
+                          hipStream_t stream);
+
+/* zr_policy_loss -- the clipped policy loss with a KL term:
+ *   lp = log q[token],  r = exp(lp - old_logp),  d = ref_logp - lp,
+ *   loss = weight * (-min(r * A, clamp(r, 1 - clip_low, 1 + clip_high) * A)
+ *                    + kl * (exp(d) - d - 1)),
+ *   dlogits = dloss/dlp * ([v = token] - q[v]) / temperature, where the clipped
+ *   side of the minimum has slope 0 (at the border itself r's).
+ *   tokens[rows]   a token outside [0, vocab) -- padding -- gives zeros.
+ *   ref_logp       read where kl is not 0; may be null otherwise.
+ *   logp[rows]     receives lp.
+ * 0 <= clip_low <= 1. */
+zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t rows, int64_t vocab,
+                         int64_t logits_stride, const void* tokens, zr_index token_type,
+                         const float* old_logp, const float* ref_logp, const float* advantage,
+                         const float* weight, double clip_low, double clip_high, double kl,
+                         double temperature, float* loss, float* logp, void* dlogits,
+                         int64_t dlogits_stride, void* workspace, int64_t workspace_bytes,
+                         hipStream_t stream);
+
 /* ------------------------------------------------------------- errors --- */
 
 /* Message for the last failed call on this thread ("" if none). */

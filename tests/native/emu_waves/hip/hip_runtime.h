@@ -13,6 +13,7 @@
 
 #include <hip/hip_runtime_api.h>   // the runtime's types and declarations
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <cstring>
@@ -25,6 +26,7 @@
 #define __align__(n) __attribute__((aligned(n)))
 #define ZR_GLOBAL_AS
 #define ZR_LDS_AS
+#define ZR_OPAQUE(x) ((void)(x))
 
 struct zr_emu_dim {
   unsigned x = 0, y = 0, z = 0;
@@ -57,7 +59,7 @@ void zr_emu_launch(void (*kernel)(Args), dim3 grid, unsigned block, const Args& 
 
 // --------------------------------------------------------- wave operations
 
-enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync };
+enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync, kExchange };
 // Gives the lane's input to the operation and returns its result.
 void zr_emu_wave(zr_emu_op op, const void* in, size_t in_bytes, void* out, size_t out_bytes);
 void zr_emu_barrier();
@@ -79,6 +81,14 @@ inline uint64_t __ballot(int x) {
   return r;
 }
 inline int __shfl_up(int x, unsigned d) { return zr_emu_two(kShiftUp, x, static_cast<int>(d)); }
+template <typename T>
+T __shfl_xor(T x, int d) {
+  int w[sizeof(T) / 4];
+  std::memcpy(w, &x, sizeof(T));
+  for (int& v : w) v = zr_emu_two(kExchange, v, d);
+  std::memcpy(&x, w, sizeof(T));
+  return x;
+}
 template <typename T>
 T min(T a, T b) { return b < a ? b : a; }
 template <typename T>
@@ -150,6 +160,7 @@ inline void zr_emu_load_lds(const void* p, void* lds, int bytes, int, int) {
   std::memcpy(v, p, 16);
   zr_emu_lds_later(lds, v);
 }
+#define __builtin_amdgcn_exp2f(x) std::exp2(static_cast<float>(x))
 #define __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, old, high) zr_emu_cvt_pk_fp8((lo), (hi), (old), (high))
 #define __builtin_amdgcn_cvt_pk_f32_fp8(codes, high) zr_emu_cvt_pk_f32((codes), (high))
 #define __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, high) zr_emu_cvt_scale((codes), (scale), (high))

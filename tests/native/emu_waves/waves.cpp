@@ -172,6 +172,9 @@ void finish(unsigned base, uint64_t live) {
         out_of(lane, in_of<int>(there((i & ~3u) + (control >> (2 * (i & 3)) & 3), lane)));
         break;
       }
+      case kExchange:
+        out_of(lane, in_of<int>(there(i ^ static_cast<unsigned>(in_of<int>(lane, 1)), lane)));
+        break;
       case kTranspose: {
         short r[4];
         for (unsigned j = 0; j < 4; ++j)

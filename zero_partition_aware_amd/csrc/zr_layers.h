@@ -23,6 +23,8 @@ using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 #define ZR_GLOBAL_AS __attribute__((address_space(1)))
 #define ZR_LDS_AS __attribute__((address_space(3)))
 #define ZR_LAUNCH(grid, block, stream, args, ...) __VA_ARGS__<<<(grid), (block), 0, (stream)>>>(args)
+// What is worked out from x before is not kept for use behind it.
+#define ZR_OPAQUE(x) asm volatile("" : "+v"(x))
 #endif
 
 // Global-memory pointers (rather than generic ones): no flat instructions.

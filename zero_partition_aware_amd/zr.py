@@ -50,6 +50,7 @@ STATUS_NAMES = {0: "ZR_OK", 1: "ZR_ERR_INVALID", 2: "ZR_ERR_OOM",
                 3: "ZR_ERR_HIP", 4: "ZR_ERR_UNSUPPORTED"}
 
 c_i64, c_i32, c_vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p
+c_f64 = ctypes.c_double
 
 
 class zr_param(ctypes.Structure):
@@ -147,6 +148,11 @@ _sigs = {
                                         _P(c_i64)]),
     "zr_ipg_accumulate_linear": (c_i32, _linear_grads),
     "zr_ipg_accumulate_linear_first": (c_i32, _linear_grads),
+    "zr_loss_workspace": (c_i32, [c_i64, c_i64, c_i64, c_i32, _P(c_i64)]),
+    "zr_distill_loss": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, c_i32,
+                                c_i64, c_i64, c_vp, c_f64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "zr_policy_loss": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
+                               c_f64, c_f64, c_f64, c_f64, c_vp, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "zr_last_error": (ctypes.c_char_p, []),
     "zr_version": (c_i32, []),
 }
@@ -755,7 +761,7 @@ def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS):
         if n < 2 and stride < c:
             stride = c
         if ((rows is None or n == rows) and (cols is None or c == cols) and stride >= c and
-                (step == 1 or c < 2)):
+                (step == 1 or c < 2 or n == 0)):
             return t.data_ptr(), stride
     if t.dtype not in dtypes:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be one of {dtypes}, not {t.dtype}")
@@ -979,3 +985,86 @@ def _linear(fn, plan, items, main_grad, workspace, window_base, window_len, stre
               _dense(main_grad, "main_grad", dev, torch.float32, wl),
               _i64(window_base, "window_base"), wl, ws,
               0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
+
+
+def zr_loss_workspace(rows, vocab, top, dtype):
+    """Bytes of workspace that a loss over [rows, vocab] logits of the torch
+    ``dtype`` needs, with ``top`` entries a row (1 for the policy loss)."""
+    v = c_i64()
+    _check(_lib.zr_loss_workspace(_i64(rows, "rows"), _i64(vocab, "vocab"), _i64(top, "top"),
+                                  _dtype_name_code(dtype), ctypes.byref(v)))
+    return v.value
+
+
+def _loss_rows(logits, dlogits, dev):
+    """(address, stride) of the logits and of the gradient (null, vocab)."""
+    z = _rows(logits, "logits", dev)
+    rows, vocab = logits.shape
+    if dlogits is None:
+        return z, (None, vocab)
+    return z, _rows(dlogits, "dlogits", dev, rows, vocab, (logits.dtype,))
+
+
+def _per_row(t, name, dev, rows):
+    """Address of one fp32 a row (None: null)."""
+    if t is None:
+        return None
+    if t.shape != (rows,):
+        raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; the call needs ({rows},)")
+    return _dense(t, name, dev, torch.float32)
+
+
+def _scratch(workspace, dev):
+    if workspace is None:
+        return None, 0
+    return _dense(workspace, "workspace", dev, torch.uint8), workspace.numel()
+
+
+_IDS = None if torch is None else (torch.int64, torch.int32)
+
+
+def zr_distill_loss(logits, ids, teacher, weight, loss, dlogits=None, temperature=1.0,
+                    workspace=None, stream=None):
+    """Each row's distillation loss from a teacher's top logits, and its
+    gradient.  logits: bf16 or fp32 [rows, vocab]; ids (int64 or int32) and
+    teacher (bf16 or fp32): [rows, top], the teacher's columns and logits, ids
+    outside [0, vocab) for none; weight: fp32 [rows] or None (1); loss: fp32
+    [rows]; dlogits: like logits, logits itself, or None.  workspace: a uint8
+    tensor of at least zr_loss_workspace bytes that no other call uses meanwhile
+    (None where that is 0)."""
+    dev = _device_of(logits, "logits")
+    (z, zs), (g, gs) = _loss_rows(logits, dlogits, dev)
+    rows, vocab = logits.shape
+    i, istride = _rows(ids, "ids", dev, rows, None, _IDS)
+    top = ids.shape[1]
+    t, tstride = _rows(teacher, "teacher", dev, rows, top)
+    ws, nbytes = _scratch(workspace, dev)
+    _check(_lib.zr_distill_loss(
+        z, logits.dtype is torch.bfloat16, rows, vocab, zs, i, ids.dtype is torch.int64, istride,
+        t, teacher.dtype is torch.bfloat16, tstride, top, _per_row(weight, "weight", dev, rows),
+        temperature, _per_row(loss, "loss", dev, rows), g, gs, ws, nbytes, _stream_of(stream, dev)))
+
+
+def zr_policy_loss(logits, tokens, old_logp, ref_logp, advantage, weight, loss, logp,
+                   dlogits=None, clip_low=0.2, clip_high=0.2, kl=0.0, temperature=1.0,
+                   workspace=None, stream=None):
+    """Each row's clipped policy loss with a KL term, its token's
+    log-probability, and its gradient.  logits: bf16 or fp32 [rows, vocab];
+    tokens: int64 or int32 [rows], outside [0, vocab) for padding; old_logp,
+    advantage, and ref_logp (None where kl is 0), weight (None: 1): fp32 [rows];
+    loss, logp: fp32 [rows]; dlogits: like logits, logits itself, or None.
+    workspace: as in zr_distill_loss, for top 1."""
+    dev = _device_of(logits, "logits")
+    (z, zs), (g, gs) = _loss_rows(logits, dlogits, dev)
+    rows, vocab = logits.shape
+    if tokens.shape != (rows,):
+        raise ZrError(ZR_ERR_INVALID,
+                      f"tokens has shape {tuple(tokens.shape)}; the call needs ({rows},)")
+    a, wide = _token_ids(tokens, dev)
+    ws, nbytes = _scratch(workspace, dev)
+    _check(_lib.zr_policy_loss(
+        z, logits.dtype is torch.bfloat16, rows, vocab, zs, a, wide,
+        _per_row(old_logp, "old_logp", dev, rows), _per_row(ref_logp, "ref_logp", dev, rows),
+        _per_row(advantage, "advantage", dev, rows), _per_row(weight, "weight", dev, rows),
+        clip_low, clip_high, kl, temperature, _per_row(loss, "loss", dev, rows),
+        _per_row(logp, "logp", dev, rows), g, gs, ws, nbytes, _stream_of(stream, dev)))
