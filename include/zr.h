@@ -596,6 +596,52 @@ zr_status zr_ipg_accumulate_linear_first(const zr_plan* plan, const zr_linear_gr
                                          int64_t window_len, void* workspace,
                                          int64_t workspace_bytes, hipStream_t stream);
 
+/* The products of layers whose weights lie in the ranks' partitions, grouped by
+ * expert: rows [c_0 + ... + c_{k-1}, + c_k) of a matrix go with the weight
+ * params[k], Y = X W^T for W [n_out, n_in], stored so (in_major 0) or as its
+ * transpose (in_major 1), as in zr_linear_grad, which gives the weights'
+ * gradients.  With one param this is a plain layer.
+ *   params[n], counts[n]  host arrays: each weight's param id (all in one
+ *                         group; a param may come more than once) and its
+ *                         rows, which may be 0 (an expert nobody was routed
+ *                         to: its weight is not read).
+ *   parts[R_g]            host array of device pointers to the partitions' bf16
+ *                         params (P_g elements each); only those that hold some
+ *                         of a weight with rows are read and may not be null.
+ *                         A gathered flat vector serves too: parts[k] = flat +
+ *                         k * P_g.
+ *   rows                  of both matrices; those behind the last count are
+ *                         neither read nor written.
+ * Products of bf16 values, exact, summed in fp32 on the matrix cores and
+ * rounded once to the output's dtype.  Outputs must not overlap inputs.
+ * ZR_ERR_UNSUPPORTED: n_out, n_in or the input's stride of 2^22, or 2^31 rows,
+ * or more, or more tiles than a launch holds. */
+zr_status zr_linear_forward_workspace(const zr_plan* plan, const int64_t* params,
+                                      const int64_t* counts, int64_t n, int64_t n_out,
+                                      int64_t n_in, int32_t in_major, int64_t* bytes);
+zr_status zr_linear_input_grad_workspace(const zr_plan* plan, const int64_t* params,
+                                         const int64_t* counts, int64_t n, int64_t n_out,
+                                         int64_t n_in, int32_t in_major, int64_t* bytes);
+
+/* zr_linear_forward -- the layers' outputs ([Megatron DP] "通信模式": the updated
+ * slices that the next forward pass reads; here without stitching the weights
+ * together):
+ *   y[t, o] = sum_i x[t, i] * W_k[o, i]     for t among the rows of params[k] */
+zr_status zr_linear_forward(const zr_plan* plan, const int64_t* params, const int64_t* counts,
+                            int64_t n, int64_t n_out, int64_t n_in, int32_t in_major,
+                            const void* const* parts, const uint16_t* x, int64_t rows,
+                            int64_t x_stride, void* y, zr_dtype y_dtype, int64_t y_stride,
+                            void* workspace, int64_t workspace_bytes, hipStream_t stream);
+
+/* zr_linear_input_grad -- the gradient of the layers' inputs:
+ *   dx[t, i] = sum_o dy[t, o] * W_k[o, i] */
+zr_status zr_linear_input_grad(const zr_plan* plan, const int64_t* params, const int64_t* counts,
+                               int64_t n, int64_t n_out, int64_t n_in, int32_t in_major,
+                               const void* const* parts, const uint16_t* dy, int64_t rows,
+                               int64_t dy_stride, void* dx, zr_dtype dx_dtype,
+                               int64_t dx_stride, void* workspace, int64_t workspace_bytes,
+                               hipStream_t stream);
+
 /* Losses over a vocabulary's logits, with their gradients.  A row z of `vocab`
  * logits (dtype), q = softmax(z / temperature) over it.  Each row has its own
  * loss; their sum's gradient dL/dz goes to dlogits, rows of the same dtype,

@@ -150,10 +150,10 @@ inline zr_emu_s16x4 zr_emu_transpose(const void* p) {
   zr_emu_wave(kTranspose, &own, sizeof(own), &r, sizeof(r));
   return r;
 }
-// Sixteen bytes a lane into LDS, lane after lane from `lds` on; there after the
-// next wait.
+// Sixteen bytes a lane into LDS, lane after lane from `lds` on; there after a
+// wait for all but the lane's last `left` of them, or fewer.
 void zr_emu_lds_later(void* lds, const void* data);
-void zr_emu_wait();
+void zr_emu_wait(unsigned left);
 inline void zr_emu_load_lds(const void* p, void* lds, int bytes, int, int) {
   unsigned char v[16];
   if (bytes != 16) __builtin_trap();
@@ -167,4 +167,4 @@ inline void zr_emu_load_lds(const void* p, void* lds, int bytes, int, int) {
 #define __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, x, y, z) zr_emu_mfma(&(a), &(b), (c))
 #define __builtin_amdgcn_ds_read_tr16_b64_v4i16(p) zr_emu_transpose(p)
 #define __builtin_amdgcn_global_load_lds(...) zr_emu_load_lds(__VA_ARGS__)
-#define __builtin_amdgcn_s_waitcnt(x) zr_emu_wait()
+#define __builtin_amdgcn_s_waitcnt(x) zr_emu_wait(((x) & 15) | (((x) >> 14 & 3) << 4))

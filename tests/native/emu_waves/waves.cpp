@@ -280,9 +280,11 @@ void zr_emu_lds_later(void* lds, const void* data) {
   std::memcpy(p.data, data, 16);
   g_lanes[g_now].later.push_back(p);
 }
-void zr_emu_wait() {
-  for (const Pending& p : g_lanes[g_now].later) std::memcpy(p.lds, p.data, 16);
-  g_lanes[g_now].later.clear();
+void zr_emu_wait(unsigned left) {
+  std::vector<Pending>& later = g_lanes[g_now].later;
+  const size_t there = later.size() > left ? later.size() - left : 0;
+  for (size_t k = 0; k < there; ++k) std::memcpy(later[k].lds, later[k].data, 16);
+  later.erase(later.begin(), later.begin() + static_cast<std::ptrdiff_t>(there));
 }
 
 // e4m3: sign, 4 exponent bits (bias 7), 3 mantissa bits, no infinities.

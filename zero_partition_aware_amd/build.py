@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libzr.so")
 # HIP translation units: the reduction path, and the layer operators
-HIP_SOURCES = ["zr_kernels", "zr_embed", "zr_linear", "zr_loss"]
+HIP_SOURCES = ["zr_kernels", "zr_embed", "zr_linear", "zr_product", "zr_loss"]
 ARCH = os.environ.get("ZR_OFFLOAD_ARCH", "gfx950")
 
 

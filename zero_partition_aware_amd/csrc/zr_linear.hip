@@ -12,7 +12,7 @@
 #include <tuple>
 #include <vector>
 
-#include "zr_layers.h"
+#include "zr_tiles.h"
 
 using namespace zr;
 
@@ -182,10 +182,6 @@ __global__ __launch_bounds__(kActThreads) void act_dequantize_kernel(const ActAr
 // two workgroups a CU, 1042, four waves of 128 x 128 1156.  (One full round of
 // tiles: weights of few tiles or few tokens were not compared.)
 
-using bf16x8 = __bf16 __attribute__((ext_vector_type(8)));
-using s16x4 = short __attribute__((ext_vector_type(4)));
-using f32x16 = float __attribute__((ext_vector_type(16)));
-
 constexpr int kMaxItems = 16;
 
 constexpr int kTileOut = 256;   // columns of dY per workgroup
@@ -219,24 +215,6 @@ struct LinearArgs {
   int32_t first;               // main_grad is written, not added to
   int32_t whole;               // whole tiles in all
 };
-
-// A tile of kDepth tokens and C columns in LDS: 16-byte units (8 bf16) of a
-// token's row, exchanged by the token's number.
-__device__ __forceinline__ int exchanged(int k, int u) { return u ^ (4 * (k & 3)); }
-template <int C>
-__device__ __forceinline__ int staged(int k, int u) {
-  return k * (C * 2) + (exchanged(k, u) << 4);
-}
-
-// The eight tokens of one column that a lane of an MFMA takes, from the
-// 16-token, 32-column block whose place `at` the lane has.
-template <int C>
-__device__ __forceinline__ bf16x8 read_columns(const char* lds, int at) {
-  using lds_s16x4 = ZR_LDS_AS s16x4;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at));
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lds + at + 4 * (C * 2)));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
 
 // One step's share of a thread: rows of dY and of X's codes, in registers
 // between their loads and their places in LDS.
@@ -419,14 +397,6 @@ __device__ __forceinline__ void multiply(Acc& acc, const Fragments& f) {
       acc[i][j] = kInMajor
                       ? __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.x[j], f.d[i], acc[i][j], 0, 0, 0)
                       : __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.d[i], f.x[j], acc[i][j], 0, 0, 0);
-}
-
-// All waves' LDS accesses before it are done after it; loads from global
-// memory stay in flight.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // What the pipelined loop keeps in registers.

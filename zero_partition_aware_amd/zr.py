@@ -91,6 +91,8 @@ _P = ctypes.POINTER
 _embedding_grad = [c_vp, c_i64, c_i64, c_vp, c_i32, c_i64, ctypes.c_float, c_vp, c_i32, c_i64,
                    c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]
 _linear_grads = [c_vp, _P(zr_linear_grad), c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp]
+_products = [c_vp, _P(c_i64), _P(c_i64), c_i64, c_i64, c_i64, c_i32, _P(c_vp), c_vp, c_i64, c_i64,
+             c_vp, c_i32, c_i64, c_vp, c_i64, c_vp]
 _sigs = {
     "zr_plan_buckets": (c_i32, [_P(zr_param), c_i64, _P(zr_group), c_i32, c_i64,
                                 c_i32, c_i64, _P(c_vp)]),
@@ -148,6 +150,10 @@ _sigs = {
                                         _P(c_i64)]),
     "zr_ipg_accumulate_linear": (c_i32, _linear_grads),
     "zr_ipg_accumulate_linear_first": (c_i32, _linear_grads),
+    "zr_linear_forward_workspace": (c_i32, _products[:7] + [_P(c_i64)]),
+    "zr_linear_input_grad_workspace": (c_i32, _products[:7] + [_P(c_i64)]),
+    "zr_linear_forward": (c_i32, _products),
+    "zr_linear_input_grad": (c_i32, _products),
     "zr_loss_workspace": (c_i32, [c_i64, c_i64, c_i64, c_i32, _P(c_i64)]),
     "zr_distill_loss": (c_i32, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i32, c_i64, c_vp, c_i32,
                                 c_i64, c_i64, c_vp, c_f64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
@@ -987,6 +993,92 @@ def _linear(fn, plan, items, main_grad, workspace, window_base, window_len, stre
               0 if workspace is None else workspace.numel(), _stream_of(stream, dev)))
 
 
+def _scratch(workspace, dev):
+    if workspace is None:
+        return None, 0
+    return _dense(workspace, "workspace", dev, torch.uint8), workspace.numel()
+
+
+def _group_list(plan, params, counts):
+    """The params and their counts as the C call takes them."""
+    n = len(params)
+    _expect_len(counts, n, "counts")
+    try:
+        return (c_i64 * max(n, 1))(*params), (c_i64 * max(n, 1))(*counts), n
+    except TypeError:
+        raise ZrError(ZR_ERR_INVALID, "params and counts must be integers") from None
+
+
+def zr_linear_forward_workspace(plan, params, counts, n_out, n_in, in_major=False):
+    """Bytes of workspace zr_linear_forward needs for these params and counts."""
+    p, c, n = _group_list(plan, params, counts)
+    v = c_i64()
+    _check(_lib.zr_linear_forward_workspace(plan.handle, p, c, n, _i64(n_out, "n_out"),
+                                            _i64(n_in, "n_in"), bool(in_major), ctypes.byref(v)))
+    return v.value
+
+
+def zr_linear_input_grad_workspace(plan, params, counts, n_out, n_in, in_major=False):
+    """Bytes of workspace zr_linear_input_grad needs for these params and counts."""
+    p, c, n = _group_list(plan, params, counts)
+    v = c_i64()
+    _check(_lib.zr_linear_input_grad_workspace(plan.handle, p, c, n, _i64(n_out, "n_out"),
+                                               _i64(n_in, "n_in"), bool(in_major),
+                                               ctypes.byref(v)))
+    return v.value
+
+
+def zr_linear_forward(plan, params, counts, parts, x, y, in_major=False, workspace=None,
+                      stream=None):
+    """y = x W^T, the first counts[0] rows with the weight params[0], the next
+    counts[1] with params[1], and so on (experts, their rows sorted), each
+    weight read from the R_g bf16 partition tensors ``parts`` (those that hold
+    none of them may be None).  x: bf16 [rows, n_in]; y: bf16 or fp32 [rows,
+    n_out]; in_major True for weights stored [n_in, n_out].  Rows behind the
+    last count stay as they are.  workspace: a uint8 tensor of at least
+    zr_linear_forward_workspace bytes that no other call uses meanwhile (None
+    where that is 0)."""
+    _product(_lib.zr_linear_forward, plan, params, counts, parts, x, "x", y, "y", False, in_major,
+             workspace, stream)
+
+
+def zr_linear_input_grad(plan, params, counts, parts, dy, dx, in_major=False, workspace=None,
+                         stream=None):
+    """dx = dy W, grouped as in zr_linear_forward.  dy: bf16 [rows, n_out]; dx:
+    bf16 or fp32 [rows, n_in]."""
+    _product(_lib.zr_linear_input_grad, plan, params, counts, parts, dy, "dy", dx, "dx", True,
+             in_major, workspace, stream)
+
+
+def _product(fn, plan, params, counts, parts, x, x_name, y, y_name, swap, in_major, workspace,
+             stream):
+    dev = _device_of(x, x_name)
+    xp, xs = _rows(x, x_name, dev, dtypes=(torch.bfloat16,))
+    rows, depth = x.shape
+    yp, ys = _rows(y, y_name, dev, rows)
+    cols = y.shape[1]
+    p, c, n = _group_list(plan, params, counts)
+    first = params[0] if n else 0
+    # an out-of-range id is left to the C call's check
+    group = plan.param_groups[first] if 0 <= first < len(plan.param_groups) else 0
+    _expect_len(parts, _world(plan, group), "parts")
+    P = _part_numel(plan, group)
+    arr = (c_vp * len(parts))()
+    for k, t in enumerate(parts):
+        if t is None:
+            continue
+        if not (t.dtype is torch.bfloat16 and t.get_device() == dev and t.is_contiguous() and
+                t.numel() >= P):
+            _dense(t, f"parts[{k}]", dev, torch.bfloat16, P)
+        arr[k] = t.data_ptr()
+    ws, nbytes = _scratch(workspace, dev)
+    status = fn(plan.handle, p, c, n, depth if swap else cols, cols if swap else depth,
+                bool(in_major), arr, xp, rows, xs, yp, y.dtype is torch.bfloat16, ys, ws, nbytes,
+                _stream_of(stream, dev))
+    if status:
+        _check(status)
+
+
 def zr_loss_workspace(rows, vocab, top, dtype):
     """Bytes of workspace that a loss over [rows, vocab] logits of the torch
     ``dtype`` needs, with ``top`` entries a row (1 for the policy loss)."""
@@ -1012,12 +1104,6 @@ def _per_row(t, name, dev, rows):
     if t.shape != (rows,):
         raise ZrError(ZR_ERR_INVALID, f"{name} has shape {tuple(t.shape)}; the call needs ({rows},)")
     return _dense(t, name, dev, torch.float32)
-
-
-def _scratch(workspace, dev):
-    if workspace is None:
-        return None, 0
-    return _dense(workspace, "workspace", dev, torch.uint8), workspace.numel()
 
 
 _IDS = None if torch is None else (torch.int64, torch.int32)
