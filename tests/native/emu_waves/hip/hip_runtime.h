@@ -27,6 +27,7 @@
 #define ZR_GLOBAL_AS
 #define ZR_LDS_AS
 #define ZR_OPAQUE(x) ((void)(x))
+#define ZR_ORDERED() ((void)0)
 
 struct zr_emu_dim {
   unsigned x = 0, y = 0, z = 0;
@@ -59,7 +60,7 @@ void zr_emu_launch(void (*kernel)(Args), dim3 grid, unsigned block, const Args& 
 
 // --------------------------------------------------------- wave operations
 
-enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync, kExchange };
+enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync, kExchange, kMfmaFlat };
 // Gives the lane's input to the operation and returns its result.
 void zr_emu_wave(zr_emu_op op, const void* in, size_t in_bytes, void* out, size_t out_bytes);
 void zr_emu_barrier();
@@ -144,6 +145,16 @@ inline F zr_emu_mfma(const void* a, const void* b, const F& c) {
   zr_emu_wave(kMfma, bytes, sizeof(bytes), &r, sizeof(r));
   return r;
 }
+template <typename F>
+inline F zr_emu_mfma_flat(const void* a, const void* b, const F& c) {
+  unsigned char bytes[48];
+  std::memcpy(bytes, a, 16);
+  std::memcpy(bytes + 16, b, 16);
+  std::memcpy(bytes + 32, &c, 16);
+  F r;
+  zr_emu_wave(kMfmaFlat, bytes, sizeof(bytes), &r, sizeof(r));
+  return r;
+}
 inline zr_emu_s16x4 zr_emu_transpose(const void* p) {
   zr_emu_s16x4 own, r;
   std::memcpy(&own, p, sizeof(own));   // checked here
@@ -165,6 +176,7 @@ inline void zr_emu_load_lds(const void* p, void* lds, int bytes, int, int) {
 #define __builtin_amdgcn_cvt_pk_f32_fp8(codes, high) zr_emu_cvt_pk_f32((codes), (high))
 #define __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, scale, high) zr_emu_cvt_scale((codes), (scale), (high))
 #define __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, x, y, z) zr_emu_mfma(&(a), &(b), (c))
+#define __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, x, y, z) zr_emu_mfma_flat(&(a), &(b), (c))
 #define __builtin_amdgcn_ds_read_tr16_b64_v4i16(p) zr_emu_transpose(p)
 #define __builtin_amdgcn_global_load_lds(...) zr_emu_load_lds(__VA_ARGS__)
 #define __builtin_amdgcn_s_waitcnt(x) zr_emu_wait(((x) & 15) | (((x) >> 14 & 3) << 4))

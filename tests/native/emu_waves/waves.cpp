@@ -152,6 +152,22 @@ void finish(unsigned base, uint64_t live) {
       std::memcpy(g_lanes[base + i].out, c, 64);
     }
   }
+  if (op == kMfmaFlat) {   // 16 x 16, over 32
+    if (~live) stop("a matrix product without all lanes", first);
+    static float a[16][32], b[32][16];
+    for (unsigned i = 0; i < 64; ++i)
+      for (unsigned k = 0; k < 8; ++k) {
+        a[i % 16][8 * (i / 16) + k] = widen(in_of<uint16_t>(base + i, k));
+        b[8 * (i / 16) + k][i % 16] = widen(in_of<uint16_t>(base + i, 8 + k));
+      }
+    for (unsigned i = 0; i < 64; ++i) {
+      float c[4];
+      std::memcpy(c, g_lanes[base + i].in + 32, 16);
+      for (unsigned v = 0; v < 4; ++v)
+        for (unsigned k = 0; k < 32; ++k) c[v] += a[4 * (i / 16) + v][k] * b[k][i % 16];
+      std::memcpy(g_lanes[base + i].out, c, 16);
+    }
+  }
   for (unsigned i = 0; i < 64; ++i) {
     if (!(live >> i & 1)) continue;
     const unsigned lane = base + i;

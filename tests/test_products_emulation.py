@@ -13,7 +13,7 @@ from tests import _emu
 
 pytestmark = pytest.mark.skipif(not os.path.exists(_emu.CLANG), reason="ROCm clang++ not available")
 
-SHAPES = ("Shape<256, 256, 2, 4, 2>", "Shape<32, 128, 1, 4, 4>")
+SHAPES = ("Shape<256, 256, 2, 4, 64, 2>", "Shape<32, 128, 1, 4, 64, 4>")
 REQUIRED = ([f"product_kernel<(anonymous namespace)::{s}, {c}, {d}>" for s in SHAPES
              for c in ("false", "true") for d in ("false", "true")] +
             [f"product_join_kernel<(anonymous namespace)::{s}>" for s in SHAPES])

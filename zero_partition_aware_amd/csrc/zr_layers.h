@@ -25,6 +25,8 @@ using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 #define ZR_LAUNCH(grid, block, stream, args, ...) __VA_ARGS__<<<(grid), (block), 0, (stream)>>>(args)
 // What is worked out from x before is not kept for use behind it.
 #define ZR_OPAQUE(x) asm volatile("" : "+v"(x))
+// No access to memory moves over it.
+#define ZR_ORDERED() asm volatile("" ::: "memory")
 #endif
 
 // Global-memory pointers (rather than generic ones): no flat instructions.

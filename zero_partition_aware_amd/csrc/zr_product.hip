@@ -31,36 +31,39 @@ struct ProductArgs {
   int32_t n;                   // groups
   int32_t depth, cols;         // k's and n's extent
   int32_t col_tiles, tiles, pieces;
-  int32_t y_bf16;
+  int32_t y_bf16, world;
 };
 
-constexpr int kDepth = 64;     // k of a staged tile
-constexpr int kUnits = kDepth / 8;
-
-// A workgroup's tile of rows and columns, by waves of 32 x 32 blocks, with
-// kStages tiles of LDS.
-template <int kRows_, int kCols_, int kWavesR_, int kWavesC_, int kStages_>
+// A workgroup's tile of rows and columns, by waves of 16 x 16 blocks, and the
+// LDS of kStages steps of kDepth k.
+template <int kRows_, int kCols_, int kWavesR_, int kWavesC_, int kDepth_, int kStages_>
 struct Shape {
-  static constexpr int kRows = kRows_, kCols = kCols_;
+  static constexpr int kRows = kRows_, kCols = kCols_, kDepth = kDepth_;
+  static constexpr int kUnits = kDepth / 8, kPhases = kDepth / 32;
   static constexpr int kWavesR = kWavesR_, kWavesC = kWavesC_, kStages = kStages_;
   static constexpr int kThreads = 64 * kWavesR * kWavesC;
-  static constexpr int kRowBlocks = kRows / kWavesR / 32, kColBlocks = kCols / kWavesC / 32;
+  static constexpr int kRowBlocks = kRows / kWavesR / 16, kColBlocks = kCols / kWavesC / 16;
   static constexpr int kXBytes = kRows * kDepth * 2, kWBytes = kCols * kDepth * 2;
   static constexpr int kStage = kXBytes + kWBytes;
   static constexpr int kXLoads = kXBytes / 16 / kThreads, kWLoads = kWBytes / 16 / kThreads;
   static_assert(kXLoads * kThreads * 16 == kXBytes && kWLoads * kThreads * 16 == kWBytes, "staging shape");
 };
 
-// A matrix whose rows run along k: 128 bytes of a row, its 16-byte units
-// exchanged (xor) by the row's number, so that eight lanes that read one unit of
-// eight rows use all banks.
-__device__ __forceinline__ int staged_row(int r, int u) { return r * (kDepth * 2) + ((u ^ (r & 7)) << 4); }
+// A matrix whose rows run along k: the 16-byte units of a row's kDepth k are
+// exchanged (xor) by its pair (64 k) or four (32 k) of rows, so that sixteen
+// lanes that read one unit of sixteen rows use all 64 banks.
+template <int kDepth>
+__device__ __forceinline__ int exchanged_row(int r, int u) {
+  static_assert(kDepth == 32 || kDepth == 64, "a row of LDS");
+  return u ^ (kDepth == 64 ? r >> 1 & 7 : r >> 2 & 3);
+}
+template <int kDepth>
+__device__ __forceinline__ int staged_row(int r, int u) { return r * (kDepth * 2) + (exchanged_row<kDepth>(r, u) << 4); }
 
 // Where a weight's tile lies: in partition a up to the element `cut` (counted
 // from the tile's first one), in b from there on.  more: in others too.
 struct Source {
-  const char* a;
-  const char* b;               // both as if the tile's first element lay there
+  uintptr_t a, b;              // as if the tile's first element lay there
   int64_t cut;
   bool more;
 };
@@ -69,8 +72,8 @@ __device__ __forceinline__ Source source_of(const ProductArgs& p, int64_t first,
   const int64_t k = first / p.part_numel, at = first - k * p.part_numel;
   s.cut = p.part_numel - at;
   s.more = span > s.cut + p.part_numel;
-  s.a = p.part[k] + at * 2;
-  s.b = span > s.cut ? p.part[k + 1] - s.cut * 2 : s.a;
+  s.a = reinterpret_cast<uintptr_t>(p.part[k]) + at * 2;
+  s.b = span > s.cut ? reinterpret_cast<uintptr_t>(p.part[k + 1]) - s.cut * 2 : s.a;
   return s;
 }
 
@@ -82,9 +85,9 @@ __device__ __forceinline__ u32x4 source_unit(const ProductArgs& p, const Source&
     const int64_t k = (first + e) / p.part_numel, at = first + e - k * p.part_numel;
     if (at + count <= p.part_numel) from = p.part[k] + at * 2;
   } else if (e + count <= s.cut) {
-    from = s.a + e * 2;
+    from = reinterpret_cast<const char*>(s.a + e * 2);
   } else if (e >= s.cut) {
-    from = s.b + e * 2;
+    from = reinterpret_cast<const char*>(s.b + e * 2);
   }
   if (from && count == 8) return load_at<u32x4, 2>(from);
   u32x4 v = {0, 0, 0, 0};
@@ -110,6 +113,13 @@ __device__ __forceinline__ u32x4 row_unit(const uint16_t* x, int count) {
     if (i < count) v[i / 2] |= static_cast<uint32_t>(*as_global<uint16_t>(x + i)) << (16 * (i & 1));
   return v;
 }
+
+// A matrix whose rows run along n: its 16-byte units are exchanged by the row's
+// number, so that the four rows that 16 lanes of a transposing read take, and the
+// four eight rows on that the next 16 do, lie in different banks.
+__device__ __forceinline__ int exchanged_column(int k, int u) { return u ^ (4 * (k & 3)) ^ (2 * (k >> 3 & 1)); }
+template <int C>
+__device__ __forceinline__ int staged_column(int k, int u) { return k * (C * 2) + (exchanged_column(k, u) << 4); }
 
 // A tile's place.
 struct Place {
@@ -151,10 +161,10 @@ struct Staged {
 // kColumns: n is the weight's fast axis.
 template <typename S, bool kColumns>
 __device__ __forceinline__ void load_step(Staged<S>& s, const ProductArgs& a, const Place& p, int k0, int tid) {
-  const int left = a.depth - k0 < kDepth ? a.depth - k0 : kDepth;
+  const int left = a.depth - k0 < S::kDepth ? a.depth - k0 : S::kDepth;
 #pragma unroll
   for (int j = 0; j < S::kXLoads; ++j) {
-    const int at = j * S::kThreads + tid, r = at / kUnits, u = 8 * (at % kUnits);
+    const int at = j * S::kThreads + tid, r = at / S::kUnits, u = 8 * (at % S::kUnits);
     s.x[j] = u32x4{0, 0, 0, 0};
     if (r < p.rows && u < left)
       s.x[j] = row_unit(p.x + r * a.x_stride + k0 + u, left - u < 8 ? left - u : 8);
@@ -166,7 +176,7 @@ __device__ __forceinline__ void load_step(Staged<S>& s, const ProductArgs& a, co
   const Source src = source_of(a, first, span);
 #pragma unroll
   for (int j = 0; j < S::kWLoads; ++j) {
-    constexpr int kPerRow = kColumns ? S::kCols / 8 : kUnits;
+    constexpr int kPerRow = kColumns ? S::kCols / 8 : S::kUnits;
     const int at = j * S::kThreads + tid, r = at / kPerRow, u = 8 * (at % kPerRow);
     const int high = kColumns ? left : p.cols, wide = kColumns ? p.cols : left;
     s.w[j] = u32x4{0, 0, 0, 0};
@@ -180,68 +190,101 @@ __device__ __forceinline__ void store_step(const Staged<S>& s, char* lds, int ti
 #pragma unroll
   for (int j = 0; j < S::kXLoads; ++j) {
     const int at = j * S::kThreads + tid;
-    *reinterpret_cast<u32x4*>(lds + staged_row(at / kUnits, at % kUnits)) = s.x[j];
+    *reinterpret_cast<u32x4*>(lds + staged_row<S::kDepth>(at / S::kUnits, at % S::kUnits)) = s.x[j];
   }
 #pragma unroll
   for (int j = 0; j < S::kWLoads; ++j) {
-    constexpr int kPerRow = kColumns ? S::kCols / 8 : kUnits;
+    constexpr int kPerRow = kColumns ? S::kCols / 8 : S::kUnits;
     const int at = j * S::kThreads + tid, r = at / kPerRow, u = at % kPerRow;
-    const int to = kColumns ? staged<S::kCols>(r, u) : staged_row(r, u);
+    const int to = kColumns ? staged_column<S::kCols>(r, u) : staged_row<S::kDepth>(r, u);
     *reinterpret_cast<u32x4*>(lds + S::kXBytes + to) = s.w[j];
   }
 }
 
-// Whole steps straight into LDS: rows and partitions on 16 bytes, a step's part
-// of the weight in two partitions at most.  Where a row or column is behind the
-// last, the tile's first is read instead; it is never stored.
-template <typename S, bool kColumns>
+// Whole steps straight into LDS: rows and partitions on 16 bytes, a tile's part
+// of the weight (where n is its fast axis, a step's) in two partitions at most,
+// or all in one (kCut false).
+// Where a row or column is behind the last, the tile's first is read instead; it
+// is never stored.
+template <typename S, bool kColumns, bool kCut>
 struct Direct {
-  uint32_t x_off[S::kXLoads], w_off[S::kWLoads];   // bytes from the step's start
-  __device__ __forceinline__ Direct(const ProductArgs& a, const Place& p, int tid) {
+  uint32_t x_off[S::kXLoads], w_off[S::kWLoads];   // a thread's bytes from a step's start
+  const char* x;               // step 0 of the rows
+  uintptr_t w;                 // and of the weight, as if all of it lay in partition k
+  uintptr_t w_next;            // in partition k + 1
+  int64_t cut;                 // bytes from step 0 to that partition
+  int32_t k;
+  __device__ __forceinline__ Direct(const ProductArgs& a, const Place& p, int k0, int tid) {
 #pragma unroll
     for (int j = 0; j < S::kXLoads; ++j) {
-      const int at = j * S::kThreads + tid, r = at / kUnits, u = (at % kUnits) ^ (r & 7);
+      const int at = j * S::kThreads + tid, r = at / S::kUnits, u = exchanged_row<S::kDepth>(r, at % S::kUnits);
       x_off[j] = (r < p.rows ? r : 0) * static_cast<uint32_t>(a.x_stride * 2) + u * 16;
     }
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
       if constexpr (kColumns) {
         constexpr int kPerRow = S::kCols / 8;
-        const int at = j * S::kThreads + tid, r = at / kPerRow, u = exchanged(r, at % kPerRow);
+        const int at = j * S::kThreads + tid, r = at / kPerRow, u = exchanged_column(r, at % kPerRow);
         w_off[j] = r * static_cast<uint32_t>(a.cols * 2) + (8 * u < p.cols ? u : 0) * 16;
       } else {
-        const int at = j * S::kThreads + tid, r = at / kUnits, u = (at % kUnits) ^ (r & 7);
+        const int at = j * S::kThreads + tid, r = at / S::kUnits, u = exchanged_row<S::kDepth>(r, at % S::kUnits);
         w_off[j] = (r < p.cols ? r : 0) * static_cast<uint32_t>(a.depth * 2) + u * 16;
       }
     }
+    x = reinterpret_cast<const char*>(p.x);
+    const int64_t first = p.w + (kColumns ? p.col : static_cast<int64_t>(p.col) * a.depth);
+    const int64_t here = first + (kColumns ? static_cast<int64_t>(k0) * a.cols : 0);
+    k = static_cast<int>(here / a.part_numel);
+    cut = ((k + 1) * a.part_numel - first) * 2;
+    w = reinterpret_cast<uintptr_t>(a.part[k]) + (first - k * a.part_numel) * 2;
+    w_next = beyond(a);
   }
-  __device__ __forceinline__ void load(const ProductArgs& a, const Place& p, int k0, char* lds, int w) const {
-    const char* x = reinterpret_cast<const char*>(p.x + k0);
+  __device__ __forceinline__ uintptr_t beyond(const ProductArgs& a) const {
+    return k + 1 < a.world ? reinterpret_cast<uintptr_t>(a.part[k + 1]) - cut : 0;
+  }
+  // Where the weight's step at k0 lies: steps go on.
+  __device__ __forceinline__ int64_t go_to(const ProductArgs& a, int k0) {
+    const int64_t at = kColumns ? static_cast<int64_t>(k0) * a.cols * 2 : k0 * 2;
+    if constexpr (kColumns && kCut) {
+      while (at >= cut) {
+        ++k;
+        w = w_next;
+        cut += a.part_numel * 2;
+        w_next = beyond(a);
+      }
+    }
+    return at;
+  }
+  // The step at k0, `at` from go_to.
+  __device__ __forceinline__ void load(int k0, int64_t at, char* lds_x, char* lds_w, int wave) const {
+    const char* from = x + k0 * 2;
 #pragma unroll
     for (int j = 0; j < S::kXLoads; ++j)
-      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)(x + x_off[j]),
-                                       (ZR_LDS_AS void*)(lds + (j * S::kThreads + 64 * w) * 16), 16, 0, 0);
-    const int64_t first = p.w + (kColumns ? static_cast<int64_t>(k0) * a.cols + p.col
-                                          : static_cast<int64_t>(p.col) * a.depth + k0);
-    const int64_t span = kColumns ? static_cast<int64_t>(kDepth - 1) * a.cols + p.cols
-                                  : static_cast<int64_t>(p.cols - 1) * a.depth + kDepth;
-    const Source s = source_of(a, first, span);
+      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)(from + x_off[j]),
+                                       (ZR_LDS_AS void*)(lds_x + (j * S::kThreads + 64 * wave) * 16), 16, 0, 0);
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
-      const char* from = (static_cast<int64_t>(w_off[j]) < 2 * s.cut ? s.a : s.b) + w_off[j];
-      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)from,
-                                       (ZR_LDS_AS void*)(lds + S::kXBytes + (j * S::kThreads + 64 * w) * 16), 16,
-                                       0, 0);
+      uintptr_t there = w + at;
+      if constexpr (kCut) there = at + w_off[j] < cut ? there : w_next + at;
+      there += w_off[j];
+      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)reinterpret_cast<const char*>(there),
+                                       (ZR_LDS_AS void*)(lds_w + (j * S::kThreads + 64 * wave) * 16), 16, 0, 0);
     }
   }
 };
 
 template <typename S>
-using Acc = f32x16[S::kColBlocks][S::kRowBlocks];
+using Acc = f32x4[S::kColBlocks][S::kRowBlocks];
 
-// A staged step's products.  The weight is the MFMA's first operand: its
-// columns n are the accumulators' rows, four of them one after the other in a
-// lane, and X's rows the lanes.
+// The fragments of 32 k that a wave multiplies.
+template <typename S>
+struct Fragments {
+  bf16x8 x[S::kRowBlocks], w[S::kColBlocks];
+};
+
+// Reads a staged step.  The weight is the MFMA's first operand: its columns n are
+// the accumulators' rows, four of them one after the other in a lane, and X's
+// rows the lanes.
 template <typename S, bool kColumns>
 struct Reader {
   int x[S::kRowBlocks], w[S::kColBlocks];   // a lane's places in a staged step
@@ -249,48 +292,139 @@ struct Reader {
   __device__ __forceinline__ Reader(int lane_, int wave) : lane(lane_) {
     const int wr = wave / S::kWavesC, wc = wave % S::kWavesC;
 #pragma unroll
-    for (int b = 0; b < S::kRowBlocks; ++b) x[b] = ((wr * S::kRowBlocks + b) * 32 + (lane & 31)) * (kDepth * 2);
-    const int g = lane >> 4, q = lane & 15;
-    const int k = 8 * (g >> 1) + (q >> 2), c = 16 * (g & 1) + 4 * (q & 3);
+    for (int b = 0; b < S::kRowBlocks; ++b) x[b] = ((wr * S::kRowBlocks + b) * 16 + (lane & 15)) * (S::kDepth * 2);
+    const int k = 8 * (lane >> 4) + (lane >> 2 & 3), c = 4 * (lane & 3);
 #pragma unroll
     for (int b = 0; b < S::kColBlocks; ++b) {
       if constexpr (kColumns) {
-        const int at = (wc * S::kColBlocks + b) * 32 + c;
-        w[b] = staged<S::kCols>(k, at / 8) + (at % 8) * 2;
+        const int at = (wc * S::kColBlocks + b) * 16 + c;
+        w[b] = staged_column<S::kCols>(k, at / 8) + (at % 8) * 2;
       } else {
-        w[b] = ((wc * S::kColBlocks + b) * 32 + (lane & 31)) * (kDepth * 2);
+        w[b] = ((wc * S::kColBlocks + b) * 16 + (lane & 15)) * (S::kDepth * 2);
       }
     }
   }
   __device__ __forceinline__ bf16x8 row(const char* lds, int at, int phase) const {
-    const int u = (2 * phase + (lane >> 5)) ^ (lane & 7);
+    const int u = exchanged_row<S::kDepth>(lane & 15, 4 * phase + (lane >> 4));
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lds + at + (u << 4)));
   }
-  __device__ __forceinline__ void multiply(Acc<S>& acc, const char* lds) const {
+  __device__ __forceinline__ void read(Fragments<S>& f, const char* lds_x, const char* lds_w, int phase) const {
 #pragma unroll
-    for (int phase = 0; phase < kDepth / 16; ++phase) {
-      bf16x8 xf[S::kRowBlocks], wf[S::kColBlocks];
+    for (int b = 0; b < S::kRowBlocks; ++b) f.x[b] = row(lds_x, x[b], phase);
 #pragma unroll
-      for (int b = 0; b < S::kRowBlocks; ++b) xf[b] = row(lds, x[b], phase);
-#pragma unroll
-      for (int b = 0; b < S::kColBlocks; ++b) {
-        if constexpr (kColumns)
-          wf[b] = read_columns<S::kCols>(lds + S::kXBytes, w[b] + 16 * phase * (S::kCols * 2));
-        else
-          wf[b] = row(lds + S::kXBytes, w[b], phase);
-      }
-#pragma unroll
-      for (int i = 0; i < S::kColBlocks; ++i)
-#pragma unroll
-        for (int j = 0; j < S::kRowBlocks; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wf[i], xf[j], acc[i][j], 0, 0, 0);
+    for (int b = 0; b < S::kColBlocks; ++b) {
+      if constexpr (kColumns) f.w[b] = read_columns<S::kCols>(lds_w, w[b] + 32 * phase * (S::kCols * 2));
+      else f.w[b] = row(lds_w, w[b], phase);
     }
   }
 };
 
+template <typename S>
+__device__ __forceinline__ void multiply(Acc<S>& acc, const Fragments<S>& f) {
+#pragma unroll
+  for (int i = 0; i < S::kColBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kRowBlocks; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
+}
+template <typename S, bool kColumns>
+__device__ __forceinline__ void multiply_step(Acc<S>& acc, const Reader<S, kColumns>& reader, const char* lds) {
+#pragma unroll
+  for (int phase = 0; phase < S::kPhases; ++phase) {
+    Fragments<S> f;
+    reader.read(f, lds, lds + S::kXBytes, phase);
+    multiply<S>(acc, f);
+  }
+}
+
+// All waves' LDS reads before it are done after it, and all but the last n of a
+// wave's loads have arrived.
 template <int n>
-__device__ __forceinline__ void wait_loads() {   // all but the last n have arrived
-  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0f70);
+__device__ __forceinline__ void meet() {
+  ZR_ORDERED();
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | 0x0070);   // vmcnt(n), lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  ZR_ORDERED();
+}
+
+// 32 k of a step.  While they multiply, the next 32's fragments are read.  Once
+// all waves have a step's fragments, the step that is kStages on goes into its
+// place, its loads between the products: a CU takes a wave's load in 16 cycles,
+// and all waves' at once would hold up the products behind them.  The pointers
+// are restricted so that the compiler sees that reads of a stage need not wait
+// for what goes into another.
+template <int kPhase, typename S, bool kColumns, bool kCut>
+__device__ __forceinline__ void phase(const Direct<S, kColumns, kCut>& in, const Reader<S, kColumns>& reader,
+                                      Acc<S>& acc, const Fragments<S>& now, Fragments<S>& then, int ahead_k,
+                                      int64_t ahead_at, const char* __restrict cur, const char* __restrict next,
+                                      char* __restrict ahead_x, char* __restrict ahead_w, int wave) {
+  constexpr bool kLast = kPhase == S::kPhases - 1;
+  if constexpr (kLast) {
+    meet<(S::kXLoads + S::kWLoads) * (S::kStages - 2)>();
+    reader.read(then, next, next + S::kXBytes, 0);
+    in.load(ahead_k, ahead_at, ahead_x, ahead_w, wave);
+  } else {
+    reader.read(then, cur, cur + S::kXBytes, kPhase + 1);
+  }
+  multiply<S>(acc, now);
+  // Reads behind the first products, loads between them, and nothing over the
+  // phase's end.
+  constexpr int kReads = S::kRowBlocks + S::kColBlocks * (kColumns ? 2 : 1), kProducts = S::kRowBlocks * S::kColBlocks;
+  constexpr int kLoads = kLast ? S::kXLoads + S::kWLoads : 0;
+  constexpr int kBehind = (kReads + kProducts - 1) / kProducts, kApart = kProducts / (kLoads > 0 ? kLoads : 1);
+#pragma unroll
+  for (int i = 0; i < kProducts; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
+    if (i * kBehind < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kBehind, 0);     // LDS read
+    if (kApart > 0 && i % kApart == kApart / 2 && i / kApart < kLoads)
+      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);                                   // load
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+// The whole steps [s, whole) through a ring of stages.
+template <typename S, bool kColumns, bool kCut>
+__device__ __forceinline__ void whole_steps(const ProductArgs& a, const Place& p, const Reader<S, kColumns>& reader,
+                                            Acc<S>& acc, int s, int whole, char* lds, int tid, int wave) {
+  static_assert(S::kPhases == 1 || S::kPhases == 2, "phases in step");
+  Direct<S, kColumns, kCut> in(a, p, s * S::kDepth, tid);
+  // behind the last step, the last is loaded again, unused
+  auto step = [&](int n) { return (n < whole ? n : whole - 1) * S::kDepth; };
+  constexpr int kEnd = S::kStages * S::kStage;
+#pragma unroll
+  for (int i = 0; i < S::kStages; ++i) {
+    char* to = lds + i * S::kStage;
+    const int k = step(s + i);
+    const int64_t at = in.go_to(a, k);
+    in.load(k, at, to, to + S::kXBytes, wave);
+  }
+  meet<(S::kXLoads + S::kWLoads) * (S::kStages - 1)>();
+  Fragments<S> f[2];
+  reader.read(f[0], lds, lds + S::kXBytes, 0);
+  int cur = 0;
+  auto one = [&](Fragments<S>& now, Fragments<S>& then) {
+    const int next = cur + S::kStage == kEnd ? 0 : cur + S::kStage;
+    const int k = step(s + S::kStages);
+    const int64_t at = in.go_to(a, k);
+    char* to = lds + cur;
+    if constexpr (S::kPhases == 1) {
+      phase<0>(in, reader, acc, now, then, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
+    } else {
+      phase<0>(in, reader, acc, now, then, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
+      phase<1>(in, reader, acc, then, now, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
+    }
+    cur = next;
+    return ++s < whole;
+  };
+  if constexpr (S::kPhases == 1) {
+#pragma unroll 1
+    while (one(f[0], f[1]) && one(f[1], f[0])) {
+    }
+  } else {
+#pragma unroll 1
+    while (one(f[0], f[1])) {
+    }
+  }
+  meet<0>();
 }
 
 // Four sums of a lane, at a row of y and columns from n on.
@@ -319,6 +453,56 @@ __device__ __forceinline__ void put_sums(const ProductArgs& a, int64_t row, int6
   }
 }
 
+// A wave's sums into y, 32 rows at a time by way of its own LDS, so that a row's
+// columns leave together: a lane has four of them, of one row.  Rows of LDS are
+// exchanged like staged ones.
+template <typename S, bool kBf16>
+__device__ __forceinline__ void store_tile(const ProductArgs& a, const Place& p, const Acc<S>& acc, char* lds, int lane,
+                                           int wave) {
+  constexpr int kSize = kBf16 ? 2 : 4, kRow = S::kColBlocks * 16 * kSize, kU = kRow / 16, kPer = 16 / kSize;
+  static_assert(2 * 32 * kRow <= S::kStages * S::kStage / (S::kThreads / 64), "a wave's share of the LDS");
+  static_assert((16 % kU == 0 || kU % 16 == 0) && S::kRowBlocks % 2 == 0, "units of a row, rows of a pass");
+  constexpr int kRowsABank = kU < 16 ? 16 / kU : 1;   // rows that the 64 banks hold
+  auto place = [&](int r, int u) { return r * kRow + ((u ^ (r / kRowsABank & ((kU < 16 ? kU : 16) - 1))) << 4); };
+  const int r0 = wave / S::kWavesC * S::kRowBlocks * 16, c0 = wave % S::kWavesC * S::kColBlocks * 16;
+#pragma unroll
+  for (int j = 0; j < S::kRowBlocks / 2; ++j) {
+    if (r0 + 32 * j >= p.rows) break;
+    char* at = lds + (j & 1) * (32 * kRow);
+#pragma unroll
+    for (int i = 0; i < S::kColBlocks; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const f32x4& s = acc[i][2 * j + h];
+        const int r = 16 * h + (lane & 15), q = lane >> 4;
+        if constexpr (kBf16)
+          *reinterpret_cast<u32x2*>(at + place(r, 2 * i + (q >> 1)) + 8 * (q & 1)) =
+              u32x2{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
+        else
+          *reinterpret_cast<f32x4*>(at + place(r, 4 * i + q)) = s;
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int q = 0; q < 32 * kU / 64; ++q) {
+      const int r = q * (64 / kU) + lane / kU, u = lane % kU, c = c0 + u * kPer;
+      const u32x4 v = *reinterpret_cast<const u32x4*>(at + place(r, u));
+      if (r0 + 32 * j + r >= p.rows || c >= p.cols) continue;
+      char* y = static_cast<char*>(a.y) + ((p.row + r0 + 32 * j + r) * a.y_stride + p.col + c) * kSize;
+      if (c + kPer <= p.cols) {
+        store_at<kSize>(y, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < kPer - 1; ++e)
+          if (c + e < p.cols) {
+            if constexpr (kBf16) reinterpret_cast<uint16_t*>(y)[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+            else reinterpret_cast<uint32_t*>(y)[e] = v[e];
+          }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+}
+
 template <typename S, bool kColumns, bool kDirect>
 __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs a) {
   __shared__ __align__(16) char lds[S::kStages * S::kStage];
@@ -331,59 +515,52 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   const int id = round + xcd * (now / 8) + (xcd < more ? xcd : more) + (blockIdx.x - round) / 8;
   const int piece = id / a.tiles, tile = id - piece * a.tiles;
   const Place p = place_of<S>(a, tile);
-  const int64_t all = (a.depth + kDepth - 1) / kDepth;
+  const int64_t all = (a.depth + S::kDepth - 1) / S::kDepth;
   const int s0 = static_cast<int>(piece * all / a.pieces), s1 = static_cast<int>((piece + 1) * all / a.pieces);
   const Reader<S, kColumns> reader(lane, w);
   Acc<S> acc = {};
   int s = s0;
   if constexpr (kDirect) {
-    const int whole = s1 < a.depth / kDepth ? s1 : a.depth / kDepth;
+    const int whole = s1 < a.depth / S::kDepth ? s1 : a.depth / S::kDepth;
     if (s < whole) {
-      const Direct<S, kColumns> in(a, p, tid);
-      // behind the last step, the last is loaded again, unused
-      auto step = [&](int n) { return (n < whole ? n : whole - 1) * kDepth; };
-      constexpr int kAhead = S::kStages - 1, kLoads = S::kXLoads + S::kWLoads;
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) in.load(a, p, step(s + i), lds + i * S::kStage, w);
-      int now_at = 0, next_at = kAhead * S::kStage;
-      for (; s < whole; ++s) {
-        wait_loads<kLoads * (kAhead - 1)>();
-        lds_barrier();
-        in.load(a, p, step(s + kAhead), lds + next_at, w);
-        reader.multiply(acc, lds + now_at);
-        now_at = now_at + S::kStage == S::kStages * S::kStage ? 0 : now_at + S::kStage;
-        next_at = next_at + S::kStage == S::kStages * S::kStage ? 0 : next_at + S::kStage;
-      }
-      wait_loads<0>();
+      // the tile's part of the weight, all of one partition or not
+      const int64_t first = p.w + (kColumns ? 0 : static_cast<int64_t>(p.col) * a.depth);
+      const int64_t end = p.w + (kColumns ? static_cast<int64_t>(a.cols) : p.col + p.cols) * a.depth;
+      if (first / a.part_numel == (end - 1) / a.part_numel)
+        whole_steps<S, kColumns, false>(a, p, reader, acc, s, whole, lds, tid, w);
+      else
+        whole_steps<S, kColumns, true>(a, p, reader, acc, s, whole, lds, tid, w);
+      s = whole;
     }
   }
   if (s < s1) {
     Staged<S> next;
-    load_step<S, kColumns>(next, a, p, s * kDepth, tid);
+    load_step<S, kColumns>(next, a, p, s * S::kDepth, tid);
     for (; s < s1; ++s) {
       lds_barrier();
       store_step<S, kColumns>(next, lds, tid);
       lds_barrier();
-      if (s + 1 < s1) load_step<S, kColumns>(next, a, p, (s + 1) * kDepth, tid);
-      reader.multiply(acc, lds);
+      if (s + 1 < s1) load_step<S, kColumns>(next, a, p, (s + 1) * S::kDepth, tid);
+      multiply_step<S, kColumns>(acc, reader, lds);
     }
+  }
+  if (a.pieces == 1) {
+    lds_barrier();             // the stages are read
+    char* own = lds + w * (S::kStages * S::kStage / (S::kThreads / 64));
+    if (a.y_bf16) store_tile<S, true>(a, p, acc, own, lane, w);
+    else store_tile<S, false>(a, p, acc, own, lane, w);
+    return;
   }
   const int wr = w / S::kWavesC, wc = w % S::kWavesC;
 #pragma unroll
   for (int j = 0; j < S::kRowBlocks; ++j) {
-    const int r = (wr * S::kRowBlocks + j) * 32 + (lane & 31);
+    const int r = (wr * S::kRowBlocks + j) * 16 + (lane & 15);
     if (r >= p.rows) continue;
 #pragma unroll
-    for (int i = 0; i < S::kColBlocks; ++i)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const f32x4 sums = {acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
-        const int c = (wc * S::kColBlocks + i) * 32 + 8 * v + 4 * (lane >> 5);
-        if (a.pieces > 1)
-          *as_global<f32x4>(a.partial + static_cast<int64_t>(id) * (S::kRows * S::kCols) + r * S::kCols + c) = sums;
-        else if (c < p.cols)
-          put_sums(a, p.row + r, p.col + c, sums);
-      }
+    for (int i = 0; i < S::kColBlocks; ++i) {
+      const int c = (wc * S::kColBlocks + i) * 16 + 4 * (lane >> 4);
+      *as_global<f32x4>(a.partial + static_cast<int64_t>(id) * (S::kRows * S::kCols) + r * S::kCols + c) = acc[i][j];
+    }
   }
 }
 
@@ -404,8 +581,8 @@ __global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const Produc
   put_sums(a, p.row + r, p.col + c, sum);
 }
 
-using Large = Shape<256, 256, 2, 4, 2>;
-using Small = Shape<32, 128, 1, 4, 4>;
+using Large = Shape<256, 256, 2, 4, 64, 2>;
+using Small = Shape<32, 128, 1, 4, 64, 4>;
 
 // ---------------------------------------------------------------------- host
 
@@ -445,7 +622,7 @@ void add_launches(const ProductArgs& shared, const std::vector<Group>& groups, b
       tiles += more;
     }
     l.a.tiles = static_cast<int32_t>(std::min(tiles, kMaxTiles + 1));
-    l.a.pieces = pieces_of(tiles, ceil_div(shared.depth, kDepth), small ? 2 * kCus : kCus);
+    l.a.pieces = pieces_of(tiles, ceil_div(shared.depth, S::kDepth), small ? 2 * kCus : kCus);
     l.bytes = l.a.pieces > 1 ? tiles * l.a.pieces * (S::kRows * S::kCols * 4) : 0;
     out->push_back(l);
   }
@@ -553,12 +730,14 @@ zr_status run_product(const zr_plan* plan, const int64_t* params, const int64_t*
       a.y = y;
       a.partial = static_cast<float*>(workspace);
       a.part_numel = gi.part;
+      a.world = gi.world;
       a.x_stride = x_stride;
       a.y_stride = y_stride;
       a.y_bf16 = y_dtype == ZR_BF16;
       // a step's part of the weight, in two partitions at most
       const int64_t wide = columns ? cols : depth;
-      const int64_t span = columns ? kDepth * cols : (l.small ? Small::kCols : Large::kCols) * depth;
+      const int64_t span = columns ? (l.small ? Small::kDepth : Large::kDepth) * cols
+                                   : (l.small ? Small::kCols : Large::kCols) * depth;
       const bool direct = aligned && aligned_to(x, 16) && x_stride % 8 == 0 && wide % 8 == 0 && span <= gi.part;
       st = l.small ? launch_product<Small>(a, columns, direct, stream)
                    : launch_product<Large>(a, columns, direct, stream);
