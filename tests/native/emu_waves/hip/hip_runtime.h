@@ -27,6 +27,7 @@
 #define ZR_GLOBAL_AS
 #define ZR_LDS_AS
 #define ZR_OPAQUE(x) ((void)(x))
+#define ZR_OPAQUE_IN(x, y) ((void)(x))
 #define ZR_ORDERED() ((void)0)
 
 struct zr_emu_dim {
@@ -60,7 +61,7 @@ void zr_emu_launch(void (*kernel)(Args), dim3 grid, unsigned block, const Args& 
 
 // --------------------------------------------------------- wave operations
 
-enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync, kExchange, kMfmaFlat };
+enum zr_emu_op { kFirstLane, kReadLane, kBallot, kShiftUp, kQuadPerm, kTranspose, kMfma, kWaveSync, kExchange, kMfmaFlat, kSwapRows };
 // Gives the lane's input to the operation and returns its result.
 void zr_emu_wave(zr_emu_op op, const void* in, size_t in_bytes, void* out, size_t out_bytes);
 void zr_emu_barrier();
@@ -171,6 +172,15 @@ inline void zr_emu_load_lds(const void* p, void* lds, int bytes, int, int) {
   std::memcpy(v, p, 16);
   zr_emu_lds_later(lds, v);
 }
+using zr_emu_u32x2 = uint32_t __attribute__((ext_vector_type(2)));
+inline zr_emu_u32x2 zr_emu_swap_rows(uint32_t x, uint32_t y) {
+  const uint32_t in[2] = {x, y};
+  zr_emu_u32x2 r;
+  zr_emu_wave(kSwapRows, in, sizeof(in), &r, sizeof(r));
+  return r;
+}
+#define __builtin_amdgcn_permlane16_swap(x, y, fetch, bound) zr_emu_swap_rows((x), (y))
+#define __builtin_amdgcn_rcpf(x) (1.0f / (x))
 #define __builtin_amdgcn_exp2f(x) std::exp2(static_cast<float>(x))
 #define __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, old, high) zr_emu_cvt_pk_fp8((lo), (hi), (old), (high))
 #define __builtin_amdgcn_cvt_pk_f32_fp8(codes, high) zr_emu_cvt_pk_f32((codes), (high))

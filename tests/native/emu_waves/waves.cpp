@@ -191,6 +191,14 @@ void finish(unsigned base, uint64_t live) {
       case kExchange:
         out_of(lane, in_of<int>(there(i ^ static_cast<unsigned>(in_of<int>(lane, 1)), lane)));
         break;
+      case kSwapRows: {
+        // rows of sixteen lanes: the odd ones' first for the even ones' second
+        int r[2];
+        r[0] = i & 16 ? in_of<int>(there(i - 16, lane), 1) : x;
+        r[1] = i & 16 ? in_of<int>(lane, 1) : in_of<int>(there(i + 16, lane));
+        std::memcpy(g_lanes[lane].out, r, 8);
+        break;
+      }
       case kTranspose: {
         short r[4];
         for (unsigned j = 0; j < 4; ++j)

@@ -25,6 +25,8 @@ using bf16x2 = __bf16 __attribute__((ext_vector_type(2)));
 #define ZR_LAUNCH(grid, block, stream, args, ...) __VA_ARGS__<<<(grid), (block), 0, (stream)>>>(args)
 // What is worked out from x before is not kept for use behind it.
 #define ZR_OPAQUE(x) asm volatile("" : "+v"(x))
+// The same for each value of the uniform y, and no bar to the order of others.
+#define ZR_OPAQUE_IN(x, y) asm("" : "+v"(x) : "s"(y))
 // No access to memory moves over it.
 #define ZR_ORDERED() asm volatile("" ::: "memory")
 #endif
@@ -57,6 +59,11 @@ template <int kAlign, typename V>
 __device__ __forceinline__ void store_at(void* p, V v) {
   typedef V __attribute__((aligned(kAlign))) U;
   *(ZR_GLOBAL_AS U*)p = v;
+}
+template <int kAlign, typename V>
+__device__ __forceinline__ void store_once_at(void* p, V v) {   // past the caches
+  typedef V __attribute__((aligned(kAlign))) U;
+  __builtin_nontemporal_store(v, (ZR_GLOBAL_AS U*)p);
 }
 
 __device__ __forceinline__ float bits_float(uint32_t u) { return __builtin_bit_cast(float, u); }

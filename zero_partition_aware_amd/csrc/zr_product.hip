@@ -5,6 +5,7 @@
 // (n = out, k = in) or the gradient of its input (n = in, k = out).  Depending
 // on how the weight is stored, k or n is its fast axis; X's is k.
 
+#include <type_traits>
 #include <vector>
 
 #include "zr_tiles.h"
@@ -27,11 +28,12 @@ struct ProductArgs {
   void* y;
   float* partial;              // a tile of sums for each piece
   int64_t part_numel;
+  double part_inverse;
   int64_t x_stride, y_stride;
   int32_t n;                   // groups
   int32_t depth, cols;         // k's and n's extent
   int32_t col_tiles, tiles, pieces;
-  int32_t y_bf16, world;
+  int32_t y_bf16, y_past, world;   // y_past: y goes past the caches
 };
 
 // A workgroup's tile of rows and columns, by waves of 16 x 16 blocks, and the
@@ -46,6 +48,7 @@ struct Shape {
   static constexpr int kXBytes = kRows * kDepth * 2, kWBytes = kCols * kDepth * 2;
   static constexpr int kStage = kXBytes + kWBytes;
   static constexpr int kXLoads = kXBytes / 16 / kThreads, kWLoads = kWBytes / 16 / kThreads;
+  static constexpr int kLds = kStages * kStage;
   static_assert(kXLoads * kThreads * 16 == kXBytes && kWLoads * kThreads * 16 == kWBytes, "staging shape");
 };
 
@@ -121,6 +124,14 @@ __device__ __forceinline__ int exchanged_column(int k, int u) { return u ^ (4 * 
 template <int C>
 __device__ __forceinline__ int staged_column(int k, int u) { return k * (C * 2) + (exchanged_column(k, u) << 4); }
 
+// a / b for 0 <= a < 2^23 and b > 0, in a few instructions.
+__device__ __forceinline__ int quotient(int a, int b) {
+  int q = static_cast<int>(static_cast<float>(a) * __builtin_amdgcn_rcpf(static_cast<float>(b)));
+  q = uniform(q);              // off by one at most: |error| < 2^23 * 2^-22 / b + 1
+  const int left = a - q * b;
+  return left < 0 ? q - 1 : left >= b ? q + 1 : q;
+}
+
 // A tile's place.
 struct Place {
   const uint16_t* x;           // its first row
@@ -140,9 +151,10 @@ __device__ __forceinline__ Place place_of(const ProductArgs& a, int tile) {
   const Group& g = a.group[lo];
   // bands of eight tiles of rows, walked along the columns
   const int t = tile - g.tile0, row_tiles = (g.rows + S::kRows - 1) / S::kRows;
-  const int band = t / (8 * a.col_tiles), at = t - band * 8 * a.col_tiles;
+  const int band = quotient(t, 8 * a.col_tiles), at = t - band * 8 * a.col_tiles;
   const int height = row_tiles - 8 * band < 8 ? row_tiles - 8 * band : 8;
-  const int r = (8 * band + at % height) * S::kRows, c = at / height * S::kCols;
+  const int over = quotient(at, height);
+  const int r = (8 * band + at - over * height) * S::kRows, c = over * S::kCols;
   Place p;
   p.row = static_cast<int64_t>(g.row0) + r;
   p.x = a.x + p.row * a.x_stride;
@@ -201,52 +213,79 @@ __device__ __forceinline__ void store_step(const Staged<S>& s, char* lds, int ti
   }
 }
 
-// Whole steps straight into LDS: rows and partitions on 16 bytes, a tile's part
-// of the weight (where n is its fast axis, a step's) in two partitions at most,
-// or all in one (kCut false).
-// Where a row or column is behind the last, the tile's first is read instead; it
-// is never stored.
-template <typename S, bool kColumns, bool kCut>
+// What a unit behind the last k is read from.
+__device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+// A thread's unit of each of the kGroups groups of kHigh rows of a step, as bytes:
+// the group's are a uniform number, the thread's one of two, in a group that is
+// all there and in the one that the last row is in.  Where a row is behind the
+// last, one before it is read instead; it is never stored.
+template <int kHigh>
+struct RowUnits {
+  uint32_t all, some;          // the thread's
+  uint32_t step;               // bytes a row
+  int32_t rows;
+  __device__ __forceinline__ RowUnits(int r, int u, int rows_, int64_t step_)
+      : step(static_cast<uint32_t>(step_)), rows(rows_) {
+    const int last = (rows - 1) % kHigh;
+    all = r * step + u * 16;
+    some = (r < last ? r : last) * step + u * 16;
+  }
+  __device__ __forceinline__ uint32_t group(int j) const { return (j * kHigh < rows ? j * kHigh : 0) * step; }
+  __device__ __forceinline__ uint32_t unit(int j) const {
+    return (j * kHigh < rows ? (j + 1) * kHigh : kHigh) > rows ? some : all;
+  }
+};
+
+// Steps straight into LDS: rows and partitions on 16 bytes, a tile's part of the
+// weight (where n is its fast axis, a step's) in two partitions at most.
+template <typename S, bool kColumns>
 struct Direct {
-  uint32_t x_off[S::kXLoads], w_off[S::kWLoads];   // a thread's bytes from a step's start
+  static constexpr int kXHigh = S::kThreads / S::kUnits;
+  static constexpr int kWWide = kColumns ? S::kCols / 8 : S::kUnits, kWHigh = S::kThreads / kWWide;
+  RowUnits<kXHigh> xu;
+  RowUnits<kWHigh> wu;         // where n is the weight's fast axis all its rows are there
   const char* x;               // step 0 of the rows
   uintptr_t w;                 // and of the weight, as if all of it lay in partition k
   uintptr_t w_next;            // in partition k + 1
   int64_t cut;                 // bytes from step 0 to that partition
   int32_t k;
-  __device__ __forceinline__ Direct(const ProductArgs& a, const Place& p, int k0, int tid) {
-#pragma unroll
-    for (int j = 0; j < S::kXLoads; ++j) {
-      const int at = j * S::kThreads + tid, r = at / S::kUnits, u = exchanged_row<S::kDepth>(r, at % S::kUnits);
-      x_off[j] = (r < p.rows ? r : 0) * static_cast<uint32_t>(a.x_stride * 2) + u * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < S::kWLoads; ++j) {
-      if constexpr (kColumns) {
-        constexpr int kPerRow = S::kCols / 8;
-        const int at = j * S::kThreads + tid, r = at / kPerRow, u = exchanged_column(r, at % kPerRow);
-        w_off[j] = r * static_cast<uint32_t>(a.cols * 2) + (8 * u < p.cols ? u : 0) * 16;
-      } else {
-        const int at = j * S::kThreads + tid, r = at / S::kUnits, u = exchanged_row<S::kDepth>(r, at % S::kUnits);
-        w_off[j] = (r < p.cols ? r : 0) * static_cast<uint32_t>(a.depth * 2) + u * 16;
-      }
-    }
-    x = reinterpret_cast<const char*>(p.x);
+  bool whole;                  // all of the tile's part lies in partition k
+  __device__ __forceinline__ Direct(const ProductArgs& a, const Place& p, int k0, int tid)
+      : xu(tid / S::kUnits, x_unit(tid), p.rows, a.x_stride * 2),
+        wu(tid / kWWide, kColumns && 8 * w_unit(tid) >= p.cols ? 0 : w_unit(tid), kColumns ? S::kDepth : p.cols,
+           (kColumns ? a.cols : a.depth) * 2) {
+    x = reinterpret_cast<const char*>(uniform(reinterpret_cast<int64_t>(p.x)));
     const int64_t first = p.w + (kColumns ? p.col : static_cast<int64_t>(p.col) * a.depth);
     const int64_t here = first + (kColumns ? static_cast<int64_t>(k0) * a.cols : 0);
-    k = static_cast<int>(here / a.part_numel);
+    // off by one at most: the estimate has 53 bits
+    k = uniform(static_cast<int>(static_cast<double>(here) * a.part_inverse));
+    if (here < k * a.part_numel) --k;
+    if (here >= (k + 1) * a.part_numel) ++k;
     cut = ((k + 1) * a.part_numel - first) * 2;
-    w = reinterpret_cast<uintptr_t>(a.part[k]) + (first - k * a.part_numel) * 2;
+    w = uniform(static_cast<int64_t>(reinterpret_cast<uintptr_t>(a.part[k]) + (first - k * a.part_numel) * 2));
     w_next = beyond(a);
+    whole = (kColumns ? static_cast<int64_t>(a.depth - 1) * a.cols + p.cols : static_cast<int64_t>(p.cols) * a.depth) * 2 <= cut;
+  }
+  // The unit of its row that a thread has in every group.
+  static __device__ __forceinline__ int x_unit(int tid) {
+    static_assert(kXHigh % 16 == 0, "the exchange is the same in each group");
+    return exchanged_row<S::kDepth>(tid / S::kUnits, tid % S::kUnits);
+  }
+  static __device__ __forceinline__ int w_unit(int tid) {
+    static_assert(kWHigh % 16 == 0, "the exchange is the same in each group");
+    if constexpr (kColumns) return exchanged_column(tid / kWWide, tid % kWWide);
+    else return exchanged_row<S::kDepth>(tid / kWWide, tid % kWWide);
   }
   __device__ __forceinline__ uintptr_t beyond(const ProductArgs& a) const {
     return k + 1 < a.world ? reinterpret_cast<uintptr_t>(a.part[k + 1]) - cut : 0;
   }
   // Where the weight's step at k0 lies: steps go on.
+  template <bool kAny>
   __device__ __forceinline__ int64_t go_to(const ProductArgs& a, int k0) {
     const int64_t at = kColumns ? static_cast<int64_t>(k0) * a.cols * 2 : k0 * 2;
-    if constexpr (kColumns && kCut) {
-      while (at >= cut) {
+    if constexpr (kColumns && kAny) {
+      while (at >= cut && k + 1 < a.world) {
         ++k;
         w = w_next;
         cut += a.part_numel * 2;
@@ -255,18 +294,35 @@ struct Direct {
     }
     return at;
   }
-  // The step at k0, `at` from go_to.
-  __device__ __forceinline__ void load(int k0, int64_t at, char* lds_x, char* lds_w, int wave) const {
-    const char* from = x + k0 * 2;
+  // The step at k0, `at` from go_to.  kAny: of a tile that a partition's end cuts
+  // perhaps, perhaps the last, with fewer than kDepth k.
+  template <bool kAny>
+  __device__ __forceinline__ void load(const ProductArgs& a, int k0, int64_t at, char* lds_x, char* lds_w, int tid,
+                                       int wave) const {
+    const uintptr_t zeros = reinterpret_cast<uintptr_t>(&kZeros);
+    const int left = a.depth - k0;
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(x) + k0 * 2;
 #pragma unroll
-    for (int j = 0; j < S::kXLoads; ++j)
-      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)(from + x_off[j]),
+    for (int j = 0; j < S::kXLoads; ++j) {
+      // (a uniform address and 32 bits of a lane's, not their sum kept in 64)
+      uint32_t off = xu.unit(j);
+      ZR_OPAQUE_IN(off, k0);
+      uintptr_t there = rows + xu.group(j) + off;
+      if constexpr (kAny)
+        if (8 * x_unit(tid) >= left) there = zeros;
+      __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)reinterpret_cast<const char*>(there),
                                        (ZR_LDS_AS void*)(lds_x + (j * S::kThreads + 64 * wave) * 16), 16, 0, 0);
+    }
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
-      uintptr_t there = w + at;
-      if constexpr (kCut) there = at + w_off[j] < cut ? there : w_next + at;
-      there += w_off[j];
+      uint32_t off = wu.unit(j);
+      ZR_OPAQUE_IN(off, k0);
+      const int64_t of_group = at + wu.group(j);
+      uintptr_t there = w + of_group;
+      if constexpr (kAny) there = of_group + off < cut ? there : w_next + of_group;
+      there += off;
+      if constexpr (kAny)
+        if ((kColumns ? j * kWHigh + tid / kWWide : 8 * w_unit(tid)) >= left) there = zeros;
       __builtin_amdgcn_global_load_lds((const ZR_GLOBAL_AS void*)reinterpret_cast<const char*>(there),
                                        (ZR_LDS_AS void*)(lds_w + (j * S::kThreads + 64 * wave) * 16), 16, 0, 0);
     }
@@ -287,35 +343,36 @@ struct Fragments {
 // rows the lanes.
 template <typename S, bool kColumns>
 struct Reader {
-  int x[S::kRowBlocks], w[S::kColBlocks];   // a lane's places in a staged step
-  int lane;
-  __device__ __forceinline__ Reader(int lane_, int wave) : lane(lane_) {
+  int x, w;                    // a lane's places in the first blocks of a staged step
+  __device__ __forceinline__ Reader(int lane, int wave) {
     const int wr = wave / S::kWavesC, wc = wave % S::kWavesC;
-#pragma unroll
-    for (int b = 0; b < S::kRowBlocks; ++b) x[b] = ((wr * S::kRowBlocks + b) * 16 + (lane & 15)) * (S::kDepth * 2);
-    const int k = 8 * (lane >> 4) + (lane >> 2 & 3), c = 4 * (lane & 3);
-#pragma unroll
-    for (int b = 0; b < S::kColBlocks; ++b) {
-      if constexpr (kColumns) {
-        const int at = (wc * S::kColBlocks + b) * 16 + c;
-        w[b] = staged_column<S::kCols>(k, at / 8) + (at % 8) * 2;
-      } else {
-        w[b] = ((wc * S::kColBlocks + b) * 16 + (lane & 15)) * (S::kDepth * 2);
-      }
+    const int u = exchanged_row<S::kDepth>(lane & 15, lane >> 4) << 4;
+    x = (wr * S::kRowBlocks * 16 + (lane & 15)) * (S::kDepth * 2) + u;
+    if constexpr (kColumns) {
+      const int k = 8 * (lane >> 4) + (lane >> 2 & 3), c = wc * S::kColBlocks * 16 + 4 * (lane & 3);
+      w = staged_column<S::kCols>(k, c / 8) + (c % 8) * 2;
+    } else {
+      w = (wc * S::kColBlocks * 16 + (lane & 15)) * (S::kDepth * 2) + u;
     }
   }
-  __device__ __forceinline__ bf16x8 row(const char* lds, int at, int phase) const {
-    const int u = exchanged_row<S::kDepth>(lane & 15, 4 * phase + (lane >> 4));
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(lds + at + (u << 4)));
+  // Blocks lie 16 rows apart, the same exchange in each; four units on is the
+  // units' bit 2.
+  static __device__ __forceinline__ bf16x8 row(const char* lds, int at, int b, int phase) {
+    return __builtin_bit_cast(
+        bf16x8, *reinterpret_cast<const u32x4*>(lds + (at ^ (phase << 6)) + b * (16 * S::kDepth * 2)));
   }
-  __device__ __forceinline__ void read(Fragments<S>& f, const char* lds_x, const char* lds_w, int phase) const {
+  __device__ __forceinline__ bf16x8 read_x(const char* lds_x, int b, int phase) const { return row(lds_x, x, b, phase); }
+  __device__ __forceinline__ bf16x8 read_w(const char* lds_w, int b, int phase) const {
+    static_assert(S::kColBlocks <= 4 && (S::kColBlocks & (S::kColBlocks - 1)) == 0, "a block is two units: bits 1 and 2");
+    if constexpr (kColumns) return read_columns<S::kCols>(lds_w, (w ^ (b << 5)) + 32 * phase * (S::kCols * 2));
+    else return row(lds_w, w, b, phase);
+  }
+  // All of a phase's.
+  __device__ __forceinline__ void read(Fragments<S>& f, const char* lds, int phase) const {
 #pragma unroll
-    for (int b = 0; b < S::kRowBlocks; ++b) f.x[b] = row(lds_x, x[b], phase);
+    for (int b = 0; b < S::kRowBlocks; ++b) f.x[b] = read_x(lds, b, phase);
 #pragma unroll
-    for (int b = 0; b < S::kColBlocks; ++b) {
-      if constexpr (kColumns) f.w[b] = read_columns<S::kCols>(lds_w, w[b] + 32 * phase * (S::kCols * 2));
-      else f.w[b] = row(lds_w, w[b], phase);
-    }
+    for (int b = 0; b < S::kColBlocks; ++b) f.w[b] = read_w(lds + S::kXBytes, b, phase);
   }
 };
 
@@ -326,15 +383,6 @@ __device__ __forceinline__ void multiply(Acc<S>& acc, const Fragments<S>& f) {
 #pragma unroll
     for (int j = 0; j < S::kRowBlocks; ++j)
       acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.w[i], f.x[j], acc[i][j], 0, 0, 0);
-}
-template <typename S, bool kColumns>
-__device__ __forceinline__ void multiply_step(Acc<S>& acc, const Reader<S, kColumns>& reader, const char* lds) {
-#pragma unroll
-  for (int phase = 0; phase < S::kPhases; ++phase) {
-    Fragments<S> f;
-    reader.read(f, lds, lds + S::kXBytes, phase);
-    multiply<S>(acc, f);
-  }
 }
 
 // All waves' LDS reads before it are done after it, and all but the last n of a
@@ -347,221 +395,232 @@ __device__ __forceinline__ void meet() {
   ZR_ORDERED();
 }
 
-// 32 k of a step.  While they multiply, the next 32's fragments are read.  Once
-// all waves have a step's fragments, the step that is kStages on goes into its
-// place, its loads between the products: a CU takes a wave's load in 16 cycles,
-// and all waves' at once would hold up the products behind them.  The pointers
-// are restricted so that the compiler sees that reads of a stage need not wait
-// for what goes into another.
-template <int kPhase, typename S, bool kColumns, bool kCut>
-__device__ __forceinline__ void phase(const Direct<S, kColumns, kCut>& in, const Reader<S, kColumns>& reader,
-                                      Acc<S>& acc, const Fragments<S>& now, Fragments<S>& then, int ahead_k,
-                                      int64_t ahead_at, const char* __restrict cur, const char* __restrict next,
-                                      char* __restrict ahead_x, char* __restrict ahead_w, int wave) {
+// 32 k of a step.  While they multiply, the next 32's fragments are read: one of
+// the rows' behind the products of the one before it, so that their registers are
+// the next one's but one, and the last is there when it is wanted.  Once all waves
+// have a step's fragments, the step that is kStages on goes into its place, its
+// loads between the products: a CU takes a wave's load in 16 cycles, and all
+// waves' at once would hold up the products behind them.  The pointers are
+// restricted so that the compiler sees that reads of a stage need not wait for
+// what goes into another.
+template <int kPhase, bool kAny, typename S, bool kColumns>
+__device__ __forceinline__ void phase(const ProductArgs& a, const Direct<S, kColumns>& in,
+                                      const Reader<S, kColumns>& reader, Acc<S>& acc, const Fragments<S>& now,
+                                      Fragments<S>& then, int ahead_k, int64_t ahead_at,
+                                      const char* __restrict from_x, const char* __restrict from_w,
+                                      char* __restrict ahead_x, char* __restrict ahead_w, int tid, int wave) {
   constexpr bool kLast = kPhase == S::kPhases - 1;
+  constexpr int kThen = kLast ? 0 : kPhase + 1;
+  constexpr int kLoads = kLast ? S::kXLoads + S::kWLoads : 0;
+  static_assert(S::kColBlocks <= S::kRowBlocks, "the weight's fragments behind as many products");
   if constexpr (kLast) {
     meet<(S::kXLoads + S::kWLoads) * (S::kStages - 2)>();
-    reader.read(then, next, next + S::kXBytes, 0);
-    in.load(ahead_k, ahead_at, ahead_x, ahead_w, wave);
-  } else {
-    reader.read(then, cur, cur + S::kXBytes, kPhase + 1);
+    in.template load<kAny>(a, ahead_k, ahead_at, ahead_x, ahead_w, tid, wave);
   }
-  multiply<S>(acc, now);
-  // Reads behind the first products, loads between them, and nothing over the
-  // phase's end.
-  constexpr int kReads = S::kRowBlocks + S::kColBlocks * (kColumns ? 2 : 1), kProducts = S::kRowBlocks * S::kColBlocks;
-  constexpr int kLoads = kLast ? S::kXLoads + S::kWLoads : 0;
-  constexpr int kBehind = (kReads + kProducts - 1) / kProducts, kApart = kProducts / (kLoads > 0 ? kLoads : 1);
+  then.x[0] = reader.read_x(from_x, 0, kThen);
 #pragma unroll
-  for (int i = 0; i < kProducts; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                     // MFMA
-    if (i * kBehind < kReads) __builtin_amdgcn_sched_group_barrier(0x100, kBehind, 0);     // LDS read
-    if (kApart > 0 && i % kApart == kApart / 2 && i / kApart < kLoads)
-      __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);                                   // load
+  for (int j = 0; j < S::kRowBlocks; ++j) {
+#pragma unroll
+    for (int i = 0; i < S::kColBlocks; ++i)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(now.w[i], now.x[j], acc[i][j], 0, 0, 0);
+    if (j + 1 < S::kRowBlocks) then.x[j + 1] = reader.read_x(from_x, j + 1, kThen);
+    if (j < S::kColBlocks) then.w[j] = reader.read_w(from_w, j, kThen);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                                               // LDS read
+#pragma unroll
+  for (int j = 0; j < S::kRowBlocks; ++j) {
+    __builtin_amdgcn_sched_group_barrier(0x008, S::kColBlocks, 0);                                 // MFMAs
+    if (j < S::kColBlocks) __builtin_amdgcn_sched_group_barrier(0x100, kColumns ? 3 : 2, 0);       // LDS reads
+    else if (j + 1 < S::kRowBlocks) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    constexpr int kEach = (kLoads + S::kRowBlocks - 1) / S::kRowBlocks;
+    if (kEach > 0 && j * kEach < kLoads) __builtin_amdgcn_sched_group_barrier(0x010, kEach, 0);    // loads
   }
   __builtin_amdgcn_sched_barrier(0);
 }
-// The whole steps [s, whole) through a ring of stages.
-template <typename S, bool kColumns, bool kCut>
-__device__ __forceinline__ void whole_steps(const ProductArgs& a, const Place& p, const Reader<S, kColumns>& reader,
-                                            Acc<S>& acc, int s, int whole, char* lds, int tid, int wave) {
-  static_assert(S::kPhases == 1 || S::kPhases == 2, "phases in step");
-  Direct<S, kColumns, kCut> in(a, p, s * S::kDepth, tid);
-  // behind the last step, the last is loaded again, unused
-  auto step = [&](int n) { return (n < whole ? n : whole - 1) * S::kDepth; };
-  constexpr int kEnd = S::kStages * S::kStage;
+
+// A piece of a tile: steps [s0, s1) of its sums.
+struct Work {
+  Place p;
+  int s0, s1, id;
+};
+template <typename S>
+__device__ __forceinline__ Work work_of(const ProductArgs& a, int block) {
+  // Consecutive workgroups go round the eight XCDs: of 256, each XCD takes 32
+  // neighbours, which share rows in its L2.
+  const int all = a.tiles * a.pieces, round = block & ~255, now = all - round < 256 ? all - round : 256;
+  const int xcd = block % 8, more = now % 8;
+  Work w;
+  w.id = round + xcd * (now / 8) + (xcd < more ? xcd : more) + (block - round) / 8;
+  const int piece = a.pieces > 1 ? w.id / a.tiles : 0;
+  w.p = place_of<S>(a, w.id - piece * a.tiles);
+  const int64_t steps = (a.depth + S::kDepth - 1) / S::kDepth;
+  w.s0 = 0;
+  w.s1 = static_cast<int>(steps);
+  if (a.pieces > 1) {
+    w.s0 = static_cast<int>(piece * steps / a.pieces);
+    w.s1 = static_cast<int>((piece + 1) * steps / a.pieces);
+  }
+  return w;
+}
+
+// kN sums of a lane, at a row of y and columns from c on, `left` of which are there.
+template <int kN>
+__device__ __forceinline__ void put_sums(const ProductArgs& a, int64_t at, int left, const u32x4& v) {   // bf16 or fp32
+  constexpr int kSize = 16 / kN;
+  char* p = static_cast<char*>(a.y) + at * kSize;
+  if (left >= kN) {
+    if (a.y_past) store_once_at<kSize>(p, v);
+    else store_at<kSize>(p, v);
+  } else {
 #pragma unroll
+    for (int e = 0; e < kN - 1; ++e)
+      if (e < left) {
+        if constexpr (kN == 8) reinterpret_cast<uint16_t*>(p)[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+        else reinterpret_cast<uint32_t*>(p)[e] = v[e];
+      }
+  }
+}
+
+// A piece's sums: into y, or, where there are others of its tile, into the
+// workspace.  A lane has four columns of a row: 16 bytes of fp32.  For bf16 it
+// exchanges four of one block for four of the next with the lane that has that
+// row's following columns, so that both have eight.
+template <typename S>
+__device__ __forceinline__ void put_tile(const ProductArgs& a, const Work& k, const Acc<S>& acc, int lane, int wave) {
+  ZR_OPAQUE(lane);             // places are worked out here, not kept over the products
+  const int r0 = wave / S::kWavesC * S::kRowBlocks * 16, c0 = wave % S::kWavesC * S::kColBlocks * 16;
+  const int q = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < S::kRowBlocks; ++j) {
+    const int r = r0 + 16 * j + (lane & 15);
+    const bool there = r < k.p.rows;
+    const int64_t at = (k.p.row + r) * a.y_stride + k.p.col;
+#pragma unroll
+    for (int i = 0; i < S::kColBlocks; i += 2) {
+      if (a.pieces > 1 || !a.y_bf16) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = c0 + 16 * (i + h) + 4 * q;
+          if (!there) continue;
+          if (a.pieces > 1)
+            *as_global<f32x4>(a.partial + static_cast<int64_t>(k.id) * (S::kRows * S::kCols) + r * S::kCols + c) =
+                acc[i + h][j];
+          else
+            put_sums<4>(a, at + c, k.p.cols - c, __builtin_bit_cast(u32x4, acc[i + h][j]));
+        }
+      } else {
+        const f32x4 &s = acc[i][j], &t = acc[i + 1][j];
+        const u32x2 lo = exchange_rows(pack_bf16(s[0], s[1]), pack_bf16(t[0], t[1]));
+        const u32x2 hi = exchange_rows(pack_bf16(s[2], s[3]), pack_bf16(t[2], t[3]));
+        const int c = c0 + 16 * (i + (q & 1)) + 8 * (q >> 1);
+        if (there) put_sums<8>(a, at + c, k.p.cols - c, u32x4{lo[0], hi[0], lo[1], hi[1]});
+      }
+    }
+  }
+}
+
+template <typename S>
+__device__ __forceinline__ void clear(Acc<S>& acc) {
+#pragma unroll
+  for (int i = 0; i < S::kColBlocks; ++i)
+#pragma unroll
+    for (int j = 0; j < S::kRowBlocks; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+}
+
+// Rows and partitions on 16 bytes.  A workgroup goes through its pieces in one
+// stream of steps: while a piece's last steps multiply, and while its sums leave,
+// the next one's first are on their way.  (Each piece has a step for every stage,
+// behind its last k of zeros.)
+template <typename S, bool kColumns>
+__global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs a) {
+  static_assert(S::kPhases == 2, "phases in step");
+  __shared__ __align__(16) char lds[S::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const int all = a.tiles * a.pieces;
+  int block = blockIdx.x;
+  Work now = work_of<S>(a, block);
+  Direct<S, kColumns> in(a, now.p, now.s0 * S::kDepth, tid);
+  constexpr int kEnd = S::kStages * S::kStage;
+  auto steps_end = [](const Work& k) { return k.s1 - k.s0 < S::kStages ? k.s0 + S::kStages : k.s1; };
+#pragma unroll 1
   for (int i = 0; i < S::kStages; ++i) {
     char* to = lds + i * S::kStage;
-    const int k = step(s + i);
-    const int64_t at = in.go_to(a, k);
-    in.load(k, at, to, to + S::kXBytes, wave);
+    const int k = (now.s0 + i) * S::kDepth;
+    const int64_t at = in.template go_to<true>(a, k);
+    in.template load<true>(a, k, at, to, to + S::kXBytes, tid, wave);
   }
   meet<(S::kXLoads + S::kWLoads) * (S::kStages - 1)>();
+  const Reader<S, kColumns> reader(lane, wave);
   Fragments<S> f[2];
-  reader.read(f[0], lds, lds + S::kXBytes, 0);
+  reader.read(f[0], lds, 0);
+  Acc<S> acc = {};
   int cur = 0;
-  auto one = [&](Fragments<S>& now, Fragments<S>& then) {
+  // A step, while that at k0 of the piece that `in` is in takes its place.
+  auto one = [&](auto any, int k0) {
+    constexpr bool kAny = decltype(any)::value;
     const int next = cur + S::kStage == kEnd ? 0 : cur + S::kStage;
-    const int k = step(s + S::kStages);
-    const int64_t at = in.go_to(a, k);
+    const int64_t at = in.template go_to<kAny>(a, k0);
     char* to = lds + cur;
-    if constexpr (S::kPhases == 1) {
-      phase<0>(in, reader, acc, now, then, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
-    } else {
-      phase<0>(in, reader, acc, now, then, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
-      phase<1>(in, reader, acc, then, now, k, at, lds + cur, lds + next, to, to + S::kXBytes, wave);
-    }
+    const char *same = lds + cur, *other = lds + next;
+    phase<0, kAny>(a, in, reader, acc, f[0], f[1], k0, at, same, same + S::kXBytes, nullptr, nullptr, tid, wave);
+    phase<1, kAny>(a, in, reader, acc, f[1], f[0], k0, at, other, other + S::kXBytes, to, to + S::kXBytes, tid, wave);
     cur = next;
-    return ++s < whole;
   };
-  if constexpr (S::kPhases == 1) {
+  for (;;) {
+    const int end = steps_end(now);
+    int s = now.s0;
+    // steps whose place a whole one of the same piece takes
+    const int plain = a.depth / S::kDepth < now.s1 ? a.depth / S::kDepth : now.s1;
+    if (in.whole) {
 #pragma unroll 1
-    while (one(f[0], f[1]) && one(f[1], f[0])) {
+      for (; s + S::kStages < plain; ++s) one(std::false_type{}, (s + S::kStages) * S::kDepth);
     }
-  } else {
 #pragma unroll 1
-    while (one(f[0], f[1])) {
+    for (; s + S::kStages < end; ++s) one(std::true_type{}, (s + S::kStages) * S::kDepth);
+    block += gridDim.x;
+    Work then = now;
+    const bool more = block < all;
+    if (more) {
+      then = work_of<S>(a, block);
+      in = Direct<S, kColumns>(a, then.p, then.s0 * S::kDepth, tid);
     }
+    // behind the last piece zeros, unused
+#pragma unroll 1
+    for (int i = 0; i < S::kStages; ++i) one(std::true_type{}, more ? (then.s0 + i) * S::kDepth : a.depth);
+    put_tile<S>(a, now, acc, lane, wave);
+    if (!more) break;
+    clear<S>(acc);
+    now = then;
   }
   meet<0>();
 }
 
-// Four sums of a lane, at a row of y and columns from n on.
-__device__ __forceinline__ void put_sums(const ProductArgs& a, int64_t row, int64_t n, const f32x4& s) {
-  const int64_t at = row * a.y_stride + n;
-  const int64_t left = a.cols - n;
-  if (a.y_bf16) {
-    uint16_t* y = static_cast<uint16_t*>(a.y) + at;
-    const u32x2 v = {pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
-    if (left >= 4) {
-      store_at<2>(y, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < left) y[i] = static_cast<uint16_t>(v[i / 2] >> (16 * (i & 1)));
-    }
-  } else {
-    float* y = static_cast<float*>(a.y) + at;
-    if (left >= 4) {
-      store_at<4>(y, s);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < left) y[i] = s[i];
-    }
-  }
-}
-
-// A wave's sums into y, 32 rows at a time by way of its own LDS, so that a row's
-// columns leave together: a lane has four of them, of one row.  Rows of LDS are
-// exchanged like staged ones.
-template <typename S, bool kBf16>
-__device__ __forceinline__ void store_tile(const ProductArgs& a, const Place& p, const Acc<S>& acc, char* lds, int lane,
-                                           int wave) {
-  constexpr int kSize = kBf16 ? 2 : 4, kRow = S::kColBlocks * 16 * kSize, kU = kRow / 16, kPer = 16 / kSize;
-  static_assert(2 * 32 * kRow <= S::kStages * S::kStage / (S::kThreads / 64), "a wave's share of the LDS");
-  static_assert((16 % kU == 0 || kU % 16 == 0) && S::kRowBlocks % 2 == 0, "units of a row, rows of a pass");
-  constexpr int kRowsABank = kU < 16 ? 16 / kU : 1;   // rows that the 64 banks hold
-  auto place = [&](int r, int u) { return r * kRow + ((u ^ (r / kRowsABank & ((kU < 16 ? kU : 16) - 1))) << 4); };
-  const int r0 = wave / S::kWavesC * S::kRowBlocks * 16, c0 = wave % S::kWavesC * S::kColBlocks * 16;
-#pragma unroll
-  for (int j = 0; j < S::kRowBlocks / 2; ++j) {
-    if (r0 + 32 * j >= p.rows) break;
-    char* at = lds + (j & 1) * (32 * kRow);
-#pragma unroll
-    for (int i = 0; i < S::kColBlocks; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4& s = acc[i][2 * j + h];
-        const int r = 16 * h + (lane & 15), q = lane >> 4;
-        if constexpr (kBf16)
-          *reinterpret_cast<u32x2*>(at + place(r, 2 * i + (q >> 1)) + 8 * (q & 1)) =
-              u32x2{pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3])};
-        else
-          *reinterpret_cast<f32x4*>(at + place(r, 4 * i + q)) = s;
-      }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-#pragma unroll
-    for (int q = 0; q < 32 * kU / 64; ++q) {
-      const int r = q * (64 / kU) + lane / kU, u = lane % kU, c = c0 + u * kPer;
-      const u32x4 v = *reinterpret_cast<const u32x4*>(at + place(r, u));
-      if (r0 + 32 * j + r >= p.rows || c >= p.cols) continue;
-      char* y = static_cast<char*>(a.y) + ((p.row + r0 + 32 * j + r) * a.y_stride + p.col + c) * kSize;
-      if (c + kPer <= p.cols) {
-        store_at<kSize>(y, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kPer - 1; ++e)
-          if (c + e < p.cols) {
-            if constexpr (kBf16) reinterpret_cast<uint16_t*>(y)[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
-            else reinterpret_cast<uint32_t*>(y)[e] = v[e];
-          }
-      }
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  }
-}
-
-template <typename S, bool kColumns, bool kDirect>
-__global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs a) {
-  __shared__ __align__(16) char lds[S::kStages * S::kStage];
-  const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  // Consecutive workgroups go round the eight XCDs: of the 256 that run at
-  // once, each XCD takes 32 neighbours, which share rows in its L2.
-  const int round = blockIdx.x & ~255;
-  const int now = static_cast<int>(gridDim.x) - round < 256 ? gridDim.x - round : 256;
-  const int xcd = blockIdx.x % 8, more = now % 8;
-  const int id = round + xcd * (now / 8) + (xcd < more ? xcd : more) + (blockIdx.x - round) / 8;
-  const int piece = id / a.tiles, tile = id - piece * a.tiles;
-  const Place p = place_of<S>(a, tile);
-  const int64_t all = (a.depth + S::kDepth - 1) / S::kDepth;
-  const int s0 = static_cast<int>(piece * all / a.pieces), s1 = static_cast<int>((piece + 1) * all / a.pieces);
-  const Reader<S, kColumns> reader(lane, w);
+// Rows or partitions anywhere: a step goes through registers.
+template <typename S, bool kColumns>
+__global__ __launch_bounds__(S::kThreads) void product_any_kernel(const ProductArgs a) {
+  __shared__ __align__(16) char lds[S::kLds];
+  const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
+  const Work k = work_of<S>(a, blockIdx.x);
+  const Reader<S, kColumns> reader(lane, wave);
   Acc<S> acc = {};
-  int s = s0;
-  if constexpr (kDirect) {
-    const int whole = s1 < a.depth / S::kDepth ? s1 : a.depth / S::kDepth;
-    if (s < whole) {
-      // the tile's part of the weight, all of one partition or not
-      const int64_t first = p.w + (kColumns ? 0 : static_cast<int64_t>(p.col) * a.depth);
-      const int64_t end = p.w + (kColumns ? static_cast<int64_t>(a.cols) : p.col + p.cols) * a.depth;
-      if (first / a.part_numel == (end - 1) / a.part_numel)
-        whole_steps<S, kColumns, false>(a, p, reader, acc, s, whole, lds, tid, w);
-      else
-        whole_steps<S, kColumns, true>(a, p, reader, acc, s, whole, lds, tid, w);
-      s = whole;
-    }
-  }
-  if (s < s1) {
-    Staged<S> next;
-    load_step<S, kColumns>(next, a, p, s * S::kDepth, tid);
-    for (; s < s1; ++s) {
-      lds_barrier();
-      store_step<S, kColumns>(next, lds, tid);
-      lds_barrier();
-      if (s + 1 < s1) load_step<S, kColumns>(next, a, p, (s + 1) * S::kDepth, tid);
-      multiply_step<S, kColumns>(acc, reader, lds);
-    }
-  }
-  if (a.pieces == 1) {
-    lds_barrier();             // the stages are read
-    char* own = lds + w * (S::kStages * S::kStage / (S::kThreads / 64));
-    if (a.y_bf16) store_tile<S, true>(a, p, acc, own, lane, w);
-    else store_tile<S, false>(a, p, acc, own, lane, w);
-    return;
-  }
-  const int wr = w / S::kWavesC, wc = w % S::kWavesC;
+  Staged<S> next;
+  load_step<S, kColumns>(next, a, k.p, k.s0 * S::kDepth, tid);
+  int at = 0;
+#pragma unroll 1
+  for (int s = k.s0; s < k.s1; ++s) {
+    // two stages in turn: the other one's readers are behind the last barrier
+    store_step<S, kColumns>(next, lds + at, tid);
+    lds_barrier();
+    if (s + 1 < k.s1) load_step<S, kColumns>(next, a, k.p, (s + 1) * S::kDepth, tid);
 #pragma unroll
-  for (int j = 0; j < S::kRowBlocks; ++j) {
-    const int r = (wr * S::kRowBlocks + j) * 16 + (lane & 15);
-    if (r >= p.rows) continue;
-#pragma unroll
-    for (int i = 0; i < S::kColBlocks; ++i) {
-      const int c = (wc * S::kColBlocks + i) * 16 + 4 * (lane >> 4);
-      *as_global<f32x4>(a.partial + static_cast<int64_t>(id) * (S::kRows * S::kCols) + r * S::kCols + c) = acc[i][j];
+    for (int phase = 0; phase < S::kPhases; ++phase) {
+      Fragments<S> f;
+      reader.read(f, lds + at, phase);
+      multiply<S>(acc, f);
     }
+    at = S::kStage - at;
   }
+  put_tile<S>(a, k, acc, lane, wave);
 }
 
 // Adds up the pieces of each tile, in their order: four sums a thread, the
@@ -578,7 +637,20 @@ __global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const Produc
   const int64_t step = static_cast<int64_t>(a.tiles) * (S::kRows * S::kCols);
   f32x4 sum = *as_global<f32x4>(from);
   for (int k = 1; k < a.pieces; ++k) sum += *as_global<f32x4>(from + k * step);
-  put_sums(a, p.row + r, p.col + c, sum);
+  const int64_t to = (p.row + r) * a.y_stride + p.col + c;
+  if (!a.y_bf16) {
+    put_sums<4>(a, to, p.cols - c, __builtin_bit_cast(u32x4, sum));
+  } else {
+    uint16_t* y = static_cast<uint16_t*>(a.y) + to;
+    const u32x2 v = {pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3])};
+    if (c + 4 <= p.cols) {
+      store_at<2>(y, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (c + e < p.cols) y[e] = static_cast<uint16_t>(v[e / 2] >> (16 * (e & 1)));
+    }
+  }
 }
 
 using Large = Shape<256, 256, 2, 4, 64, 2>;
@@ -674,9 +746,16 @@ zr_status plan_product(const zr_plan* plan, const int64_t* params, const int64_t
 
 template <typename S>
 zr_status launch_product(const ProductArgs& a, bool columns, bool direct, hipStream_t stream) {
-  auto* kernel = columns ? (direct ? product_kernel<S, true, true> : product_kernel<S, true, false>)
-                         : (direct ? product_kernel<S, false, true> : product_kernel<S, false, false>);
-  ZR_LAUNCH(a.tiles * a.pieces, S::kThreads, stream, a, kernel);
+  const int64_t items = int64_t(a.tiles) * a.pieces;
+  if (direct) {
+    // as many workgroups as the chip holds
+    const int64_t grid = std::min<int64_t>(items, kCus * (2 * S::kLds > 160 * 1024 ? 1 : 2));
+    auto* kernel = columns ? product_kernel<S, true> : product_kernel<S, false>;
+    ZR_LAUNCH(grid, S::kThreads, stream, a, kernel);
+  } else {
+    auto* kernel = columns ? product_any_kernel<S, true> : product_any_kernel<S, false>;
+    ZR_LAUNCH(items, S::kThreads, stream, a, kernel);
+  }
   zr_status st = launched("product launch");
   if (st != ZR_OK || a.pieces == 1) return st;
   ZR_LAUNCH(a.tiles * (S::kRows * S::kCols / (4 * kJoinThreads)), kJoinThreads, stream, a, product_join_kernel<S>);
@@ -723,6 +802,10 @@ zr_status run_product(const zr_plan* plan, const int64_t* params, const int64_t*
       if (l.bytes > 0 && (!workspace || !aligned_to(workspace, 16) || workspace_bytes < l.bytes))
         return fail(ZR_ERR_INVALID, "workspace is null, not 16-byte aligned or smaller than " +
                                         std::to_string(l.bytes) + " bytes");
+    // An output that the last-level cache (256 MB) does not hold beside the inputs
+    // would only drive those out of it: 16384 x 8192 from 2048, 268 MB in all, 417 us
+    // past the caches and 445 through them; 8192 x 4096 from 4096, 67 MB, 191 and 187.
+    const bool past = used * cols * dtype_size(y_dtype) > (int64_t(128) << 20);
     for (Launch& l : launches) {
       ProductArgs& a = l.a;
       for (int r = 0; r < gi.world; ++r) a.part[r] = static_cast<const char*>(parts[r]);
@@ -730,10 +813,12 @@ zr_status run_product(const zr_plan* plan, const int64_t* params, const int64_t*
       a.y = y;
       a.partial = static_cast<float*>(workspace);
       a.part_numel = gi.part;
+      a.part_inverse = 1.0 / static_cast<double>(gi.part);
       a.world = gi.world;
       a.x_stride = x_stride;
       a.y_stride = y_stride;
       a.y_bf16 = y_dtype == ZR_BF16;
+      a.y_past = past;
       // a step's part of the weight, in two partitions at most
       const int64_t wide = columns ? cols : depth;
       const int64_t span = columns ? (l.small ? Small::kDepth : Large::kDepth) * cols

@@ -36,4 +36,11 @@ __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// The lanes of a wave in four rows of sixteen: those of rows 1 and 3 give their x
+// for the y of the lanes in the row before.
+__device__ __forceinline__ u32x2 exchange_rows(uint32_t x, uint32_t y) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+  return u32x2{r[0], r[1]};
+}
+
 }  // namespace zr
