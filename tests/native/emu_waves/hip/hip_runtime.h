@@ -180,6 +180,7 @@ inline zr_emu_u32x2 zr_emu_swap_rows(uint32_t x, uint32_t y) {
   return r;
 }
 #define __builtin_amdgcn_permlane16_swap(x, y, fetch, bound) zr_emu_swap_rows((x), (y))
+#define __builtin_amdgcn_logf(x) std::log2(static_cast<float>(x))
 #define __builtin_amdgcn_rcpf(x) (1.0f / (x))
 #define __builtin_amdgcn_exp2f(x) std::exp2(static_cast<float>(x))
 #define __builtin_amdgcn_cvt_pk_fp8_f32(lo, hi, old, high) zr_emu_cvt_pk_fp8((lo), (hi), (old), (high))

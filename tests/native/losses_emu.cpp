@@ -131,7 +131,7 @@ void loss_case(Rng& r, int seed, int64_t rows, int64_t vocab, bool bf16, double 
       }
       const double got = per.at(5 * ps + i);
       if (std::fabs(lp) > 3e38) lp = -kInf;   // past fp32
-      CHECK(got == lp || std::fabs(got - lp) <= 2e-6 * (1 + std::fabs(lp)), "seed %d row %ld: logp %g for %g", seed,
+      CHECK(got == lp || std::fabs(got - lp) <= 2e-6 * (1 + std::fabs(lp)), "seed %d row %ld: logp %.9g for %.9g", seed,
             long(i), got, lp);
     }
     const double got = per.at(4 * ps + i);

@@ -84,7 +84,8 @@ def test_workspace():
         assert lib.zr_loss_workspace(*args, ctypes.byref(n)) != zr.ZR_OK and n.value == 0
     assert lib.zr_loss_workspace(1, 10, 1, 0, None) == zr.ZR_ERR_INVALID
     assert zr.zr_loss_workspace(0, 50257, 4, torch.float32) == 0
-    assert zr.zr_loss_workspace(8192, 128256, 64, torch.bfloat16) == 0
+    assert zr.zr_loss_workspace(200, 128256, 64, torch.bfloat16) == 0
+    assert zr.zr_loss_workspace(8192, 128256, 64, torch.bfloat16) == 16
     assert zr.zr_loss_workspace(1, 128256, 64, "bf16") >= 64 * 4
     with pytest.raises(zr.ZrError):
         zr.zr_loss_workspace(1, 10, 1, torch.float16)

@@ -9,11 +9,14 @@
 //                 dL/dz = dL/dlp / tau ([v = a] - q).
 // Both gradients are one multiple of q with corrections at few columns, so one
 // kernel serves both: statistics of the row, a handful of numbers, the row
-// written.  Maxima are exact, exponentials and a lane's sums fp32; what is
-// computed once a row (logarithms, ratios, the loss) is 64-bit, since a ratio
-// next to the clip's border decides between a gradient and none.
+// written.  Maxima are exact, exponentials and a lane's sums fp32.  log q, and how
+// far it is from old and ref, are 64-bit differences: a ratio next to the clip's
+// border decides between a gradient and none.  (The exponentials and logarithms
+// themselves are fp32: those of 64 bits held wave 0, and all waves behind it, for
+// 6,000 cycles a row.)
 
 #include <cmath>
+#include <type_traits>
 
 #include "zr_layers.h"
 
@@ -34,8 +37,11 @@ struct LossArgs {
   const float* weight;             // null: 1
   const float *old_logp, *ref_logp, *advantage;
   float *loss, *logp;
-  double tau, clip_low, clip_high, kl;
+  double tau, inverse_tau;
   float c;                         // log2(e) / tau
+  float clip_low, clip_high;       // the ratio's borders, and their logarithms
+  double log_low, log_high;
+  float kl;
   int32_t wide, teacher_bf16;
   int64_t rows;
   int32_t vocab, top;
@@ -43,6 +49,7 @@ struct LossArgs {
   int32_t chunks, chunk;           // how many, of how many vectors each
   float* stats;                    // [row][chunk] maximum and sum
   float* picked;                   // [row][entry] its logit
+  int32_t* counter;                // rows taken beyond the first of each workgroup; null: none are
 };
 
 // -------------------------------------------------------------- a row's data
@@ -72,10 +79,36 @@ __device__ __forceinline__ u32x4 filled(float x) {   // x: exact in bf16
   return u32x4{w, w, w, w};
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.44269504f); }
+// The natural logarithm of s > 0, off by some 2^-24: of its mantissa in fp32, and
+// the exponent apart.
+__device__ __forceinline__ double log_of(float s) {
+  if (!(s < INFINITY)) return s;
+  const uint32_t b = float_bits(s);
+  int n = static_cast<int>(b >> 23) - 127;
+  float f = bits_float((b & 0x7fffffu) | 0x3f800000u);
+  if (f > 1.41421356f) f *= 0.5f, ++n;
+  return n * 0.69314718055994531 + static_cast<double>(__builtin_amdgcn_logf(f) * 0.69314718f);
+}
+// exp(d) - d - 1, to fp32's relative precision.
+__device__ __forceinline__ float exp_minus(float d) {
+  if (d > -0.5f && d < 0.5f) {   // d^2 (1/2 + d/6 + ... + d^7/9!)
+    float r = 1.0f / 362880;
+    r = __builtin_fmaf(r, d, 1.0f / 40320);
+    r = __builtin_fmaf(r, d, 1.0f / 5040);
+    r = __builtin_fmaf(r, d, 1.0f / 720);
+    r = __builtin_fmaf(r, d, 1.0f / 120);
+    r = __builtin_fmaf(r, d, 1.0f / 24);
+    r = __builtin_fmaf(r, d, 1.0f / 6);
+    r = __builtin_fmaf(r, d, 0.5f);
+    return r * d * d;
+  }
+  const float e = exp_fast(d);
+  return e == INFINITY ? e : e - d - 1.0f;
+}
 
-// The maximum of some logits and the sum of 2^(c (z - maximum)) over them.  The
-// difference is taken before the product: logits of the type's lowest value,
-// all of a row's perhaps, stay finite.  A NaN is in the sum, not the maximum.
+// The maximum of some logits and the sum of 2^(c (z - maximum)) over them.  A NaN
+// is in the sum, not the maximum.
 struct Stats {
   float m, s;
 };
@@ -88,40 +121,69 @@ __device__ __forceinline__ Stats joined(const Stats& a, const Stats& b, float c)
   r.s = a.s * exp2_fast((a.m - at) * c) + b.s * exp2_fast((b.m - at) * c);
   return r;
 }
+
+// 2^(c (z - m)) for many z, m the same in all lanes.  Fast: an FMA and the
+// exponential, and then `fix` once for all that is off by the rounding of c m.
+// There m is held where c m is under 10^8, so that the rounding is a few units: a
+// sum over logits further out is 0 or infinite, which tells them (logits of the
+// type's lowest value, all of a row's perhaps).  Otherwise the difference is taken
+// first and stays finite.
+struct Powers {
+  float m, c, mc, fix;
+  __device__ __forceinline__ Powers(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), fix(1.0f) {}
+  static __device__ __forceinline__ Powers fast(float m, float c) {
+    const float most = 1e8f / c;
+    m = m > most ? most : m < -most ? -most : m;
+    Powers p(m, c);
+    p.fix = exp2_fast(-__builtin_fmaf(m, c, -p.mc));
+    return p;
+  }
+  template <bool kFast>
+  __device__ __forceinline__ float of(float z) const {
+    return exp2_fast(kFast ? __builtin_fmaf(z, c, -mc) : (z - m) * c);
+  }
+};
 template <typename T>
 __device__ __forceinline__ float top_of(float m, const u32x4& v) {
 #pragma unroll
-  for (int k = 0; k < kPer<T>; ++k) {
-    const float x = element<T>(v, k);
-    m = x > m ? x : m;
-  }
+  for (int k = 0; k < kPer<T>; k += 2) m = __builtin_fmaxf(__builtin_fmaxf(m, element<T>(v, k)), element<T>(v, k + 1));
   return m;
 }
-template <typename T>
-__device__ __forceinline__ float sum_of(const u32x4& v, float at, float c) {
+template <bool kFast, typename T>
+__device__ __forceinline__ float sum_of(const u32x4& v, const Powers& p) {
   float s = 0.0f;
 #pragma unroll
-  for (int k = 0; k < kPer<T>; ++k) s += exp2_fast((element<T>(v, k) - at) * c);
+  for (int k = 0; k < kPer<T>; ++k) s += p.of<kFast>(element<T>(v, k));
   return s;
 }
-template <typename T>
-__device__ __forceinline__ void add_to(Stats& r, const u32x4& v, float c) {
-  const float m = top_of<T>(r.m, v), at = base(m);
-  r.s = r.s * exp2_fast((r.m - at) * c) + sum_of<T>(v, at, c);
-  r.m = m;
-}
-template <typename T>
-__device__ __forceinline__ u32x4 gradient(const u32x4& v, float m, float c, float scale) {
+template <bool kFast, typename T>
+__device__ __forceinline__ u32x4 gradient(const u32x4& v, const Powers& p, float scale) {
   u32x4 g;
   float x[kPer<T>];
 #pragma unroll
-  for (int k = 0; k < kPer<T>; ++k) x[k] = exp2_fast((element<T>(v, k) - m) * c) * scale;
+  for (int k = 0; k < kPer<T>; ++k) x[k] = p.of<kFast>(element<T>(v, k)) * scale;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     if constexpr (sizeof(T) == 2) g[k] = pack_bf16(x[2 * k], x[2 * k + 1]);
     else g[k] = float_bits(x[k]);
   }
   return g;
+}
+// The statistics of a workgroup's waves, put together in every wave: a power of
+// two of them, one a lane.
+template <int kWaves>
+__device__ __forceinline__ Stats over_waves(const Stats* wave, float c) {
+  const Stats own = wave[threadIdx.x % kWaves];
+  Stats st = own;
+#pragma unroll
+  for (int d = 1; d < kWaves; d *= 2) {
+    const float o = __shfl_xor(st.m, d);
+    st.m = o > st.m ? o : st.m;
+  }
+  st.s *= exp2_fast((own.m - base(st.m)) * c);
+#pragma unroll
+  for (int d = 1; d < kWaves; d *= 2) st.s += __shfl_xor(st.s, d);
+  return st;
 }
 
 // Values unpacked in one pass are not kept for the next: the registers hold the
@@ -157,7 +219,8 @@ __device__ __forceinline__ float most_of_wave(float x) {
   }
   return x;
 }
-__device__ __forceinline__ double sum_of_wave(double x) {
+template <typename V>
+__device__ __forceinline__ V sum_of_wave(V x) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) x += __shfl_xor(x, d);
   return x;
@@ -165,17 +228,23 @@ __device__ __forceinline__ double sum_of_wave(double x) {
 
 // ------------------------------------------------------------- a row's entries
 
-// In LDS: the entries' columns (-1: none), their probabilities and logits, and
-// what wave 0 works out for all.
-template <bool kTeacher, int kWaves>
-struct Shared {
-  static constexpr int kTop = kTeacher ? kMaxTop : 1;
+// A row's entries in LDS: their columns (-1: none), what is subtracted from q
+// there, and their logits.
+template <bool kTeacher>
+struct Entries {
+  static constexpr int kTop = kTeacher ? kMaxTop : 4;
   int32_t id[kTop];
   float p[kTop];
   float z[kTop];
+  int32_t used;                // the row counts
+};
+// And what else a workgroup shares.
+template <bool kTeacher, int kWaves>
+struct Shared {
+  Entries<kTeacher> row[2];
   Stats wave[kWaves];
   float coef;
-  int32_t used;
+  int32_t next;
 };
 
 __device__ __forceinline__ int32_t entry_id(const LossArgs& a, int64_t row, int j) {
@@ -201,109 +270,151 @@ struct Teacher {
   double lse = 0.0, mean = 0.0;
 };
 
-// Wave 0: reads the row's entries into LDS and finds out whether the row counts:
-// it has an entry in the vocabulary (and, for the teacher's, one above -inf),
-// and the teacher's a weight.  kLogits: their logits too.
-template <typename T, bool kTeacher, int kWaves, bool kLogits>
-__device__ __forceinline__ Teacher read_entries(const LossArgs& a, int64_t row, Shared<kTeacher, kWaves>& sh, int lane) {
+// A wave's first 64 entries of a row and the row's numbers, asked for.
+struct Asked {
+  int32_t id;
+  float t, weight, advantage, old_logp, ref_logp;
+};
+template <bool kTeacher>
+__device__ __forceinline__ Asked ask(const LossArgs& a, int64_t row, int lane) {
+  Asked q{-1, 0.0f, 1.0f, 0.0f, 0.0f, 0.0f};
+  if (lane < a.top) {
+    q.id = entry_id(a, row, lane);
+    if constexpr (kTeacher) q.t = teacher_logit(a, row, lane);
+  }
+  q.weight = weight_of(a, row);
+  if constexpr (!kTeacher) {
+    q.advantage = as_global<float>(a.advantage)[row];
+    q.old_logp = as_global<float>(a.old_logp)[row];
+    if (a.ref_logp) q.ref_logp = as_global<float>(a.ref_logp)[row];
+  }
+  return q;
+}
+
+// One wave: puts the row's entries into LDS and finds out whether the row counts:
+// it has an entry in the vocabulary (and, for the teacher's, one above -inf, and a
+// weight).
+template <bool kTeacher>
+__device__ __forceinline__ void put_asked(const LossArgs& a, int64_t row, const Asked& q, Entries<kTeacher>& e,
+                                          int lane) {
+  bool some = false;
+  for (int j = lane; j < a.top; j += 64) {
+    int32_t id = j < 64 ? q.id : entry_id(a, row, j);
+    if constexpr (kTeacher) {
+      const float t = j < 64 ? q.t : teacher_logit(a, row, j);
+      if (t == -INFINITY) id = -1;   // no probability, no matter what q is
+      e.p[j] = t;
+    } else {
+      e.p[j] = 1.0f;
+    }
+    e.id[j] = id;
+    some = some || id >= 0;
+  }
+  // four at a time are compared below
+  if (kTeacher && lane < (-a.top & 3)) e.id[a.top + lane] = -1;
+  const bool used = __ballot(some) != 0 && (!kTeacher || q.weight != 0.0f);
+  if (lane == 0) e.used = used;
+}
+
+// The same wave, of a row that counts: the entries' logits (kLogits; otherwise
+// they are there already) and the teacher's probabilities, those of one column
+// added up.
+template <typename T, bool kTeacher, bool kLogits>
+__device__ __forceinline__ Teacher finish_entries(const LossArgs& a, int64_t row, Entries<kTeacher>& e, int lane) {
   Teacher t;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  if constexpr (kLogits)
+    for (int j = lane; j < a.top; j += 64)
+      if (e.id[j] >= 0) e.z[j] = one(z + e.id[j]);
   if constexpr (kTeacher) {
-    float m = -INFINITY, bad = 0.0f;
-    for (int j = lane; j < a.top; j += 64) {
-      int32_t id = entry_id(a, row, j);
-      const float x = id < 0 ? -INFINITY : teacher_logit(a, row, j);
-      if (x != x) bad = x;
-      if (x == -INFINITY) id = -1;   // no probability, no matter what q is
-      m = x > m ? x : m;
-      sh.id[j] = id;
-      sh.p[j] = x;
-      if constexpr (kLogits) sh.z[j] = id < 0 ? 0.0f : one(z + id);
-    }
+    float m = -INFINITY;
+    for (int j = lane; j < a.top; j += 64)
+      if (e.id[j] >= 0) m = e.p[j] > m ? e.p[j] : m;
     m = most_of_wave(m);
-    const bool some = __ballot(m > -INFINITY || bad != bad) != 0;
-    const float w = weight_of(a, row);
     double s = 0.0, mean = 0.0;
     for (int j = lane; j < a.top; j += 64) {
-      if (sh.id[j] < 0) continue;
-      const double d = (static_cast<double>(sh.p[j]) - m) / a.tau, e = exp(d);
-      s += e;
-      if (e > 0.0) mean += e * d;
+      if (e.id[j] < 0) continue;
+      const float d = e.p[j] - m, x = exp2_fast(d * a.c);
+      s += x;
+      if (x != 0.0f) mean += static_cast<double>(x) * d;
+      e.p[j] = x;
     }
     s = sum_of_wave(s);
     mean = sum_of_wave(mean);
-    for (int j = lane; j < a.top; j += 64)
-      sh.p[j] = sh.id[j] < 0 ? 0.0f
-                             : static_cast<float>(exp((static_cast<double>(sh.p[j]) - m) / a.tau) / s);
+    const float part = 1.0f / static_cast<float>(s);
+    for (int j = lane; j < a.top; j += 64) e.p[j] = e.id[j] < 0 ? 0.0f : e.p[j] * part;
     // both less m / tau
-    t.lse = log(s);
-    t.mean = mean / s;
-    if (lane == 0) {
-      sh.used = some && w != 0.0f;
-      sh.coef = static_cast<float>(w * a.tau);
-    }
-  } else {
-    const int32_t id = entry_id(a, row, 0);
-    if (lane == 0) {
-      sh.id[0] = id;
-      sh.p[0] = 1.0f;
-      if constexpr (kLogits) sh.z[0] = id < 0 ? 0.0f : one(z + id);
-      sh.used = id >= 0;
-    }
+    t.lse = log_of(static_cast<float>(s));
+    t.mean = mean * static_cast<double>(part) * a.inverse_tau;
   }
   return t;
 }
 
 // Wave 0, with the row's statistics and the entries' logits: the loss, and the
 // multiple of q in the gradient.
-template <bool kTeacher, int kWaves>
-__device__ __forceinline__ void finish_row(const LossArgs& a, int64_t row, Shared<kTeacher, kWaves>& sh,
-                                           const Teacher& t, const Stats& st, int lane, bool store) {
-  const double log_s = log(static_cast<double>(st.s));
+template <bool kTeacher>
+__device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, const Entries<kTeacher>& sh,
+                                            const Asked& of_row, const Teacher& t, const Stats& st, int lane,
+                                            bool store) {
+  const double log_s = log_of(st.s);
   if constexpr (kTeacher) {
     // log q[id] = (z - m) / tau - log s
     double cross = 0.0;
     for (int j = lane; j < a.top; j += 64)
       if (sh.id[j] >= 0 && sh.p[j] != 0.0f)
-        cross += sh.p[j] * ((static_cast<double>(sh.z[j]) - st.m) / a.tau - log_s);
+        cross += sh.p[j] * ((static_cast<double>(sh.z[j]) - st.m) * a.inverse_tau - log_s);
     cross = sum_of_wave(cross);
     if (lane == 0 && store)
-      a.loss[row] = static_cast<float>(weight_of(a, row) * a.tau * a.tau * ((t.mean - t.lse) - cross));
+      a.loss[row] = static_cast<float>(of_row.weight * a.tau * a.tau * ((t.mean - t.lse) - cross));
+    return static_cast<float>(of_row.weight * a.tau);
   } else {
-    const double lp = (static_cast<double>(sh.z[0]) - st.m) / a.tau - log_s;
-    const double w = weight_of(a, row), adv = a.advantage[row];
-    const double r = exp(lp - a.old_logp[row]);
-    const double lo = 1.0 - a.clip_low, hi = 1.0 + a.clip_high;
-    const double held = r < lo ? lo : r > hi ? hi : r;   // NaN stays
-    const bool cut = (adv > 0.0 && r > hi) || (adv < 0.0 && r < lo);
-    double loss = cut ? -held * adv : -r * adv, slope = cut ? 0.0 : -r * adv;
+    const double lp = (static_cast<double>(sh.z[0]) - st.m) * a.inverse_tau - log_s;
+    const float w = of_row.weight, adv = of_row.advantage;
+    const double over = lp - of_row.old_logp;
+    float r = exp_fast(static_cast<float>(over));
+    r = r > 3.4e38f ? 3.4e38f : r;   // times an advantage of 0 it is 0
+    const bool cut = (adv > 0.0f && over > a.log_high) || (adv < 0.0f && over < a.log_low);
+    float loss = -adv * (!cut ? r : adv > 0.0f ? a.clip_high : a.clip_low), slope = cut ? 0.0f : -r * adv;
     if (a.ref_logp) {
-      const double d = a.ref_logp[row] - lp, e = expm1(d);
-      loss += a.kl * (e == INFINITY ? e : e - d);
-      slope -= a.kl * e;
+      const float d = static_cast<float>(of_row.ref_logp - lp), e = exp_minus(d);
+      loss += a.kl * e;
+      slope -= a.kl * (e == INFINITY ? e : e + d);
     }
-    if (lane == 0) {
-      sh.coef = w == 0.0 ? 0.0f : static_cast<float>(-w * slope / a.tau);
-      if (store) {
-        a.loss[row] = w == 0.0 ? 0.0f : static_cast<float>(w * loss);
-        a.logp[row] = static_cast<float>(lp);
-      }
+    if (lane == 0 && store) {
+      a.loss[row] = w == 0.0f ? 0.0f : w * loss;
+      a.logp[row] = static_cast<float>(lp);
     }
+    return w == 0.0f ? 0.0f : static_cast<float>(-w * slope * a.inverse_tau);
   }
+}
+// A row that does not count.
+template <bool kTeacher>
+__device__ __forceinline__ void put_nothing(const LossArgs& a, int64_t row) {
+  a.loss[row] = 0.0f;
+  if constexpr (!kTeacher) a.logp[row] = 0.0f;
 }
 
 // The gradient at the entries' columns inside [v0, v1), over what the row's
-// pass wrote there.  Entries of one column write one value.
-template <typename T, int kThreads, bool kTeacher, int kWaves>
-__device__ __forceinline__ void put_entries(const LossArgs& a, T* out, const Shared<kTeacher, kWaves>& sh,
+// pass wrote there.  The p of one column are added up, in their order; entries of
+// one column write one value.
+template <typename T, int kThreads, bool kTeacher>
+__device__ __forceinline__ void put_entries(const LossArgs& a, T* out, const Entries<kTeacher>& e, float coef,
                                             const Stats& st, int v0, int v1) {
-  const float coef = sh.coef, part = 1.0f / st.s;
+  const float part = 1.0f / st.s;
   for (int j = threadIdx.x; j < a.top; j += kThreads) {
-    const int32_t id = sh.id[j];
+    const int32_t id = e.id[j];
     if (id < v0 || id >= v1) continue;
-    float p = 0.0f;
-    for (int i = 0; i < a.top; ++i) p += sh.id[i] == id ? sh.p[i] : 0.0f;
-    put_one(out + id, coef * (exp2_fast((sh.z[j] - st.m) * a.c) * part - p));
+    float p = kTeacher ? 0.0f : e.p[0];
+    if constexpr (kTeacher) {
+#pragma unroll 4
+      for (int i = 0; i < a.top; i += 4) {
+        const u32x4 other = *reinterpret_cast<const u32x4*>(&e.id[i]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (static_cast<int32_t>(other[k]) == id) p += e.p[i + k];
+      }
+    }
+    put_one(out + id, coef * (exp2_fast((e.z[j] - st.m) * a.c) * part - p));
   }
 }
 
@@ -313,89 +424,160 @@ __device__ __forceinline__ void stores_done() {
   __syncthreads();
 }
 
+// The statistics of a row with logits far out, taken again from memory by all of
+// the workgroup.
+template <typename T, int kThreads>
+__device__ __forceinline__ Stats far_stats(const LossArgs& a, const T* z, Stats* wave) {
+  Stats st = kNoStats;
+#pragma unroll 1
+  for (int v = threadIdx.x; v < a.vocab; v += kThreads) {
+    const float x = one(z + v);
+    st = joined(st, Stats{x, exp2_fast((x - base(x)) * a.c)}, a.c);
+  }
+  st = over_wave(st, a.c);
+  __syncthreads();             // all have read what was there
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x / 64] = st;
+  __syncthreads();
+  return over_waves<kThreads / 64>(wave, a.c);
+}
+
 // ------------------------------------------------------ a row in a workgroup
 
-// A row a workgroup, the first kVecs vectors of a lane in registers between
-// the two passes, so that HBM is read once; what is behind them is read twice.
+// A row a workgroup, the first kVecs vectors of a lane in registers between the
+// two passes, so that HBM is read once; what is behind them is read twice.  While
+// a row's gradient is written the next one's logits are on their way into the
+// registers that get free, and wave 0 works out its entries.  A workgroup's next
+// row comes from a counter: rows that do not count take a third of the others'
+// time.
 template <typename T, bool kTeacher, int kThreads, int kVecs>
-__global__ __launch_bounds__(kThreads) void loss_row_kernel(const LossArgs a) {
+__global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a) {
   constexpr int kWaves = kThreads / 64;
-  __shared__ Shared<kTeacher, kWaves> sh;
+  __shared__ __align__(16) Shared<kTeacher, kWaves> sh;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
-  const int64_t row = blockIdx.x;
-  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
+  const int rows = static_cast<int>(a.rows);
   const int vecs = a.vocab / kPer<T>, left = a.vocab % kPer<T>;
-  Teacher t;
-  if (w == 0) t = read_entries<T, kTeacher, kWaves, true>(a, row, sh, lane);
-  __syncthreads();
-  const bool used = sh.used != 0;
-  T* out = a.grad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
-  if (!used) {
-    if (tid == 0) {
-      a.loss[row] = 0.0f;
-      if constexpr (!kTeacher) a.logp[row] = 0.0f;
-    }
-    if (out) {
-      for (int v = tid; v < vecs; v += kThreads) store_at<sizeof(T)>(out + static_cast<int64_t>(v) * kPer<T>, u32x4{0, 0, 0, 0});
-      if (tid < left) put_one(out + static_cast<int64_t>(vecs) * kPer<T> + tid, 0.0f);
-    }
-    return;
-  }
-  u32x4 x[kVecs];
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = i * kThreads + tid;
-    x[i] = filled<T>(-INFINITY);
-    if (v < vecs) x[i] = load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>);
-  }
-  float last = -INFINITY;
-  if (tid < left) last = one(z + static_cast<int64_t>(vecs) * kPer<T> + tid);
-  Stats st;
-  st.m = last;
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) st.m = top_of<T>(st.m, x[i]);
-  const float at = base(st.m);
-  st.s = exp2_fast((last - at) * a.c);
-  keep_packed(x);
-#pragma unroll
-  for (int i = 0; i < kVecs; ++i) st.s += sum_of<T>(x[i], at, a.c);
-  for (int v = kVecs * kThreads + tid; v < vecs; v += kThreads)
-    add_to<T>(st, load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), a.c);
-  st = over_wave(st, a.c);
-  if (lane == 0) sh.wave[w] = st;
-  __syncthreads();
-  st = sh.wave[0];
-  for (int k = 1; k < kWaves; ++k) st = joined(st, sh.wave[k], a.c);
-  const bool empty = st.s == 0.0f;   // every logit -inf
+  const int64_t end = static_cast<int64_t>(vecs) * kPer<T> + tid;   // a lane's of the elements behind the vectors
+  auto take = [&]() { return a.counter ? static_cast<int>(gridDim.x) + atomicAdd(a.counter, 1) : rows; };
+  auto vec = [&](int i) { return i * kThreads + tid; };
+  // A lane's i-th vector of a row: a uniform address and 32 bits of the lane's,
+  // not their sums kept for every i.
+  auto place = [&](auto* of_row, int i) {
+    uint32_t off = 16 * tid;
+    ZR_OPAQUE_IN(off, i);
+    return reinterpret_cast<decltype(of_row)>(reinterpret_cast<uintptr_t>(of_row) + i * (16 * kThreads) + off);
+  };
+  int row = blockIdx.x, now = 0;
+  Asked of_row{};              // of the row, in wave 0
   if (w == 0) {
-    if (empty) {
-      if (lane == 0) {
-        a.loss[row] = 0.0f;
-        if constexpr (!kTeacher) a.logp[row] = 0.0f;
-      }
-    } else {
-      finish_row<kTeacher>(a, row, sh, t, st, lane, true);
-    }
+    of_row = ask<kTeacher>(a, row, lane);
+    if (lane == 0) sh.next = take();
+    put_asked(a, row, of_row, sh.row[0], lane);
   }
-  if (!out) return;
   __syncthreads();
-  const float scale = empty ? 0.0f : sh.coef / st.s;
-  const float m = base(st.m);
-  keep_packed(x);
+  u32x4 x[kVecs];
+  float last = -INFINITY;
+  const T* z = static_cast<const T*>(a.logits) + row * a.stride;
 #pragma unroll
-  for (int i = 0; i < kVecs; ++i) {
-    const int v = i * kThreads + tid;
-    if (v < vecs)
-      store_at<sizeof(T)>(out + static_cast<int64_t>(v) * kPer<T>, gradient<T>(x[i], m, a.c, scale));
+  for (int i = 0; i < kVecs; ++i) x[i] = filled<T>(-INFINITY);
+  Teacher t;
+  if (uniform(sh.row[0].used)) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+      if (vec(i) < vecs) x[i] = load_at<u32x4, sizeof(T)>(place(z, i));
+    if (tid < left) last = one(z + end);
+    if (w == 0) t = finish_entries<T, kTeacher, true>(a, row, sh.row[0], lane);
   }
-  for (int v = kVecs * kThreads + tid; v < vecs; v += kThreads)
-    store_at<sizeof(T)>(out + static_cast<int64_t>(v) * kPer<T>,
-                        gradient<T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), m, a.c, scale));
-  if (tid < left)
-    put_one(out + static_cast<int64_t>(vecs) * kPer<T> + tid, exp2_fast((last - m) * a.c) * scale);
-  if (empty) return;
-  stores_done();
-  put_entries<T, kThreads>(a, out, sh, st, 0, a.vocab);
+#pragma unroll 1
+  for (;;) {
+    const int next = uniform(sh.next);
+    Asked asked{};
+    if (w == 0 && next < rows) asked = ask<kTeacher>(a, next, lane);
+    const bool used = uniform(sh.row[now].used) != 0;
+    if (used) {
+      float top = last;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) top = top_of<T>(top, x[i]);
+      for (int v = vec(kVecs); v < vecs; v += kThreads)
+        top = top_of<T>(top, load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>));
+      Stats st{uniform(most_of_wave(top)), 0.0f};
+      const Powers p = Powers::fast(base(st.m), a.c);
+      if (st.m != -INFINITY) st.m = p.m;
+      keep_packed(x);
+      st.s = p.of<true>(last);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) st.s += sum_of<true, T>(x[i], p);
+      for (int v = vec(kVecs); v < vecs; v += kThreads)
+        st.s += sum_of<true, T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), p);
+      st.s = sum_of_wave(st.s) * p.fix;
+      if (lane == 0) sh.wave[w] = st;
+    }
+    __syncthreads();
+    Stats st = over_waves<kWaves>(sh.wave, a.c);
+    const bool far = used && st.m != -INFINITY && (st.s == 0.0f || st.s == INFINITY);
+    if (far) st = far_stats<T, kThreads>(a, z, sh.wave);
+    const bool some = used && st.s != 0.0f;   // not every logit is -inf
+    if (w == 0) {
+      // only the policy's gradient waits for the loss
+      float coef = kTeacher ? static_cast<float>(of_row.weight * a.tau) : 0.0f;
+      if (!kTeacher && some) coef = finish_row(a, row, sh.row[now], of_row, t, st, lane, true);
+      if (lane == 0) {
+        if (!some) put_nothing<kTeacher>(a, row);
+        sh.coef = coef;
+      }
+      if (next < rows) put_asked(a, next, asked, sh.row[now ^ 1], lane);
+    }
+    __syncthreads();
+    const bool then = next < rows && uniform(sh.row[now ^ 1].used) != 0;
+    if (w == 0) {
+      if (lane == 0) sh.next = take();
+      if (kTeacher && some) finish_row(a, row, sh.row[now], of_row, t, st, lane, true);
+      if (then) t = finish_entries<T, kTeacher, true>(a, next, sh.row[now ^ 1], lane);
+      of_row = asked;
+    }
+    T* out = a.grad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
+    const T* ahead = static_cast<const T*>(a.logits) + next * a.stride;
+    const float coef = some ? sh.coef : 0.0f;
+    const Powers p = Powers::fast(some ? uniform(base(st.m)) : 0.0f, a.c);
+    const float scale = some ? coef / st.s * p.fix : 0.0f;
+    const bool plain = some && !far && out;
+    keep_packed(x);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      if (vec(i) < vecs) {
+        if (plain) store_at<sizeof(T)>(place(out, i), gradient<true, T>(x[i], p, scale));
+        if (then) x[i] = load_at<u32x4, sizeof(T)>(place(ahead, i));
+      }
+    }
+    if (plain) {
+      for (int v = vec(kVecs); v < vecs; v += kThreads)
+        store_at<sizeof(T)>(
+            out + static_cast<int64_t>(v) * kPer<T>,
+            gradient<true, T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), p, scale));
+      if (tid < left) put_one(out + end, p.of<true>(last) * scale);
+    } else if (out) {
+      const Powers q(base(st.m), a.c);
+#pragma unroll 1
+      for (int v = tid; v < vecs; v += kThreads) {
+        u32x4 g = {0, 0, 0, 0};
+        if (some)
+          g = gradient<false, T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), q, coef / st.s);
+        store_at<sizeof(T)>(out + static_cast<int64_t>(v) * kPer<T>, g);
+      }
+      if (tid < left) put_one(out + end, some ? q.of<false>(last) * (coef / st.s) : 0.0f);
+    }
+    if (then && tid < left) last = one(ahead + end);
+    stores_done();
+    if (out && some) put_entries<T, kThreads>(a, out, sh.row[now], coef, st, 0, a.vocab);
+    if (next >= rows) break;
+    row = next;
+    z = ahead;
+    now ^= 1;
+  }
+}
+
+// The counter of rows, before the rows.
+__global__ __launch_bounds__(64) void loss_begin_kernel(const LossArgs a) {
+  if (threadIdx.x == 0) *a.counter = 0;
 }
 
 // -------------------------------------------------------- a row in pieces
@@ -415,7 +597,8 @@ __global__ __launch_bounds__(kPieceThreads) void loss_stats_kernel(const LossArg
   const int v0 = blockIdx.x * a.chunk, v1 = v0 + a.chunk < vecs ? v0 + a.chunk : vecs;
   const bool end = static_cast<int>(blockIdx.x) + 1 == a.chunks;
   Stats st = kNoStats;
-  for (int v = v0 + tid; v < v1; v += kPieceThreads * kPieceVecs) {
+  // all lanes of a wave go round together
+  for (int v = v0 + tid; v - lane < v1; v += kPieceThreads * kPieceVecs) {
     u32x4 x[kPieceVecs];
 #pragma unroll
     for (int i = 0; i < kPieceVecs; ++i) {
@@ -423,14 +606,14 @@ __global__ __launch_bounds__(kPieceThreads) void loss_stats_kernel(const LossArg
       if (v + i * kPieceThreads < v1)
         x[i] = load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v + i * kPieceThreads) * kPer<T>);
     }
-    float m = st.m;
+    Stats o = kNoStats;
 #pragma unroll
-    for (int i = 0; i < kPieceVecs; ++i) m = top_of<T>(m, x[i]);
-    const float at = base(m);
-    st.s *= exp2_fast((st.m - at) * a.c);
-    st.m = m;
+    for (int i = 0; i < kPieceVecs; ++i) o.m = top_of<T>(o.m, x[i]);
+    o.m = uniform(most_of_wave(o.m));
+    const Powers p(base(o.m), a.c);
 #pragma unroll
-    for (int i = 0; i < kPieceVecs; ++i) st.s += sum_of<T>(x[i], at, a.c);
+    for (int i = 0; i < kPieceVecs; ++i) o.s += sum_of<false, T>(x[i], p);
+    st = joined(st, o, a.c);
   }
   if (end && tid < left) {
     Stats o;
@@ -457,7 +640,7 @@ __global__ __launch_bounds__(kPieceThreads) void loss_stats_kernel(const LossArg
 template <typename T, bool kTeacher>
 __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArgs a) {
   constexpr int kWaves = kPieceThreads / 64;
-  __shared__ Shared<kTeacher, kWaves> sh;
+  __shared__ __align__(16) Shared<kTeacher, kWaves> sh;
   const int tid = threadIdx.x, lane = tid & 63, w = uniform(tid >> 6);
   const int64_t row = blockIdx.y;
   const T* z = static_cast<const T*>(a.logits) + row * a.stride;
@@ -473,25 +656,27 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
   st = over_wave(st, a.c);
   const bool empty = st.s == 0.0f;
   if (w == 0) {
-    const Teacher t = read_entries<T, kTeacher, kWaves, false>(a, row, sh, lane);
+    Entries<kTeacher>& e = sh.row[0];
+    const Asked of_row = ask<kTeacher>(a, row, lane);
+    put_asked(a, row, of_row, e, lane);
     for (int j = lane; j < a.top; j += 64)
-      if (sh.id[j] >= 0) sh.z[j] = as_global<float>(a.picked)[row * a.top + j];
+      if (e.id[j] >= 0) e.z[j] = as_global<float>(a.picked)[row * a.top + j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // lane 0's flag
     const bool first = blockIdx.x == 0;
-    if (sh.used != 0 && !empty) {
-      finish_row<kTeacher>(a, row, sh, t, st, lane, first);
+    if (e.used != 0 && !empty) {
+      const Teacher t = finish_entries<T, kTeacher, false>(a, row, e, lane);
+      const float coef = finish_row(a, row, e, of_row, t, st, lane, first);
+      if (lane == 0) sh.coef = coef;
     } else if (lane == 0) {
-      sh.used = 0;
-      if (first) {
-        a.loss[row] = 0.0f;
-        if constexpr (!kTeacher) a.logp[row] = 0.0f;
-      }
+      e.used = 0;
+      if (first) put_nothing<kTeacher>(a, row);
     }
   }
   if (!out) return;
   __syncthreads();
-  const bool used = sh.used != 0;
-  const float scale = used ? sh.coef / st.s : 0.0f, m = base(st.m);
+  const bool used = sh.row[0].used != 0;
+  const Powers p(base(st.m), a.c);
+  const float scale = used ? sh.coef / st.s : 0.0f;
   for (int v = v0 + tid; v < v1; v += kPieceThreads * kPieceVecs) {
     u32x4 x[kPieceVecs];
 #pragma unroll
@@ -502,22 +687,25 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
     for (int i = 0; i < kPieceVecs; ++i)
       if (v + i * kPieceThreads < v1)
         store_at<sizeof(T)>(out + static_cast<int64_t>(v + i * kPieceThreads) * kPer<T>,
-                            used ? gradient<T>(x[i], m, a.c, scale) : u32x4{0, 0, 0, 0});
+                            used ? gradient<false, T>(x[i], p, scale) : u32x4{0, 0, 0, 0});
   }
   if (end && tid < left) {
     const int64_t v = static_cast<int64_t>(vecs) * kPer<T> + tid;
-    put_one(out + v, used ? exp2_fast((one(z + v) - m) * a.c) * scale : 0.0f);
+    put_one(out + v, used ? p.of<false>(one(z + v)) * scale : 0.0f);
   }
   if (!used) return;
   stores_done();
-  put_entries<T, kPieceThreads>(a, out, sh, st, v0 * kPer<T>, end ? a.vocab : v1 * kPer<T>);
+  put_entries<T, kPieceThreads>(a, out, sh.row[0], sh.coef, st, v0 * kPer<T>, end ? a.vocab : v1 * kPer<T>);
 }
 
 // ---------------------------------------------------------------------- host
 
+constexpr int64_t kCus = 256;
+
 // How a call's rows are cut.
 struct Shape {
   int32_t chunks = 1, chunk = 0;
+  int32_t lanes = 0, grid = 0;       // rows in one piece: a workgroup's lanes, and how many of them
   int64_t stats = 0, bytes = 0;      // workspace: the statistics, all
 };
 template <typename T>
@@ -533,7 +721,11 @@ Shape shape_of(int64_t rows, int64_t vocab, int64_t top) {
   if (s.chunks > 1) {
     s.stats = rows * s.chunks * 8;
     s.bytes = ceil_div(s.stats + rows * top * 4, 16) * 16;
+    return s;
   }
+  s.lanes = vecs <= 256 * 16 ? 256 : vecs <= 512 * 16 ? 512 : 1024;
+  s.grid = static_cast<int32_t>(s.lanes == 1024 ? std::min(rows, kCus) : rows);
+  if (rows > s.grid) s.bytes = 16;
   return s;
 }
 Shape shape_for(zr_dtype dtype, int64_t rows, int64_t vocab, int64_t top) {
@@ -582,12 +774,16 @@ zr_status launch_loss(LossArgs& a, const Shape& s, hipStream_t stream) {
               loss_piece_kernel<T, kTeacher>);
     return launched("loss launch");
   }
-  const int64_t vecs = a.vocab / kPer<T>;
-  const uint32_t rows = static_cast<uint32_t>(a.rows);
-  if (vecs <= 256 * 4) ZR_LAUNCH(rows, 256, stream, a, loss_row_kernel<T, kTeacher, 256, 4>);
-  else if (vecs <= 256 * 16) ZR_LAUNCH(rows, 256, stream, a, loss_row_kernel<T, kTeacher, 256, 16>);
-  else if (vecs <= 512 * 16) ZR_LAUNCH(rows, 512, stream, a, loss_row_kernel<T, kTeacher, 512, 16>);
-  else ZR_LAUNCH(rows, 1024, stream, a, loss_row_kernel<T, kTeacher, 1024, 16>);
+  if (a.rows > s.grid) {
+    a.counter = reinterpret_cast<int32_t*>(a.stats);
+    ZR_LAUNCH(1, 64, stream, a, loss_begin_kernel);
+    const zr_status st = launched("loss counter launch");
+    if (st != ZR_OK) return st;
+  }
+  if (a.vocab / kPer<T> <= 256 * 4) ZR_LAUNCH(s.grid, 256, stream, a, loss_row_kernel<T, kTeacher, 256, 4>);
+  else if (s.lanes == 256) ZR_LAUNCH(s.grid, 256, stream, a, loss_row_kernel<T, kTeacher, 256, 16>);
+  else if (s.lanes == 512) ZR_LAUNCH(s.grid, 512, stream, a, loss_row_kernel<T, kTeacher, 512, 16>);
+  else ZR_LAUNCH(s.grid, 1024, stream, a, loss_row_kernel<T, kTeacher, 1024, 16>);
   return launched("loss launch");
 }
 
@@ -603,11 +799,12 @@ zr_status run_loss(LossArgs& a, zr_dtype dtype, int64_t vocab, int64_t top, zr_i
   a.top = static_cast<int32_t>(top);
   a.wide = ids_type == ZR_I64;
   a.tau = temperature;
+  a.inverse_tau = 1.0 / temperature;
   a.c = static_cast<float>(1.4426950408889634 / temperature);
   a.chunks = s.chunks;
   a.chunk = s.chunk;
   a.stats = static_cast<float*>(workspace);
-  a.picked = s.bytes > 0 ? a.stats + s.stats / 4 : nullptr;
+  a.picked = s.chunks > 1 ? a.stats + s.stats / 4 : nullptr;
   return dtype == ZR_BF16 ? launch_loss<uint16_t, kTeacher>(a, s, stream)
                           : launch_loss<float, kTeacher>(a, s, stream);
 }
@@ -678,9 +875,11 @@ extern "C" zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t 
     a.weight = weight;
     a.loss = loss;
     a.logp = logp;
-    a.clip_low = clip_low;
-    a.clip_high = clip_high;
-    a.kl = kl;
+    a.clip_low = static_cast<float>(1.0 - clip_low);
+    a.clip_high = static_cast<float>(1.0 + clip_high);
+    a.log_low = std::log(1.0 - clip_low);
+    a.log_high = std::log(1.0 + clip_high);
+    a.kl = static_cast<float>(kl);
     a.rows = rows;
     zr_status st = check_loss(a, dtype, vocab, 1, token_type, "tokens", temperature);
     if (st != ZR_OK) return st;
