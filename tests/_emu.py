@@ -22,9 +22,9 @@ SANITIZED = ["-O1", "-fno-omit-frame-pointer", "-fsanitize=address,undefined",
              "-fno-sanitize-recover=all", "-ffp-contract=off"]
 
 
-def build(tmp_path, sources, driver):
+def build(tmp_path, sources, driver, *flags):
     """The driver with the library's ``sources`` (of csrc), sanitized."""
-    units = [(os.path.join(CSRC, s), SANITIZED) for s in (*sources, "zr_plan.cpp")]
+    units = [(os.path.join(CSRC, s), [*SANITIZED, *flags]) for s in (*sources, "zr_plan.cpp")]
     # the coroutines and the plain loops
     units += [(os.path.join(NATIVE, "emu_waves", "waves.cpp"), ["-O2"]),
               (os.path.join(NATIVE, driver + ".cpp"), ["-O2"])]

@@ -24,7 +24,20 @@ void product_case(Rng& r, int seed) {
     (input ? n_out : n_in) = r.uni(520, 900) / 8 * 8 + (even ? 0 : r.uni(0, 7));
     (input ? n_in : n_out) = r.uni(1, 20) * (even ? 8 : 1);
   }
-  const int64_t experts = r.pick<int64_t>({1, 1, 2, 3, 5, 140});
+  // sizes whose tiles are large, and whose sums are in pieces too
+  const bool wide = !small && r.one_in(3);
+  if (wide) {
+    const bool pieces = r.one_in(2);
+    (input ? n_out : n_in) = r.uni(pieces ? 225 : 17, pieces ? 240 : 22) * 8 + (even ? 0 : r.uni(1, 7));
+    (input ? n_in : n_out) = r.uni(17, 20) * 8 + (even ? 0 : r.uni(1, 7));
+  }
+  const bool deep = !wide && r.one_in(6);   // pieces of few tiles
+  if (deep) {
+    (input ? n_out : n_in) = r.uni(300, 310) * 8 + (even ? 0 : r.uni(1, 7));
+    (input ? n_in : n_out) = r.uni(1, 5) * 8 + (even ? 0 : r.uni(1, 7));
+  }
+  if (even && r.one_in(4)) (input ? n_out : n_in) -= r.uni(1, 7);   // a last unit of k that is not whole
+  const int64_t experts = wide || deep ? 1 : r.pick<int64_t>({1, 1, 2, 3, 5, 140});
   const int64_t depth = input ? n_out : n_in, cols = input ? n_in : n_out;
   const int64_t lead = even ? 8 * r.uni(0, 2) : r.uni(0, 9);
   std::vector<int64_t> numels, params, counts;
@@ -40,7 +53,9 @@ void product_case(Rng& r, int seed) {
   for (int64_t k = 0; k < experts; ++k) {
     params.push_back((lead ? 1 : 0) + (experts > 5 ? r.uni(0, 1) : k));
     int64_t c = r.one_in(4) ? 0 : small || experts > 5 ? r.uni(1, experts > 5 ? 3 : 64) : r.pick<int64_t>({1, 65, 128, 200, 257, 300});
-    if (depth * cols > 200 * 200) c = std::min<int64_t>(c, 130);
+    if (wide) c = depth > 1000 ? r.uni(130, 160) : r.uni(400, 500);
+    else if (deep) c = r.pick<int64_t>({1, 30, 40, 64, 66, 80});
+    else if (depth * cols > 200 * 200) c = std::min<int64_t>(c, 130);
     counts.push_back(c);
     rows += c;
   }
@@ -68,7 +83,8 @@ void product_case(Rng& r, int seed) {
     const int64_t f = plan.offset(params[size_t(e)]) + (in_major ? i * n_out + o : o * n_in + i);
     return parts[size_t(f / plan.part)]->at(f % plan.part);
   };
-  Rows x(rows, depth, depth + (even ? r.pick<int64_t>({0, 8}) : r.pick<int64_t>({0, 1, 5})), true, even ? 0 : r.uni(0, 7));
+  Rows x(rows, depth, even ? (depth + 7) / 8 * 8 + r.pick<int64_t>({0, 8}) : depth + r.pick<int64_t>({0, 1, 5}), true,
+         even ? 0 : r.uni(0, 7));
   for (int64_t t = 0; t < used; ++t)
     for (int64_t k = 0; k < depth; ++k) x.put(t * x.stride + k, float(r.uni(-2, 2)));
   Rows y(rows, cols, cols + r.pick<int64_t>({0, 0, 1, 8}), r.one_in(2), r.uni(0, 7));

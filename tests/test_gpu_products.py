@@ -107,6 +107,35 @@ def test_whole_numbers(input_grad, in_major):
         c.check(exact=True)
 
 
+# (rows, columns, depth) that every shape of tiles is the choice for, with its sums
+# whole and in pieces, on 16 bytes and off them
+TILES = [(30, 256, 64), (9, 128, 9600), (300, 1024, 256), (42, 32, 2048), (4118, 928, 64), (3609, 32, 9520),
+         (2886, 4240, 144), (149, 11520, 4096)]
+
+
+@pytest.mark.parametrize("off", (0, 1))
+@pytest.mark.parametrize("columns", (False, True))
+@pytest.mark.parametrize("tiles", TILES, ids=lambda t: "x".join(map(str, t)))
+def test_every_shape_of_tiles(tiles, columns, off):
+    rows, cols, depth = tiles[0], tiles[1] + off, tiles[2] + off
+    n_out, n_in = (depth, cols) if columns else (cols, depth)
+    c = Case(5, n_out, n_in, [rows], columns, bf16=False, whole=True, world=2, align=1 if off else 8)
+    c.call()
+    c.check(exact=True)
+
+
+@pytest.mark.parametrize("counts", ([3], [70], [900]))
+def test_rows_on_16_bytes_with_a_ragged_end(counts):
+    """What stands behind a row's last element is not multiplied."""
+    for k, (n_out, n_in) in enumerate(((203, 128), (1001, 256))):
+        c = Case(k, n_out, n_in, counts, True, align=8, bf16=False, whole=True)
+        wide = torch.full((c.rows, (n_out + 7) // 8 * 8), float("nan"), device="cuda", dtype=torch.bfloat16)
+        wide[:, :n_out] = c.x
+        c.x = wide[:, :n_out]
+        c.call()
+        c.check(exact=True)
+
+
 def test_many_groups_and_repeated_weights():
     rng = np.random.default_rng(0)
     for n, most in ((300, 5), (140, 90)):

@@ -13,13 +13,16 @@ from tests import _emu
 
 pytestmark = pytest.mark.skipif(not os.path.exists(_emu.CLANG), reason="ROCm clang++ not available")
 
-SHAPES = ("Shape<256, 256, 2, 4, 64, 2>", "Shape<32, 128, 1, 4, 64, 4>")
-REQUIRED = ([f"product_kernel<(anonymous namespace)::{s}, {c}, {d}>" for s in SHAPES
-             for c in ("false", "true") for d in ("false", "true")] +
+SHAPES = ("Shape<32, 128, 1, 4, 64, 4>", "Shape<64, 128, 1, 4, 64, 3>", "Shape<128, 128, 2, 2, 64, 2>",
+          "Shape<256, 256, 2, 4, 64, 2>")
+REQUIRED = ([f"{k}<(anonymous namespace)::{s}, {c}>" for k in ("product_kernel", "product_any_kernel")
+             for s in SHAPES for c in ("false", "true")] +
             [f"product_join_kernel<(anonymous namespace)::{s}>" for s in SHAPES])
 
 
 def test_product_kernels_on_cpu_under_asan_ubsan(tmp_path):
-    exe = _emu.build(tmp_path, ["zr_product.hip"], "products_emu")
+    # a chip of two compute units: every shape of tiles at sizes that are quick here,
+    # and several tiles to a workgroup
+    exe = _emu.build(tmp_path, ["zr_product.hip"], "products_emu", "-DZR_CUS=2")
     launched = _emu.run(exe, [("60", str(1000 * k)) for k in range(6)], "product")
     assert launched >= set(REQUIRED), set(REQUIRED) - launched

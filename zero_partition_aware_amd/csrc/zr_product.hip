@@ -63,58 +63,53 @@ __device__ __forceinline__ int exchanged_row(int r, int u) {
 template <int kDepth>
 __device__ __forceinline__ int staged_row(int r, int u) { return r * (kDepth * 2) + (exchanged_row<kDepth>(r, u) << 4); }
 
-// Where a weight's tile lies: in partition a up to the element `cut` (counted
-// from the tile's first one), in b from there on.  more: in others too.
+// Where a weight's part lies: in partition a up to the byte `cut` (counted from the
+// part's first one), in b from there to `end`.
 struct Source {
-  uintptr_t a, b;              // as if the tile's first element lay there
-  int64_t cut;
-  bool more;
+  uintptr_t a, b;              // as if the part's first element lay there
+  int64_t cut, end;
 };
 __device__ __forceinline__ Source source_of(const ProductArgs& p, int64_t first, int64_t span) {
   Source s;
-  const int64_t k = first / p.part_numel, at = first - k * p.part_numel;
-  s.cut = p.part_numel - at;
-  s.more = span > s.cut + p.part_numel;
+  // off by one at most: the estimate has 53 bits
+  int k = uniform(static_cast<int>(static_cast<double>(first) * p.part_inverse));
+  if (first < k * p.part_numel) --k;
+  if (first >= (k + 1) * p.part_numel) ++k;
+  const int64_t at = first - k * p.part_numel, left = p.part_numel - at;
+  s.cut = left * 2;
+  s.end = s.cut + (span > left ? p.part_numel * 2 : 0);
   s.a = reinterpret_cast<uintptr_t>(p.part[k]) + at * 2;
-  s.b = span > s.cut ? reinterpret_cast<uintptr_t>(p.part[k + 1]) - s.cut * 2 : s.a;
+  s.b = span > left ? reinterpret_cast<uintptr_t>(p.part[k + 1]) - s.cut : s.a;
   return s;
 }
 
-// `count` (1 to 8) elements from the e-th of a tile on.
-__device__ __forceinline__ u32x4 source_unit(const ProductArgs& p, const Source& s, int64_t first, int64_t e,
-                                             int count) {
-  const char* from = nullptr;
-  if (s.more) {
-    const int64_t k = (first + e) / p.part_numel, at = first + e - k * p.part_numel;
-    if (at + count <= p.part_numel) from = p.part[k] + at * 2;
-  } else if (e + count <= s.cut) {
-    from = reinterpret_cast<const char*>(s.a + e * 2);
-  } else if (e >= s.cut) {
-    from = reinterpret_cast<const char*>(s.b + e * 2);
-  }
-  if (from && count == 8) return load_at<u32x4, 2>(from);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= count) continue;
-    const char* q;
-    if (from) {
-      q = from + 2 * i;
-    } else {
-      const int64_t k = (first + e + i) / p.part_numel;
-      q = p.part[k] + (first + e + i - k * p.part_numel) * 2;
-    }
-    v[i / 2] |= static_cast<uint32_t>(*as_global<uint16_t>(q)) << (16 * (i & 1));
-  }
-  return v;
+// The last `count` (1 to 8) elements of a unit, zeros behind them.
+__device__ __forceinline__ u32x4 last_of(const u32x4& v, int count) {
+  uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
+  const int by = 16 * (8 - count);
+  if (by >= 64) lo = hi, hi = 0;
+  const int rest = by & 63;
+  lo = lo >> rest | hi << 1 << (63 - rest);
+  hi >>= rest;
+  return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+               static_cast<uint32_t>(hi >> 32)};
 }
-__device__ __forceinline__ u32x4 row_unit(const uint16_t* x, int count) {
-  if (count == 8) return load_at<u32x4, 2>(x);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < count) v[i / 2] |= static_cast<uint32_t>(*as_global<uint16_t>(x + i)) << (16 * (i & 1));
-  return v;
+// A row's unit at `from` with `count` elements, zeros behind them (all of it where
+// there are none).  whole: the eight that end with them lie together, and are there;
+// if not, where(i) is the i-th one's address.
+template <typename F>
+__device__ __forceinline__ u32x4 row_end(const char* from, int count, bool whole, F where) {
+  if (count >= 8 && whole) return load_at<u32x4, 2>(from);
+  if (count > 0 && whole) return last_of(load_at<u32x4, 2>(from + 2 * (count - 8)), count);
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int i = 0; i < (count < 8 ? count : 8); ++i) {
+    const uint64_t v = *as_global<uint16_t>(where(i));
+    if (i < 4) lo |= v << (16 * i);
+    else hi |= v << (16 * (i - 4));
+  }
+  return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+               static_cast<uint32_t>(hi >> 32)};
 }
 
 // A matrix whose rows run along n: its 16-byte units are exchanged by the row's
@@ -165,54 +160,6 @@ __device__ __forceinline__ Place place_of(const ProductArgs& a, int tile) {
   return p;
 }
 
-// One step's units of a thread, in registers.
-template <typename S>
-struct Staged {
-  u32x4 x[S::kXLoads], w[S::kWLoads];
-};
-// kColumns: n is the weight's fast axis.
-template <typename S, bool kColumns>
-__device__ __forceinline__ void load_step(Staged<S>& s, const ProductArgs& a, const Place& p, int k0, int tid) {
-  const int left = a.depth - k0 < S::kDepth ? a.depth - k0 : S::kDepth;
-#pragma unroll
-  for (int j = 0; j < S::kXLoads; ++j) {
-    const int at = j * S::kThreads + tid, r = at / S::kUnits, u = 8 * (at % S::kUnits);
-    s.x[j] = u32x4{0, 0, 0, 0};
-    if (r < p.rows && u < left)
-      s.x[j] = row_unit(p.x + r * a.x_stride + k0 + u, left - u < 8 ? left - u : 8);
-  }
-  const int64_t first = p.w + (kColumns ? static_cast<int64_t>(k0) * a.cols + p.col
-                                        : static_cast<int64_t>(p.col) * a.depth + k0);
-  const int64_t span = kColumns ? static_cast<int64_t>(left - 1) * a.cols + p.cols
-                                : static_cast<int64_t>(p.cols - 1) * a.depth + left;
-  const Source src = source_of(a, first, span);
-#pragma unroll
-  for (int j = 0; j < S::kWLoads; ++j) {
-    constexpr int kPerRow = kColumns ? S::kCols / 8 : S::kUnits;
-    const int at = j * S::kThreads + tid, r = at / kPerRow, u = 8 * (at % kPerRow);
-    const int high = kColumns ? left : p.cols, wide = kColumns ? p.cols : left;
-    s.w[j] = u32x4{0, 0, 0, 0};
-    if (r < high && u < wide)
-      s.w[j] = source_unit(a, src, first, static_cast<int64_t>(r) * (kColumns ? a.cols : a.depth) + u,
-                           wide - u < 8 ? wide - u : 8);
-  }
-}
-template <typename S, bool kColumns>
-__device__ __forceinline__ void store_step(const Staged<S>& s, char* lds, int tid) {
-#pragma unroll
-  for (int j = 0; j < S::kXLoads; ++j) {
-    const int at = j * S::kThreads + tid;
-    *reinterpret_cast<u32x4*>(lds + staged_row<S::kDepth>(at / S::kUnits, at % S::kUnits)) = s.x[j];
-  }
-#pragma unroll
-  for (int j = 0; j < S::kWLoads; ++j) {
-    constexpr int kPerRow = kColumns ? S::kCols / 8 : S::kUnits;
-    const int at = j * S::kThreads + tid, r = at / kPerRow, u = at % kPerRow;
-    const int to = kColumns ? staged_column<S::kCols>(r, u) : staged_row<S::kDepth>(r, u);
-    *reinterpret_cast<u32x4*>(lds + S::kXBytes + to) = s.w[j];
-  }
-}
-
 // What a unit behind the last k is read from.
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
@@ -236,6 +183,101 @@ struct RowUnits {
     return (j * kHigh < rows ? (j + 1) * kHigh : kHigh) > rows ? some : all;
   }
 };
+
+// One step's units of a thread, in registers.
+template <typename S>
+struct Staged {
+  u32x4 x[S::kXLoads], w[S::kWLoads];
+};
+// A thread's places in the steps of a tile that lies anywhere (kColumns: n is the
+// weight's fast axis).  A unit on any address is one load, at the rate of an aligned
+// one.
+template <typename S, bool kColumns>
+struct Anywhere {
+  static constexpr int kWWide = kColumns ? S::kCols / 8 : S::kUnits, kWHigh = S::kThreads / kWWide;
+  RowUnits<S::kThreads / S::kUnits> xu;
+  RowUnits<kWHigh> wu;
+  int x_k, w_row, w_unit;      // the first k of the thread's units of x; its row and unit of the weight's
+  __device__ __forceinline__ Anywhere(const ProductArgs& a, const Place& p, int tid)
+      : xu(tid / S::kUnits, tid % S::kUnits, p.rows, a.x_stride * 2),
+        wu(tid / kWWide, unit_of(p, tid) / 8, kColumns ? S::kDepth : p.cols, (kColumns ? a.cols : a.depth) * 2),
+        x_k(8 * (tid % S::kUnits)), w_row(tid / kWWide), w_unit(unit_of(p, tid)) {}
+  // What is behind the last column is never stored: any unit that is there will do,
+  // and the next row's elements behind a row's last.
+  static __device__ __forceinline__ int unit_of(const Place& p, int tid) {
+    const int u = 8 * (tid % kWWide);
+    return kColumns && u >= p.cols ? 0 : u;
+  }
+  __device__ __forceinline__ void load(Staged<S>& s, const ProductArgs& a, const Place& p, int k0) const {
+    const int left = a.depth - k0 < S::kDepth ? a.depth - k0 : S::kDepth;
+    const char* rows = reinterpret_cast<const char*>(p.x) + static_cast<int64_t>(k0) * 2;
+    const int64_t first = p.w + (kColumns ? static_cast<int64_t>(k0) * a.cols + p.col
+                                          : static_cast<int64_t>(p.col) * a.depth + k0);
+    const int64_t span = kColumns ? static_cast<int64_t>(left - 1) * a.cols + p.cols
+                                  : static_cast<int64_t>(p.cols - 1) * a.depth + left;
+    const Source src = source_of(a, first, span);
+    uint32_t x_at[S::kXLoads], w_at[S::kWLoads];
+#pragma unroll
+    for (int j = 0; j < S::kXLoads; ++j) {
+      uint32_t off = xu.unit(j);
+      ZR_OPAQUE_IN(off, k0);
+      x_at[j] = xu.group(j) + off;
+    }
+    bool plain = left == S::kDepth;
+#pragma unroll
+    for (int j = 0; j < S::kWLoads; ++j) {
+      uint32_t off = wu.unit(j);
+      ZR_OPAQUE_IN(off, k0);
+      w_at[j] = wu.group(j) + off;
+      plain = plain && (w_at[j] + 16ll <= src.cut || (w_at[j] >= src.cut && w_at[j] + 16ll <= src.end));
+    }
+    // A wave whose units are all whole and each in one partition: no branches
+    // between its loads, so that each is waited for by itself.
+    if (__ballot(!plain) == 0) {
+#pragma unroll
+      for (int j = 0; j < S::kXLoads; ++j) s.x[j] = load_at<u32x4, 2>(rows + x_at[j]);
+#pragma unroll
+      for (int j = 0; j < S::kWLoads; ++j)
+        s.w[j] = load_at<u32x4, 2>(reinterpret_cast<const char*>((w_at[j] < src.cut ? src.a : src.b) + w_at[j]));
+      return;
+    }
+#pragma unroll
+    for (int j = 0; j < S::kXLoads; ++j) {
+      const char* from = rows + x_at[j];
+      s.x[j] = row_end(from, left - x_k, a.depth >= 8, [&](int i) { return from + 2 * i; });
+    }
+#pragma unroll
+    for (int j = 0; j < S::kWLoads; ++j) {
+      const int64_t at = w_at[j];
+      const int count = !kColumns ? left - w_unit : j * kWHigh + w_row < left ? p.cols - w_unit : 0;
+      // its elements, or, where k is the fast axis, the eight that end with them
+      const int64_t from = kColumns || count >= 8 ? at : at - 2 * (8 - count);
+      const bool in_a = from >= 0 && from + 16 <= src.cut, in_b = from >= src.cut && from + 16 <= src.end;
+      const char* there = reinterpret_cast<const char*>((in_a ? src.a : src.b) + at);
+      auto each = [&](int i) {
+        const int64_t e = first + at / 2 + i, k = e / a.part_numel;
+        return a.part[k] + (e - k * a.part_numel) * 2;
+      };
+      s.w[j] = row_end(there, kColumns && (in_a || in_b) && count > 0 ? 8 : count, (in_a || in_b) && a.depth >= 8, each);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0070 | 0x0f00);   // vmcnt(0), so that the plain steps' waits are what they need
+  }
+};
+template <typename S, bool kColumns>
+__device__ __forceinline__ void store_step(const Staged<S>& s, char* lds, int tid) {
+#pragma unroll
+  for (int j = 0; j < S::kXLoads; ++j) {
+    const int at = j * S::kThreads + tid;
+    *reinterpret_cast<u32x4*>(lds + staged_row<S::kDepth>(at / S::kUnits, at % S::kUnits)) = s.x[j];
+  }
+#pragma unroll
+  for (int j = 0; j < S::kWLoads; ++j) {
+    constexpr int kPerRow = kColumns ? S::kCols / 8 : S::kUnits;
+    const int at = j * S::kThreads + tid, r = at / kPerRow, u = at % kPerRow;
+    const int to = kColumns ? staged_column<S::kCols>(r, u) : staged_row<S::kDepth>(r, u);
+    *reinterpret_cast<u32x4*>(lds + S::kXBytes + to) = s.w[j];
+  }
+}
 
 // Steps straight into LDS: rows and partitions on 16 bytes, a tile's part of the
 // weight (where n is its fast axis, a step's) in two partitions at most.
@@ -532,7 +574,7 @@ __device__ __forceinline__ void clear(Acc<S>& acc) {
 // the next one's first are on their way.  (Each piece has a step for every stage,
 // behind its last k of zeros.)
 template <typename S, bool kColumns>
-__global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs a) {
+__global__ __launch_bounds__(S::kThreads, 2) void product_kernel(const ProductArgs a) {
   static_assert(S::kPhases == 2, "phases in step");
   __shared__ __align__(16) char lds[S::kLds];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
@@ -595,30 +637,40 @@ __global__ __launch_bounds__(S::kThreads) void product_kernel(const ProductArgs 
   meet<0>();
 }
 
-// Rows or partitions anywhere: a step goes through registers.
+// Rows or partitions anywhere: steps go through registers, kStages - 1 of them on
+// their way, into two stages of LDS in turn (the other one's readers are behind the
+// last barrier).
 template <typename S, bool kColumns>
-__global__ __launch_bounds__(S::kThreads) void product_any_kernel(const ProductArgs a) {
-  __shared__ __align__(16) char lds[S::kLds];
+__global__ __launch_bounds__(S::kThreads, 2) void product_any_kernel(const ProductArgs a) {
+  constexpr int kAhead = S::kStages - 1;
+  __shared__ __align__(16) char lds[2 * S::kStage];
   const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6);
   const Work k = work_of<S>(a, blockIdx.x);
   const Reader<S, kColumns> reader(lane, wave);
+  const Anywhere<S, kColumns> in(a, k.p, tid);
   Acc<S> acc = {};
-  Staged<S> next;
-  load_step<S, kColumns>(next, a, k.p, k.s0 * S::kDepth, tid);
+  Staged<S> next[kAhead];
+  // (behind the last step that one again)
+  auto load = [&](Staged<S>& to, int s) { in.load(to, a, k.p, (s < k.s1 ? s : k.s1 - 1) * S::kDepth); };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(next[i], k.s0 + i);
   int at = 0;
 #pragma unroll 1
-  for (int s = k.s0; s < k.s1; ++s) {
-    // two stages in turn: the other one's readers are behind the last barrier
-    store_step<S, kColumns>(next, lds + at, tid);
-    lds_barrier();
-    if (s + 1 < k.s1) load_step<S, kColumns>(next, a, k.p, (s + 1) * S::kDepth, tid);
+  for (int s0 = k.s0; s0 < k.s1; s0 += kAhead) {
 #pragma unroll
-    for (int phase = 0; phase < S::kPhases; ++phase) {
-      Fragments<S> f;
-      reader.read(f, lds + at, phase);
-      multiply<S>(acc, f);
+    for (int i = 0; i < kAhead; ++i) {
+      if (s0 + i >= k.s1) break;
+      store_step<S, kColumns>(next[i], lds + at, tid);
+      lds_barrier();
+      load(next[i], s0 + i + kAhead);
+#pragma unroll
+      for (int phase = 0; phase < S::kPhases; ++phase) {
+        Fragments<S> f;
+        reader.read(f, lds + at, phase);
+        multiply<S>(acc, f);
+      }
+      at = S::kStage - at;
     }
-    at = S::kStage - at;
   }
   put_tile<S>(a, k, acc, lane, wave);
 }
@@ -654,16 +706,68 @@ __global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const Produc
 }
 
 using Large = Shape<256, 256, 2, 4, 64, 2>;
+using Middle = Shape<128, 128, 2, 2, 64, 2>;
+using Low = Shape<64, 128, 1, 4, 64, 3>;
 using Small = Shape<32, 128, 1, 4, 64, 4>;
+constexpr int kShapes = 4;
+template <typename F>
+void with_shape(int shape, F f) {
+  if (shape == 0) f(Small{});
+  else if (shape == 1) f(Low{});
+  else if (shape == 2) f(Middle{});
+  else f(Large{});
+}
 
 // ---------------------------------------------------------------------- host
 
-constexpr int64_t kCus = 256;
+#ifndef ZR_CUS
+#define ZR_CUS 256   // the chip's; the kernels run on a smaller one in tests on the CPU
+#endif
+constexpr int64_t kCus = ZR_CUS;
 
-// How many pieces the sums of a launch are cut into.
-int32_t pieces_of(int64_t tiles, int64_t steps, int64_t slots) {
-  if (tiles * 2 > slots) return 1;
-  return static_cast<int32_t>(std::max<int64_t>(1, std::min(slots / tiles, steps / 4)));
+template <typename S>
+constexpr int64_t kSlots = kCus * (2 * S::kLds > 160 * 1024 ? 1 : 2);   // workgroups that the chip holds
+
+// What a step costs where a CU has one workgroup and where it has two, and what a
+// piece costs beside its steps, in us, measured at 4096 x 4096 with 1 to 4096 rows:
+// straight into LDS, and by way of registers.
+struct Cost {
+  double one, two, piece;
+};
+template <typename S>
+constexpr Cost kCost[2] = {};
+template <>
+constexpr Cost kCost<Small>[2] = {{0.25, 0.5, 1}, {0.7, 0.9, 1}};
+template <>
+constexpr Cost kCost<Low>[2] = {{0.37, 0.6, 1}, {0.95, 1.15, 1}};
+template <>
+constexpr Cost kCost<Middle>[2] = {{0.8, 0.95, 2}, {1.1, 1.45, 2}};
+template <>
+constexpr Cost kCost<Large>[2] = {{1.45, 1.45, 5}, {2.2, 2.2, 5}};
+
+// What a call has to do.
+struct Load {
+  int64_t steps, sums;         // of k; rows times columns
+  bool any;                    // sizes or places that are no multiples of 16 bytes
+};
+
+// What a launch takes, about, with its sums in so many pieces: the rounds of its
+// workgroups, and the second launch that joins the pieces, written and read.
+template <typename S>
+double cost_of(const Load& l, int64_t tiles, int64_t pieces) {
+  const Cost& c = kCost<S>[l.any];
+  const int64_t items = tiles * pieces;
+  const double round = (items > kCus ? c.two : c.one) * static_cast<double>(ceil_div(l.steps, pieces)) + c.piece;
+  const double join = pieces == 1 ? 0 : 3 + static_cast<double>(pieces * l.sums) * 4 * 0.32e-6;
+  return static_cast<double>(ceil_div(items, kSlots<S>)) * round + join;
+}
+// In how many pieces, of four steps or more, that is least.
+template <typename S>
+int32_t pieces_of(const Load& l, int64_t tiles) {
+  int64_t best = 1;
+  for (int64_t k = 2; k <= std::min<int64_t>(32, l.steps / 4) && tiles * k <= kSlots<S>; ++k)
+    if (cost_of<S>(l, tiles, k) < cost_of<S>(l, tiles, best)) best = k;
+  return static_cast<int32_t>(best);
 }
 
 // A launch holds fewer than 2^32 threads (what is cut has few tiles).
@@ -671,19 +775,19 @@ constexpr int64_t kMaxTiles = int64_t(1) << 22;
 
 struct Launch {
   ProductArgs a;
-  bool small;
+  int shape;
   int64_t bytes;
 };
 
 // The call's launches; `a` has what they share.
 template <typename S>
-void add_launches(const ProductArgs& shared, const std::vector<Group>& groups, bool small,
+void add_launches(const ProductArgs& shared, const std::vector<Group>& groups, bool any, int shape,
                   std::vector<Launch>* out) {
   for (size_t k = 0; k < groups.size();) {
     Launch l{};
     l.a = shared;
-    l.small = small;
-    int64_t tiles = 0;
+    l.shape = shape;
+    int64_t tiles = 0, rows = 0;
     l.a.col_tiles = static_cast<int32_t>(ceil_div(shared.cols, S::kCols));
     for (; k < groups.size() && l.a.n < kMaxGroups; ++k) {
       const int64_t more = ceil_div(groups[k].rows, S::kRows) * l.a.col_tiles;
@@ -692,13 +796,38 @@ void add_launches(const ProductArgs& shared, const std::vector<Group>& groups, b
       g.tile0 = static_cast<int32_t>(std::min(tiles, kMaxTiles));
       l.a.group[l.a.n++] = g;
       tiles += more;
+      rows += g.rows;
     }
     l.a.tiles = static_cast<int32_t>(std::min(tiles, kMaxTiles + 1));
-    l.a.pieces = pieces_of(tiles, ceil_div(shared.depth, S::kDepth), small ? 2 * kCus : kCus);
+    l.a.pieces = pieces_of<S>(Load{ceil_div(shared.depth, S::kDepth), rows * shared.cols, any}, tiles);
     l.bytes = l.a.pieces > 1 ? tiles * l.a.pieces * (S::kRows * S::kCols * 4) : 0;
     out->push_back(l);
   }
 }
+
+// The shape of a call's tiles: Small where no group has more rows than one of its
+// tiles; of the others the one that costs least.
+int shape_of(const std::vector<Group>& groups, int64_t rows, int64_t depth, int64_t cols, bool any) {
+  int64_t most = 0;
+  for (const Group& g : groups) most = std::max<int64_t>(most, g.rows);
+  if (most <= Small::kRows) return 0;
+  int best = 0;
+  double least = 0;
+  for (int k = 1; k < kShapes; ++k) {
+    with_shape(k, [&](auto s) {
+      using S = decltype(s);
+      int64_t tiles = 0;
+      for (const Group& g : groups) tiles += ceil_div(g.rows, S::kRows) * ceil_div(cols, S::kCols);
+      const Load l{ceil_div(depth, S::kDepth), rows * cols, any};
+      const double cost = cost_of<S>(l, tiles, pieces_of<S>(l, tiles));
+      if (best == 0 || cost < least) best = k, least = cost;
+    });
+  }
+  return best;
+}
+
+// Rows of whole 16-byte units, X's and the weight's (columns: n is its fast axis).
+bool whole_units(int64_t depth, int64_t cols, bool columns) { return depth % 8 == 0 && (!columns || cols % 8 == 0); }
 
 // Checks a call and plans its launches.  `input`: the gradient of the input.
 zr_status plan_product(const zr_plan* plan, const int64_t* params, const int64_t* counts, int64_t n, int64_t n_out,
@@ -714,6 +843,7 @@ zr_status plan_product(const zr_plan* plan, const int64_t* params, const int64_t
   a.depth = static_cast<int32_t>(input ? n_out : n_in);
   a.cols = static_cast<int32_t>(input ? n_in : n_out);
   std::vector<Group> groups;
+  bool misplaced = false;      // a weight or a partition that does not begin on 16 bytes
   int64_t row = 0;
   for (int64_t k = 0; k < n; ++k) {
     const int64_t p = params[k];
@@ -728,17 +858,16 @@ zr_status plan_product(const zr_plan* plan, const int64_t* params, const int64_t
     if (counts[k] > 0) {
       Group g{};
       g.w = pi.offset;
+      misplaced = misplaced || pi.offset % 8 != 0 || plan->groups[pi.group].part % 8 != 0;
       g.row0 = static_cast<int32_t>(row);
       g.rows = static_cast<int32_t>(counts[k]);
       groups.push_back(g);
     }
     row += counts[k];
   }
-  (void)in_major;
-  int64_t large = 0;
-  for (const Group& g : groups) large = std::max<int64_t>(large, g.rows);
-  if (large > 64) add_launches<Large>(a, groups, false, out);
-  else add_launches<Small>(a, groups, true, out);
+  const bool any = !whole_units(a.depth, a.cols, input != (in_major != 0)) || misplaced;
+  const int shape = shape_of(groups, row, a.depth, a.cols, any);
+  with_shape(shape, [&](auto s) { add_launches<decltype(s)>(a, groups, any, shape, out); });
   for (const Launch& l : *out)
     if (l.a.tiles > kMaxTiles) return fail(ZR_ERR_UNSUPPORTED, "more tiles than a launch holds");
   return ZR_OK;
@@ -749,7 +878,7 @@ zr_status launch_product(const ProductArgs& a, bool columns, bool direct, hipStr
   const int64_t items = int64_t(a.tiles) * a.pieces;
   if (direct) {
     // as many workgroups as the chip holds
-    const int64_t grid = std::min<int64_t>(items, kCus * (2 * S::kLds > 160 * 1024 ? 1 : 2));
+    const int64_t grid = std::min(items, kSlots<S>);
     auto* kernel = columns ? product_kernel<S, true> : product_kernel<S, false>;
     ZR_LAUNCH(grid, S::kThreads, stream, a, kernel);
   } else {
@@ -820,12 +949,12 @@ zr_status run_product(const zr_plan* plan, const int64_t* params, const int64_t*
       a.y_bf16 = y_dtype == ZR_BF16;
       a.y_past = past;
       // a step's part of the weight, in two partitions at most
-      const int64_t wide = columns ? cols : depth;
-      const int64_t span = columns ? (l.small ? Small::kDepth : Large::kDepth) * cols
-                                   : (l.small ? Small::kCols : Large::kCols) * depth;
-      const bool direct = aligned && aligned_to(x, 16) && x_stride % 8 == 0 && wide % 8 == 0 && span <= gi.part;
-      st = l.small ? launch_product<Small>(a, columns, direct, stream)
-                   : launch_product<Large>(a, columns, direct, stream);
+      const bool whole = aligned_to(x, 16) && x_stride % 8 == 0 && whole_units(depth, cols, columns);
+      with_shape(l.shape, [&](auto s) {
+        using S = decltype(s);
+        const int64_t span = columns ? std::min<int64_t>(S::kDepth, depth) * cols : std::min<int64_t>(S::kCols, cols) * depth;
+        st = launch_product<S>(a, columns, aligned && whole && span <= gi.part, stream);
+      });
       if (st != ZR_OK) return st;
     }
     return ZR_OK;
