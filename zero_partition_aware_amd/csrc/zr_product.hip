@@ -94,22 +94,36 @@ __device__ __forceinline__ u32x4 last_of(const u32x4& v, int count) {
   return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
                static_cast<uint32_t>(hi >> 32)};
 }
-// A row's unit at `from` with `count` elements, zeros behind them (all of it where
-// there are none).  whole: the eight that end with them lie together, and are there;
-// if not, where(i) is the i-th one's address.
-template <typename F>
-__device__ __forceinline__ u32x4 row_end(const char* from, int count, bool whole, F where) {
-  if (count >= 8 && whole) return load_at<u32x4, 2>(from);
-  if (count > 0 && whole) return last_of(load_at<u32x4, 2>(from + 2 * (count - 8)), count);
+// `count` elements one by one, zeros behind them; where(i): the i-th one's address.
+// kAtOnce: all eight loads on their way together.
+template <bool kAtOnce, typename F>
+__device__ __forceinline__ u32x4 gathered(int count, F where) {
+  if constexpr (kAtOnce) {
+    uint16_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = *as_global<uint16_t>(where(i < count ? i : count - 1));
+    u32x4 to;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      to[i / 2] = (i < count ? v[i] : 0u) | (i + 1 < count ? static_cast<uint32_t>(v[i + 1]) << 16 : 0u);
+    return to;
+  }
   uint64_t lo = 0, hi = 0;
 #pragma unroll 1
-  for (int i = 0; i < (count < 8 ? count : 8); ++i) {
+  for (int i = 0; i < count; ++i) {
     const uint64_t v = *as_global<uint16_t>(where(i));
     if (i < 4) lo |= v << (16 * i);
     else hi |= v << (16 * (i - 4));
   }
   return u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
                static_cast<uint32_t>(hi >> 32)};
+}
+// The `count` (8 or fewer) elements at `from`, which lie together, zeros behind
+// them.  before: so do eight that end with them.
+__device__ __forceinline__ u32x4 row_end(const char* from, int count, bool before) {
+  if (count >= 8) return load_at<u32x4, 2>(from);
+  if (count > 0 && before) return last_of(load_at<u32x4, 2>(from + 2 * (count - 8)), count);
+  return gathered<false>(count, [&](int i) { return from + 2 * i; });
 }
 
 // A matrix whose rows run along n: its 16-byte units are exchanged by the row's
@@ -243,22 +257,32 @@ struct Anywhere {
     }
 #pragma unroll
     for (int j = 0; j < S::kXLoads; ++j) {
-      const char* from = rows + x_at[j];
-      s.x[j] = row_end(from, left - x_k, a.depth >= 8, [&](int i) { return from + 2 * i; });
+      s.x[j] = row_end(rows + x_at[j], left - x_k, a.depth >= 8);
     }
 #pragma unroll
     for (int j = 0; j < S::kWLoads; ++j) {
       const int64_t at = w_at[j];
       const int count = !kColumns ? left - w_unit : j * kWHigh + w_row < left ? p.cols - w_unit : 0;
-      // its elements, or, where k is the fast axis, the eight that end with them
+      // the eight to load: a unit's, or, behind k's end, those that end with its elements
       const int64_t from = kColumns || count >= 8 ? at : at - 2 * (8 - count);
       const bool in_a = from >= 0 && from + 16 <= src.cut, in_b = from >= src.cut && from + 16 <= src.end;
-      const char* there = reinterpret_cast<const char*>((in_a ? src.a : src.b) + at);
-      auto each = [&](int i) {
-        const int64_t e = first + at / 2 + i, k = e / a.part_numel;
-        return a.part[k] + (e - k * a.part_numel) * 2;
+      auto in_two = [&](int i) {
+        const int64_t e = at + 2 * i;
+        return reinterpret_cast<const char*>((e < src.cut ? src.a : src.b) + e);
       };
-      s.w[j] = row_end(there, kColumns && (in_a || in_b) && count > 0 ? 8 : count, (in_a || in_b) && a.depth >= 8, each);
+      const int few = count < 8 ? count : 8;
+      if (count <= 0) {
+        s.w[j] = u32x4{0, 0, 0, 0};
+      } else if ((in_a || in_b) && (kColumns || a.depth >= 8)) {
+        s.w[j] = row_end(in_two(0), kColumns ? 8 : few, true);
+      } else if (at + 2 * few <= src.end) {
+        s.w[j] = gathered<true>(few, in_two);
+      } else {
+        s.w[j] = gathered<false>(few, [&](int i) {
+          const int64_t e = first + at / 2 + i, k = e / a.part_numel;
+          return a.part[k] + (e - k * a.part_numel) * 2;
+        });
+      }
     }
     __builtin_amdgcn_s_waitcnt(0x0070 | 0x0f00);   // vmcnt(0), so that the plain steps' waits are what they need
   }
@@ -688,6 +712,7 @@ __global__ __launch_bounds__(kJoinThreads) void product_join_kernel(const Produc
   const float* from = a.partial + static_cast<int64_t>(tile) * (S::kRows * S::kCols) + at;
   const int64_t step = static_cast<int64_t>(a.tiles) * (S::kRows * S::kCols);
   f32x4 sum = *as_global<f32x4>(from);
+#pragma unroll 8
   for (int k = 1; k < a.pieces; ++k) sum += *as_global<f32x4>(from + k * step);
   const int64_t to = (p.row + r) * a.y_stride + p.col + c;
   if (!a.y_bf16) {
@@ -761,11 +786,12 @@ double cost_of(const Load& l, int64_t tiles, int64_t pieces) {
   const double join = pieces == 1 ? 0 : 3 + static_cast<double>(pieces * l.sums) * 4 * 0.32e-6;
   return static_cast<double>(ceil_div(items, kSlots<S>)) * round + join;
 }
+constexpr int64_t kMaxPieces = 64;
 // In how many pieces, of four steps or more, that is least.
 template <typename S>
 int32_t pieces_of(const Load& l, int64_t tiles) {
   int64_t best = 1;
-  for (int64_t k = 2; k <= std::min<int64_t>(32, l.steps / 4) && tiles * k <= kSlots<S>; ++k)
+  for (int64_t k = 2; k <= std::min<int64_t>(kMaxPieces, l.steps / 4) && tiles * k <= kSlots<S>; ++k)
     if (cost_of<S>(l, tiles, k) < cost_of<S>(l, tiles, best)) best = k;
   return static_cast<int32_t>(best);
 }
