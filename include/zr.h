@@ -613,7 +613,11 @@ zr_status zr_ipg_accumulate_linear_first(const zr_plan* plan, const zr_linear_gr
  *   rows                  of both matrices; those behind the last count are
  *                         neither read nor written.
  * Products of bf16 values, exact, summed in fp32 on the matrix cores and
- * rounded once to the output's dtype.  Outputs must not overlap inputs.
+ * rounded once to the output's dtype.  Outputs must not overlap inputs.  The
+ * order of a sum goes by the params, the counts and the sizes, not by addresses
+ * and strides.  The workspace, from the query for the same lists and sizes, may be
+ * 0 bytes and null (sums that are not cut into pieces); calls that may run at
+ * once need one each.
  * ZR_ERR_UNSUPPORTED: n_out, n_in or the input's stride of 2^22, or 2^31 rows,
  * or more, or more tiles than a launch holds. */
 zr_status zr_linear_forward_workspace(const zr_plan* plan, const int64_t* params,
@@ -648,8 +652,10 @@ zr_status zr_linear_input_grad(const zr_plan* plan, const int64_t* params, const
  * rounded once: the dy of the layer that made the logits (zr_linear_input_grad,
  * zr_linear_grad).  dlogits may be null (losses only), or be logits itself,
  * pointer and stride, which it then replaces; otherwise outputs must not
- * overlap inputs.  Sums are as above; logarithms, ratios and losses 64-bit,
- * stored in fp32.
+ * overlap inputs.  Sums, exponentials and logarithms are fp32; log q and its
+ * distances from old_logp and ref_logp are 64-bit differences, so that a ratio
+ * next to the clip's border falls on the right side of it; losses are stored in
+ * fp32.
  *   weight[rows]   each row's factor (a mask, one over the tokens of the step);
  *                  null: 1.  Weight 0 gives a loss and a gradient of 0.
  * A row that nothing is asked of (no entry in the vocabulary; logits that are
@@ -657,7 +663,7 @@ zr_status zr_linear_input_grad(const zr_plan* plan, const int64_t* params, const
  * and +inf spread as in the formulas; logits of -inf have q = 0, and logits of
  * the type's lowest value are numbers like others.
  * The workspace (zr_loss_workspace; top 1 for the policy loss) may be 0 bytes
- * and null.
+ * and null; calls that may run at once need one each.
  * ZR_ERR_UNSUPPORTED: vocab of 2^30, more than 1024 entries, or 2^22 rows or
  * more. */
 zr_status zr_loss_workspace(int64_t rows, int64_t vocab, int64_t top, zr_dtype dtype,

@@ -69,25 +69,25 @@ def test_nothing_to_do_needs_no_gpu(fn):
 
 
 def test_workspace():
-    plan = zr.zr_plan_buckets([768 * 2048], [0], [(1, 1)], 1 << 30)
+    plan = zr.zr_plan_buckets([4096 * 4096], [0], [(1, 1)], 1 << 30)
     for call in (zr.zr_linear_forward_workspace, zr.zr_linear_input_grad_workspace):
-        assert call(plan, [0], [0], 768, 2048) == 0 and call(plan, [], [], 768, 2048) == 0
-        assert call(plan, [0], [4], 768, 2048) > 0
-        for bad in (([0], [-1], 768, 2048), ([1], [1], 768, 2048), ([0], [1], 768, 2047), ([0], [1], 0, 0)):
+        assert call(plan, [0], [0], 4096, 4096) == 0 and call(plan, [], [], 4096, 4096) == 0
+        assert call(plan, [0], [4], 4096, 4096) > 0
+        for bad in (([0], [-1], 4096, 4096), ([1], [1], 4096, 4096), ([0], [1], 4096, 4095), ([0], [1], 0, 0)):
             with pytest.raises(zr.ZrError):
                 call(plan, *bad)
         with pytest.raises(zr.ZrError, match="counts has 1"):
-            call(plan, [0, 0], [1], 768, 2048)
+            call(plan, [0, 0], [1], 4096, 4096)
         with pytest.raises(zr.ZrError, match="integers"):
-            call(plan, [0], [1.5], 768, 2048)
+            call(plan, [0], [1.5], 4096, 4096)
     assert lib.zr_linear_forward_workspace(plan.handle, None, None, 0, 1, 1, 0, None) == zr.ZR_ERR_INVALID
 
 
 @pytest.mark.parametrize("fn", CALLS)
 def test_workspace_refusals(fn):
-    plan = zr.zr_plan_buckets([768 * 768], [0], [(1, 1)], 1 << 30)
-    base = dict(plan=plan.handle, params=(0,), counts=(4,), n_out=768, n_in=768, parts=(A,), rows=4, x_stride=768,
-                y_stride=768)
+    plan = zr.zr_plan_buckets([4096 * 4096], [0], [(1, 1)], 1 << 30)
+    base = dict(plan=plan.handle, params=(0,), counts=(4,), n_out=4096, n_in=4096, parts=(A,), rows=4, x_stride=4096,
+                y_stride=4096)
     for change in (dict(), dict(workspace=A, bytes=16), dict(workspace=A + 8, bytes=1 << 30)):
         assert _call(fn, **{**base, **change}) == zr.ZR_ERR_INVALID and "workspace" in zr.zr_last_error()
 
