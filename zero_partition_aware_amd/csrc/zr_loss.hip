@@ -702,19 +702,30 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
 
 constexpr int64_t kCus = 256;
 
-// How a call's rows are cut.
+// How a call's rows are cut.  Few rows in pieces, in two launches; many a row to a
+// workgroup, with as many lanes as hold the row in registers (50257 bf16, 1024
+// rows: 59 us with 512 lanes, 70 with 1024; 32000: 32 with 256, 39 with 512).  us in
+// pieces, and not:
+//     rows               32        64        96       128       256
+//     128256 bf16    15, 20    18, 21    24, 24    28, 26    48, 32
+//     50257 fp32     14, 13    16, 14    19, 15    23, 18    39, 28
+//     300000 bf16    19, 43    33, 53    47, 58   (what registers do not hold is
+//                                                  read twice by a workgroup)
+// Of 1024 lanes a CU holds one workgroup: it takes row after row, the next one's
+// logits ahead.
 struct Shape {
   int32_t chunks = 1, chunk = 0;
   int32_t lanes = 0, grid = 0;       // rows in one piece: a workgroup's lanes, and how many of them
   int64_t stats = 0, bytes = 0;      // workspace: the statistics, all
 };
+constexpr int64_t kRowVecs = 1024 * 16;   // of a row, in a workgroup's registers
 template <typename T>
 Shape shape_of(int64_t rows, int64_t vocab, int64_t top) {
   Shape s;
   const int64_t vecs = vocab / kPer<T>;
   const int64_t wanted = rows > 0 ? ceil_div(1024, rows) : 1;
   const int64_t most = std::max<int64_t>(1, vecs / (kPieceThreads * kPieceVecs));
-  if (rows <= 128 && most > 1) {
+  if (rows <= (vecs > kRowVecs ? 128 : 64) && most > 1) {
     s.chunk = static_cast<int32_t>(ceil_div(vecs, std::min<int64_t>({wanted, most, kMaxChunks})));
     s.chunks = static_cast<int32_t>(ceil_div(vecs, s.chunk));
   }
