@@ -121,7 +121,7 @@ class Case:
 
 
 SIZES = [(1, 1), (3, 7), (2, 40), (5, 1000), (64, 1023), (130, 8192), (130, 8200), (200, 4099), (7, 50257),
-         (1, 128256), (129, 33001)]
+         (1, 128256), (129, 33001), (64, 20001), (65, 20001)]
 
 
 @pytest.mark.parametrize("bf16", [True, False])
@@ -280,6 +280,30 @@ def test_two_streams_and_graphs():
             assert all(torch.equal(a, b) for a, b in zip(eager[::2], (c.loss, c.dlogits)))
             assert c.top or torch.equal(eager[1], c.logp)
             torch.randn(1000, device="cuda").sum().item()
+
+
+def test_two_graphs_share_a_workspace():
+    """Pieces, and rows taken from a counter: nothing outlives a call."""
+    rng = np.random.default_rng(11)
+    cases = [Case(rng, 9, 40000, True, top=8), Case(rng, 300, 70000, True, top=8, masked=0.3),
+             Case(rng, 290, 33000, False, kl=0.1, masked=0.3)]
+    ws = workspace(max(c.ws.numel() for c in cases))
+    graphs = []
+    for c in cases:
+        c.ws = ws
+        c.call()
+        c.check(range(0, len(c.loss), 40))
+        graphs.append((torch.cuda.CUDAGraph(), c.dlogits.clone(), c.loss.clone()))
+        with torch.cuda.graph(graphs[-1][0]):
+            c.call()
+    for _ in range(3):
+        for (g, dlogits, loss), c in zip(graphs, cases):
+            c.dlogits.fill_(3.0)
+            g.replay()
+            assert torch.equal(dlogits, c.dlogits) and torch.equal(loss, c.loss)
+            c.call()
+            assert torch.equal(dlogits, c.dlogits) and torch.equal(loss, c.loss)
+        torch.cuda.synchronize()
 
 
 def test_offsets_past_32_bits():

@@ -209,6 +209,28 @@ def test_two_streams_and_graphs():
         c.check()
 
 
+def test_two_graphs_share_a_workspace():
+    """Sums in pieces: nothing in the workspace outlives a call."""
+    cases = [Case(8, 264, 8192, [3], False, align=8), Case(9, 8192, 256, [70], True, align=8),
+             Case(10, 131, 9001, [40], False)]
+    ws = workspace(max(c.ws.numel() for c in cases))
+    graphs = []
+    for c in cases:
+        c.ws = ws
+        c.call()
+        c.check()
+        graphs.append((torch.cuda.CUDAGraph(), c.y.clone()))
+        with torch.cuda.graph(graphs[-1][0]):
+            c.call()
+    for _ in range(3):
+        for (g, eager), c in zip(graphs, cases):
+            c.wide.fill_(7.5)
+            g.replay()
+            c.call()
+            assert torch.equal(eager, c.y)
+        torch.cuda.synchronize()
+
+
 def test_offsets_past_32_bits():
     """A weight behind 2^32 bytes of its partition, and outputs of more."""
     gen = torch.Generator(device="cuda").manual_seed(0)
