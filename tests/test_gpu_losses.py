@@ -285,8 +285,8 @@ def test_two_streams_and_graphs():
 def test_two_graphs_share_a_workspace():
     """Pieces, and rows taken from a counter: nothing outlives a call."""
     rng = np.random.default_rng(11)
-    cases = [Case(rng, 9, 40000, True, top=8), Case(rng, 300, 70000, True, top=8, masked=0.3),
-             Case(rng, 290, 33000, False, kl=0.1, masked=0.3)]
+    cases = [Case(rng, 9, 40000, True, top=8), Case(rng, 530, 70000, True, top=8, masked=0.3),
+             Case(rng, 520, 33000, False, kl=0.1, masked=0.3)]
     ws = workspace(max(c.ws.numel() for c in cases))
     graphs = []
     for c in cases:

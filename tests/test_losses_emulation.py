@@ -19,7 +19,7 @@ REQUIRED = ([f"loss_stats_kernel<{t}>" for t in ("float", "unsigned short")] +
 
 
 def test_loss_kernels_on_cpu_under_asan_ubsan(tmp_path):
-    exe = _emu.build(tmp_path, ["zr_loss.hip"], "losses_emu")
+    exe = _emu.build(tmp_path, ["zr_loss.hip"], "losses_emu", "-DZR_CUS=40")
     runs = [("1", str(-k)) for k in range(1, 13)] + [("60", str(100 * k)) for k in range(6)]
     launched = _emu.run(exe, runs, "loss")
     assert launched >= set(REQUIRED), set(REQUIRED) - launched

@@ -49,7 +49,7 @@ struct LossArgs {
   int32_t chunks, chunk;           // how many, of how many vectors each
   float* stats;                    // [row][chunk] maximum and sum
   float* picked;                   // [row][entry] its logit
-  int32_t* counter;                // rows taken beyond the first of each workgroup; null: none are
+  int32_t* counter;                // rows taken beyond the first of each workgroup; null: every gridDim.x-th
 };
 
 // -------------------------------------------------------------- a row's data
@@ -447,8 +447,8 @@ __device__ __forceinline__ Stats far_stats(const LossArgs& a, const T* z, Stats*
 // two passes, so that HBM is read once; what is behind them is read twice.  While
 // a row's gradient is written the next one's logits are on their way into the
 // registers that get free, and wave 0 works out its entries.  A workgroup's next
-// row comes from a counter: rows that do not count take a third of the others'
-// time.
+// row comes from a counter, where there are many: rows that do not count take a
+// third of the others' time.
 template <typename T, bool kTeacher, int kThreads, int kVecs>
 __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a) {
   constexpr int kWaves = kThreads / 64;
@@ -457,7 +457,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
   const int rows = static_cast<int>(a.rows);
   const int vecs = a.vocab / kPer<T>, left = a.vocab % kPer<T>;
   const int64_t end = static_cast<int64_t>(vecs) * kPer<T> + tid;   // a lane's of the elements behind the vectors
-  auto take = [&]() { return a.counter ? static_cast<int>(gridDim.x) + atomicAdd(a.counter, 1) : rows; };
+  auto take = [&](int row) { return static_cast<int>(gridDim.x) + (a.counter ? atomicAdd(a.counter, 1) : row); };
   auto vec = [&](int i) { return i * kThreads + tid; };
   // A lane's i-th vector of a row: a uniform address and 32 bits of the lane's,
   // not their sums kept for every i.
@@ -470,7 +470,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
   Asked of_row{};              // of the row, in wave 0
   if (w == 0) {
     of_row = ask<kTeacher>(a, row, lane);
-    if (lane == 0) sh.next = take();
+    if (lane == 0) sh.next = take(row);
     put_asked(a, row, of_row, sh.row[0], lane);
   }
   __syncthreads();
@@ -529,7 +529,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     __syncthreads();
     const bool then = next < rows && uniform(sh.row[now ^ 1].used) != 0;
     if (w == 0) {
-      if (lane == 0) sh.next = take();
+      if (lane == 0) sh.next = take(next);
       if (kTeacher && some) finish_row(a, row, sh.row[now], of_row, t, st, lane, true);
       if (then) t = finish_entries<T, kTeacher, true>(a, next, sh.row[now ^ 1], lane);
       of_row = asked;
@@ -700,7 +700,10 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
 
 // ---------------------------------------------------------------------- host
 
-constexpr int64_t kCus = 256;
+#ifndef ZR_CUS
+#define ZR_CUS 256   // the chip's; the kernels run on a smaller one in tests on the CPU
+#endif
+constexpr int64_t kCus = ZR_CUS;
 
 // How a call's rows are cut.  Few rows in pieces, in two launches; many a row to a
 // workgroup, with as many lanes as hold the row in registers (50257 bf16, 1024
@@ -712,7 +715,9 @@ constexpr int64_t kCus = 256;
 //     300000 bf16    19, 43    33, 53    47, 58   (what registers do not hold is
 //                                                  read twice by a workgroup)
 // Of 1024 lanes a CU holds one workgroup: it takes row after row, the next one's
-// logits ahead.
+// logits ahead; from the third row on from a counter, whose own launch costs 2 to 3
+// us (losses only, 50257 fp32: 512 rows 31 us with it, 27 without; 777 rows 41 and
+// 45, 4096 rows 159 and 171).
 struct Shape {
   int32_t chunks = 1, chunk = 0;
   int32_t lanes = 0, grid = 0;       // rows in one piece: a workgroup's lanes, and how many of them
@@ -736,7 +741,7 @@ Shape shape_of(int64_t rows, int64_t vocab, int64_t top) {
   }
   s.lanes = vecs <= 256 * 16 ? 256 : vecs <= 512 * 16 ? 512 : 1024;
   s.grid = static_cast<int32_t>(s.lanes == 1024 ? std::min(rows, kCus) : rows);
-  if (rows > s.grid) s.bytes = 16;
+  if (rows > 2 * s.grid) s.bytes = 16;
   return s;
 }
 Shape shape_for(zr_dtype dtype, int64_t rows, int64_t vocab, int64_t top) {
@@ -785,7 +790,7 @@ zr_status launch_loss(LossArgs& a, const Shape& s, hipStream_t stream) {
               loss_piece_kernel<T, kTeacher>);
     return launched("loss launch");
   }
-  if (a.rows > s.grid) {
+  if (s.bytes > 0) {
     a.counter = reinterpret_cast<int32_t*>(a.stats);
     ZR_LAUNCH(1, 64, stream, a, loss_begin_kernel);
     const zr_status st = launched("loss counter launch");
