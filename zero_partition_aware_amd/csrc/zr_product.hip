@@ -93,6 +93,21 @@ __device__ __forceinline__ Source source_of(const ProductArgs& p, int64_t first,
   return s;
 }
 
+// Where an element of the flat space lies: the at-th of partition k.
+struct Element {
+  int32_t k;
+  int64_t at;
+};
+__device__ __forceinline__ Element element_of(const ProductArgs& p, int64_t e) {
+  // off by one at most: the estimate has 53 bits
+  Element r;
+  r.k = static_cast<int32_t>(static_cast<double>(e) * p.part_inverse);
+  r.at = e - r.k * p.part_numel;
+  if (r.at < 0) --r.k, r.at += p.part_numel;
+  if (r.at >= p.part_numel) ++r.k, r.at -= p.part_numel;
+  return r;
+}
+
 // The last `count` (1 to 8) elements of a unit, zeros behind them.
 __device__ __forceinline__ u32x4 last_of(const u32x4& v, int count) {
   uint64_t lo = v[0] | static_cast<uint64_t>(v[1]) << 32, hi = v[2] | static_cast<uint64_t>(v[3]) << 32;
@@ -219,6 +234,9 @@ struct Staged {
 template <typename S, bool kColumns>
 struct Anywhere {
   static constexpr int kWWide = kColumns ? S::kCols / 8 : S::kUnits, kWHigh = S::kThreads / kWWide;
+  // Beside a Large tile's sums there are no registers for partitions smaller than
+  // its part of the weight (they would spill: 2000 rows of 4097 x 4095, 177 to 278 us).
+  static constexpr bool kFew = S::kRows <= 128;
   RowUnits<S::kThreads / S::kUnits> xu;
   RowUnits<kWHigh> wu;
   int x_k, w_row, w_unit;      // the first k of the thread's units of x; its row and unit of the weight's
@@ -255,6 +273,26 @@ struct Anywhere {
       w_at[j] = wu.group(j) + off;
       plain = plain && (w_at[j] + 16ll <= src.cut || (w_at[j] >= src.cut && w_at[j] + 16ll <= src.end));
     }
+    // Partitions so small that a step has parts of more than two: each unit's own.
+    if constexpr (kFew) {
+      if (left == S::kDepth && src.end < span * 2) {
+        const char* from[S::kWLoads];
+        bool alone = true;
+#pragma unroll
+        for (int j = 0; j < S::kWLoads; ++j) {
+          const Element e = element_of(a, first + w_at[j] / 2);
+          alone = alone && e.at + 8 <= a.part_numel;
+          from[j] = a.part[e.k] + e.at * 2;
+        }
+        if (__ballot(!alone) == 0) {
+#pragma unroll
+          for (int j = 0; j < S::kXLoads; ++j) s.x[j] = load_at<u32x4, 2>(rows + x_at[j]);
+#pragma unroll
+          for (int j = 0; j < S::kWLoads; ++j) s.w[j] = load_at<u32x4, 2>(from[j]);
+          return;
+        }
+      }
+    }
     // A wave whose units are all whole and each in one partition: no branches
     // between its loads, so that each is waited for by itself.
     if (__ballot(!plain) == 0) {
@@ -280,6 +318,10 @@ struct Anywhere {
         const int64_t e = at + 2 * i;
         return reinterpret_cast<const char*>((e < src.cut ? src.a : src.b) + e);
       };
+      auto each = [&](int i) {
+        const int64_t e = first + at / 2 + i, k = e / a.part_numel;
+        return a.part[k] + (e - k * a.part_numel) * 2;
+      };
       const int few = count < 8 ? count : 8;
       if (count <= 0) {
         s.w[j] = u32x4{0, 0, 0, 0};
@@ -287,11 +329,20 @@ struct Anywhere {
         s.w[j] = row_end(in_two(0), kColumns ? 8 : few, true);
       } else if (at + 2 * few <= src.end) {
         s.w[j] = gathered<true>(few, in_two);
+      } else if constexpr (kFew) {   // in a third partition, or one after that
+        const Element e = element_of(a, first + at / 2);
+        const char* there = a.part[e.k] + e.at * 2;
+        if (count >= 8 && e.at + 8 <= a.part_numel)
+          s.w[j] = load_at<u32x4, 2>(there);
+        else if (a.part_numel >= 8)
+          s.w[j] = gathered<true>(few, [&](int i) {
+            const int64_t r = e.at + i - a.part_numel;
+            return r < 0 ? there + 2 * i : a.part[e.k + 1] + r * 2;
+          });
+        else
+          s.w[j] = gathered<false>(few, each);
       } else {
-        s.w[j] = gathered<false>(few, [&](int i) {
-          const int64_t e = first + at / 2 + i, k = e / a.part_numel;
-          return a.part[k] + (e - k * a.part_numel) * 2;
-        });
+        s.w[j] = gathered<false>(few, each);
       }
     }
     __builtin_amdgcn_s_waitcnt(0x0070 | 0x0f00);   // vmcnt(0), so that the plain steps' waits are what they need
