@@ -1,0 +1,48 @@
+"""The losses at the ends of what their arguments may hold, on the GPU: rows of
+chosen values in the forms that take a row to a workgroup and that cut it into
+pieces.  Where values are compared, tolerances are those of test_gpu_losses.py."""
+
+import numpy as np
+import pytest
+
+from tests._lib import load
+
+pytestmark = pytest.mark.gpu
+
+zr = load()
+torch = pytest.importorskip("torch")
+from tests.test_gpu_losses import Case  # noqa: E402
+
+# whole rows, rows in pieces, and several rows to a workgroup
+FORMS = [(9, 300), (9, 40000), (160, 1500), (600, 66000)]
+
+
+def _put(c, **values):
+    """Replaces the first rows' numbers of a case: weight, old, ref, advantage."""
+    for name, v in values.items():
+        host, dev = dict(weight=(c.w, c.weight), old=(c.old, c.per[0]), ref=(c.ref, c.per[1]),
+                         advantage=(c.adv, c.per[2]))[name]
+        host[:len(v)] = v
+        dev.copy_(torch.from_numpy(host))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_rows_of_weight_0(rows, vocab, bf16, in_place):
+    """Zeros, whatever the row holds; its log-probability is still given."""
+    def values(z):
+        z[0, 5], z[1, 5], z[2, 5] = np.nan, np.inf, -np.inf
+        z[3, :] = -np.inf
+    for top in (0, 3):
+        c = Case(np.random.default_rng(3), rows, vocab, bf16, top=top, kl=0.3, values=values, in_place=in_place)
+        c.ids[:6] = [[7, 8, 9]] * 6 if top else 7
+        c.ids_dev.copy_(torch.from_numpy(c.ids))
+        _put(c, weight=[0.0] * 5, advantage=[1.0, 1.0, 1.0, 1.0, np.nan], ref=[-3.0, -3.0, -3.0, -3.0, np.nan])
+        c.call()
+        c.check([2, 5, 6, 7, rows - 1])
+        bits = c.dlogits[:5].contiguous().view(torch.int16 if bf16 else torch.int32)
+        assert (bits == 0).all() and (c.loss[:5] == 0).all()
+        if not top:
+            logp = c.logp[:5].cpu().numpy()
+            assert np.isnan(logp[:2]).all() and np.isfinite(logp[[2, 4]]).all() and logp[3] == 0

@@ -236,8 +236,11 @@ struct Entries {
   int32_t id[kTop];
   float p[kTop];
   float z[kTop];
-  int32_t used;                // the row counts
+  int32_t used;                // one of the below
 };
+// What is asked of a row: nothing; its log-probability, with a loss and a gradient
+// of 0 (the policy's rows of weight 0, whatever their logits are); all.
+enum { kNothing, kLogpOnly, kAll };
 // And what else a workgroup shares.
 template <bool kTeacher, int kWaves>
 struct Shared {
@@ -291,9 +294,9 @@ __device__ __forceinline__ Asked ask(const LossArgs& a, int64_t row, int lane) {
   return q;
 }
 
-// One wave: puts the row's entries into LDS and finds out whether the row counts:
-// it has an entry in the vocabulary (and, for the teacher's, one above -inf, and a
-// weight).
+// One wave: puts the row's entries into LDS and finds out what is asked of the
+// row: nothing where it has no entry in the vocabulary (for the teacher's, none
+// above -inf, or no weight).
 template <bool kTeacher>
 __device__ __forceinline__ void put_asked(const LossArgs& a, int64_t row, const Asked& q, Entries<kTeacher>& e,
                                           int lane) {
@@ -312,7 +315,7 @@ __device__ __forceinline__ void put_asked(const LossArgs& a, int64_t row, const 
   }
   // four at a time are compared below
   if (kTeacher && lane < (-a.top & 3)) e.id[a.top + lane] = -1;
-  const bool used = __ballot(some) != 0 && (!kTeacher || q.weight != 0.0f);
+  const int used = __ballot(some) == 0 ? kNothing : q.weight != 0.0f ? kAll : kTeacher ? kNothing : kLogpOnly;
   if (lane == 0) e.used = used;
 }
 
@@ -384,7 +387,7 @@ __device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, cons
       a.loss[row] = w == 0.0f ? 0.0f : w * loss;
       a.logp[row] = static_cast<float>(lp);
     }
-    return w == 0.0f ? 0.0f : static_cast<float>(-w * slope * a.inverse_tau);
+    return static_cast<float>(-w * slope * a.inverse_tau);
   }
 }
 // A row that does not count.
@@ -480,7 +483,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) x[i] = filled<T>(-INFINITY);
   Teacher t;
-  if (uniform(sh.row[0].used)) {
+  if (uniform(sh.row[0].used) != kNothing) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
       if (vec(i) < vecs) x[i] = load_at<u32x4, sizeof(T)>(place(z, i));
@@ -492,7 +495,8 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     const int next = uniform(sh.next);
     Asked asked{};
     if (w == 0 && next < rows) asked = ask<kTeacher>(a, next, lane);
-    const bool used = uniform(sh.row[now].used) != 0;
+    const int asks = uniform(sh.row[now].used);
+    const bool used = asks != kNothing;
     if (used) {
       float top = last;
 #pragma unroll
@@ -516,6 +520,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     const bool far = used && st.m != -INFINITY && (st.s == 0.0f || st.s == INFINITY);
     if (far) st = far_stats<T, kThreads>(a, z, sh.wave);
     const bool some = used && st.s != 0.0f;   // not every logit is -inf
+    const bool sloped = some && (kTeacher || asks == kAll);
     if (w == 0) {
       // only the policy's gradient waits for the loss
       float coef = kTeacher ? static_cast<float>(of_row.weight * a.tau) : 0.0f;
@@ -527,7 +532,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
       if (next < rows) put_asked(a, next, asked, sh.row[now ^ 1], lane);
     }
     __syncthreads();
-    const bool then = next < rows && uniform(sh.row[now ^ 1].used) != 0;
+    const bool then = next < rows && uniform(sh.row[now ^ 1].used) != kNothing;
     if (w == 0) {
       if (lane == 0) sh.next = take(next);
       if (kTeacher && some) finish_row(a, row, sh.row[now], of_row, t, st, lane, true);
@@ -536,10 +541,10 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     }
     T* out = a.grad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
     const T* ahead = static_cast<const T*>(a.logits) + next * a.stride;
-    const float coef = some ? sh.coef : 0.0f;
-    const Powers p = Powers::fast(some ? uniform(base(st.m)) : 0.0f, a.c);
-    const float scale = some ? coef / st.s * p.fix : 0.0f;
-    const bool plain = some && !far && out;
+    const float coef = sloped ? sh.coef : 0.0f;
+    const Powers p = Powers::fast(sloped ? uniform(base(st.m)) : 0.0f, a.c);
+    const float scale = sloped ? coef / st.s * p.fix : 0.0f;
+    const bool plain = sloped && !far && out;
     keep_packed(x);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -559,15 +564,15 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
 #pragma unroll 1
       for (int v = tid; v < vecs; v += kThreads) {
         u32x4 g = {0, 0, 0, 0};
-        if (some)
+        if (sloped)
           g = gradient<false, T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), q, coef / st.s);
         store_at<sizeof(T)>(out + static_cast<int64_t>(v) * kPer<T>, g);
       }
-      if (tid < left) put_one(out + end, some ? q.of<false>(last) * (coef / st.s) : 0.0f);
+      if (tid < left) put_one(out + end, sloped ? q.of<false>(last) * (coef / st.s) : 0.0f);
     }
     if (then && tid < left) last = one(ahead + end);
     stores_done();
-    if (out && some) put_entries<T, kThreads>(a, out, sh.row[now], coef, st, 0, a.vocab);
+    if (out && sloped) put_entries<T, kThreads>(a, out, sh.row[now], coef, st, 0, a.vocab);
     if (next >= rows) break;
     row = next;
     z = ahead;
@@ -663,18 +668,18 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
       if (e.id[j] >= 0) e.z[j] = as_global<float>(a.picked)[row * a.top + j];
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // lane 0's flag
     const bool first = blockIdx.x == 0;
-    if (e.used != 0 && !empty) {
+    if (e.used != kNothing && !empty) {
       const Teacher t = finish_entries<T, kTeacher, false>(a, row, e, lane);
       const float coef = finish_row(a, row, e, of_row, t, st, lane, first);
       if (lane == 0) sh.coef = coef;
     } else if (lane == 0) {
-      e.used = 0;
+      e.used = kNothing;
       if (first) put_nothing<kTeacher>(a, row);
     }
   }
   if (!out) return;
   __syncthreads();
-  const bool used = sh.row[0].used != 0;
+  const bool used = sh.row[0].used == kAll;
   const Powers p(base(st.m), a.c);
   const float scale = used ? sh.coef / st.s : 0.0f;
   for (int v = v0 + tid; v < v1; v += kPieceThreads * kPieceVecs) {
