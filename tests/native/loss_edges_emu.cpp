@@ -175,10 +175,35 @@ void weights() {
   in_all_forms("weight 0, kl", Policy{0, false, 0.25}, rows);
 }
 
+// The KL term alone, with a reference anywhere.
+void references() {
+  std::vector<PolicyRow> rows;
+  PolicyRow r;
+  r.z = plain;
+  r.token = 11;
+  r.advantage = 0;
+  r.old = -5;
+  r.weight = 0.75f;
+  for (float x : {-100.0f, -1e6f, -1.7e7f, -3e7f, -1e8f, -1e9f, -3e38f, -INFINITY, 20.0f, 60.0f, INFINITY, kNaN}) {
+    r.ref = x;
+    rows.push_back(r);
+  }
+  for (int k = 0; k < 40; ++k) {   // next to the row's own, and around it
+    r.ref = -13.0f + 0.31f * float(k);
+    rows.push_back(r);
+  }
+  // a token that the policy masks
+  r.z = with(11, -INFINITY);
+  r.ref = -3;
+  rows.push_back(r);
+  in_all_forms("reference", Policy{0, false, 1.0}, rows);
+  in_all_forms("reference, kl < 0", Policy{0, false, -0.01, 1.5}, rows);
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> sections = {{"weights", weights}};
+  const std::map<std::string, void (*)()> sections = {{"weights", weights}, {"references", references}};
   const auto it = sections.find(argc > 1 ? argv[1] : "");
   CHECK(it != sections.end(), "no such section");
   it->second();

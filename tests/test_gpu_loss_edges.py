@@ -11,6 +11,7 @@ pytestmark = pytest.mark.gpu
 
 zr = load()
 torch = pytest.importorskip("torch")
+from tests._layers import U  # noqa: E402
 from tests.test_gpu_losses import Case  # noqa: E402
 
 # whole rows, rows in pieces, and several rows to a workgroup
@@ -46,3 +47,25 @@ def test_rows_of_weight_0(rows, vocab, bf16, in_place):
         if not top:
             logp = c.logp[:5].cpu().numpy()
             assert np.isnan(logp[:2]).all() and np.isfinite(logp[[2, 4]]).all() and logp[3] == 0
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_references_far_from_the_policy(rows, vocab, bf16):
+    far = [-100.0, -1e6, -1.7e7, -3e7, -1e8, -1e9, 5.0, -np.inf]
+    c = Case(np.random.default_rng(4), rows, vocab, bf16, kl=0.5)
+    c.ids[:8] = 7
+    c.ids_dev.copy_(torch.from_numpy(c.ids))
+    _put(c, ref=far, advantage=[0.0] * 8)
+    c.call()
+    c.check(list(range(7)) + [rows - 1])
+    # no reference at all: an infinite loss, whose slope is kl
+    got = c.dlogits[7].double().cpu().numpy()
+    q = torch.softmax(torch.from_numpy(c.z[7]), 0).numpy()
+    q[7] -= 1
+    assert c.loss[7] == np.inf
+    # c.check's bound for a multiple of 0.5 w
+    part = U * (3 * np.log(vocab) + vocab / 256 + 210)
+    want = -0.5 * c.w[7] * q
+    tol = 1.01 * (0.5 * c.w[7] * (np.abs(q) * (part + 300 * U) + 11 * U) + (2.0 ** -8 if bf16 else U) * np.abs(want))
+    assert (np.abs(got - want) <= tol + 2.0 ** -126).all()

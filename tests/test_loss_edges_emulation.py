@@ -25,3 +25,7 @@ def edges(tmp_path_factory):
 
 def test_rows_of_weight_0(edges):
     edges("weights")
+
+
+def test_references_far_from_the_policy(edges):
+    edges("references")

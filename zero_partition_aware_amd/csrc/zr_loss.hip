@@ -41,7 +41,7 @@ struct LossArgs {
   float c;                         // log2(e) / tau
   float clip_low, clip_high;       // the ratio's borders, and their logarithms
   double log_low, log_high;
-  float kl;
+  double kl;
   int32_t wide, teacher_bf16;
   int64_t rows;
   int32_t vocab, top;
@@ -90,21 +90,27 @@ __device__ __forceinline__ double log_of(float s) {
   if (f > 1.41421356f) f *= 0.5f, ++n;
   return n * 0.69314718055994531 + static_cast<double>(__builtin_amdgcn_logf(f) * 0.69314718f);
 }
-// exp(d) - d - 1, to fp32's relative precision.
-__device__ __forceinline__ float exp_minus(float d) {
-  if (d > -0.5f && d < 0.5f) {   // d^2 (1/2 + d/6 + ... + d^7/9!)
+// exp(d) - 1 and exp(d) - d - 1, of an fp32 exponential or series, neither from the
+// other where that would cancel.
+struct AboveOne {
+  double exp, line;
+};
+__device__ __forceinline__ AboveOne above_one(double d) {
+  const float x = static_cast<float>(d);
+  if (x > -0.5f && x < 0.5f) {   // d^2 (1/2 + d/6 + ... + d^7/9!)
     float r = 1.0f / 362880;
-    r = __builtin_fmaf(r, d, 1.0f / 40320);
-    r = __builtin_fmaf(r, d, 1.0f / 5040);
-    r = __builtin_fmaf(r, d, 1.0f / 720);
-    r = __builtin_fmaf(r, d, 1.0f / 120);
-    r = __builtin_fmaf(r, d, 1.0f / 24);
-    r = __builtin_fmaf(r, d, 1.0f / 6);
-    r = __builtin_fmaf(r, d, 0.5f);
-    return r * d * d;
+    r = __builtin_fmaf(r, x, 1.0f / 40320);
+    r = __builtin_fmaf(r, x, 1.0f / 5040);
+    r = __builtin_fmaf(r, x, 1.0f / 720);
+    r = __builtin_fmaf(r, x, 1.0f / 120);
+    r = __builtin_fmaf(r, x, 1.0f / 24);
+    r = __builtin_fmaf(r, x, 1.0f / 6);
+    r = __builtin_fmaf(r, x, 0.5f);
+    const double line = r * d * d;
+    return {d + line, line};
   }
-  const float e = exp_fast(d);
-  return e == INFINITY ? e : e - d - 1.0f;
+  const double e = exp_fast(x) - 1.0;
+  return {e, e == INFINITY ? e : e - d};
 }
 
 // The maximum of some logits and the sum of 2^(c (z - maximum)) over them.  A NaN
@@ -377,14 +383,14 @@ __device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, cons
     float r = exp_fast(static_cast<float>(over));
     r = r > 3.4e38f ? 3.4e38f : r;   // times an advantage of 0 it is 0
     const bool cut = (adv > 0.0f && over > a.log_high) || (adv < 0.0f && over < a.log_low);
-    float loss = -adv * (!cut ? r : adv > 0.0f ? a.clip_high : a.clip_low), slope = cut ? 0.0f : -r * adv;
+    double loss = -adv * (!cut ? r : adv > 0.0f ? a.clip_high : a.clip_low), slope = cut ? 0.0f : -r * adv;
     if (a.ref_logp) {
-      const float d = static_cast<float>(of_row.ref_logp - lp), e = exp_minus(d);
-      loss += a.kl * e;
-      slope -= a.kl * (e == INFINITY ? e : e + d);
+      const AboveOne e = above_one(of_row.ref_logp - lp);
+      loss += a.kl * e.line;
+      slope -= a.kl * e.exp;
     }
     if (lane == 0 && store) {
-      a.loss[row] = w == 0.0f ? 0.0f : w * loss;
+      a.loss[row] = w == 0.0f ? 0.0f : static_cast<float>(w * loss);
       a.logp[row] = static_cast<float>(lp);
     }
     return static_cast<float>(-w * slope * a.inverse_tau);
@@ -900,7 +906,7 @@ extern "C" zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t 
     a.clip_high = static_cast<float>(1.0 + clip_high);
     a.log_low = std::log(1.0 - clip_low);
     a.log_high = std::log(1.0 + clip_high);
-    a.kl = static_cast<float>(kl);
+    a.kl = kl;
     a.rows = rows;
     zr_status st = check_loss(a, dtype, vocab, 1, token_type, "tokens", temperature);
     if (st != ZR_OK) return st;
