@@ -57,12 +57,14 @@ Want want_of(const Policy& c, const PolicyRow& row, const std::vector<double>& z
   w.size *= row.weight;
   w.coef = -row.weight * slope / c.tau;
   if (row.weight == 0) w.loss = w.coef = w.size = 0;
+  // the multiple of q in the gradient is an fp32 number
+  if (std::fabs(w.coef) >= 0x1.ffffffp127) w.coef = std::copysign(kInf, w.coef);
   return w;
 }
 
 // An error that fp32 may make, or the same that is no finite number of fp32.
 bool same(double got, double want, double tolerance) {
-  if (std::fabs(want) > 3.5e38) want = std::copysign(kInf, want);
+  if (std::fabs(want) >= 0x1.ffffffp127) want = std::copysign(kInf, want);
   return got == want || (got != got && want != want) || std::fabs(got - want) <= tolerance;
 }
 
@@ -200,10 +202,40 @@ void references() {
   in_all_forms("reference, kl < 0", Policy{0, false, -0.01, 1.5}, rows);
 }
 
+// Ratios that fp32 does not hold, with advantages of any size, and references as
+// far above the policy.
+void ratios() {
+  std::vector<PolicyRow> rows;
+  PolicyRow r;
+  r.z = plain;
+  r.token = 2;
+  for (float old : {-100.0f, -200.0f, -500.0f, -900.0f, -1e9f, -INFINITY, 100.0f, 1e9f, INFINITY})
+    for (float a : {-0.5f, -3.0f, -1e-10f, -1e-30f, 0.0f, 0.5f, 1e-30f}) {
+      r.old = old;
+      r.advantage = a;
+      rows.push_back(r);
+    }
+  // small weights hold them again
+  r.weight = 1e-20f;
+  r.advantage = -1;
+  for (float old : {-90.0f, -100.0f, -120.0f}) {
+    r.old = old;
+    rows.push_back(r);
+  }
+  in_all_forms("ratio", Policy{0}, rows);
+  rows.clear();
+  r.advantage = 0;
+  for (float ref : {70.0f, 85.0f, 100.0f, 500.0f, 1e9f}) {
+    r.ref = ref;
+    rows.push_back(r);
+  }
+  in_all_forms("reference above", Policy{0, false, 1e-12}, rows);
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> sections = {{"weights", weights}, {"references", references}};
+  const std::map<std::string, void (*)()> sections = {{"weights", weights}, {"references", references}, {"ratios", ratios}};
   const auto it = sections.find(argc > 1 ? argv[1] : "");
   CHECK(it != sections.end(), "no such section");
   it->second();

@@ -69,3 +69,27 @@ def test_references_far_from_the_policy(rows, vocab, bf16):
     want = -0.5 * c.w[7] * q
     tol = 1.01 * (0.5 * c.w[7] * (np.abs(q) * (part + 300 * U) + 11 * U) + (2.0 ** -8 if bf16 else U) * np.abs(want))
     assert (np.abs(got - want) <= tol + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_ratios_that_fp32_does_not_hold(rows, vocab, bf16):
+    """Large ones by their own formula, infinite ones, and any of them with an
+    advantage of 0."""
+    c = Case(np.random.default_rng(5), rows, vocab, bf16, weighted=False)
+    lp = [c.z[i] - np.log(np.exp(c.z[i]).sum()) for i in range(9)]
+    old = np.float32([lp[i][7] - x for i, x in enumerate((60, 100, 500, 100, 1e9, 100, 1e9, 1e9, -1e9))])
+    adv = np.float32([-1e-20, -1e-20, -1e-20, -1e-30, -1e-30, 0.0, 0.0, 1.0, -1.0])
+    old[6] = -np.inf
+    c.ids[:9] = 7
+    c.ids_dev.copy_(torch.from_numpy(c.ids))
+    _put(c, old=old, advantage=adv)
+    c.call()
+    c.check([0, 3, 5, rows - 1])
+    loss, g = c.loss.cpu().numpy(), c.dlogits.float().cpu().numpy()
+    want = [1e-20 * np.exp(lp[i][7] - float(old[i])) for i in (0, 1)]
+    assert np.isclose(loss[0], want[0], rtol=1e-4) and np.isclose(loss[1], want[1], rtol=1e-4)
+    assert loss[2] == np.inf and loss[4] == np.inf and (loss[5:7] == 0).all()
+    # clipped on either side: the border's loss, and no gradient
+    assert np.isclose(loss[7:9], [-1.28, 0.8], rtol=1e-6).all()
+    assert (g[5:9] == 0).all() and g[2, 7] == np.inf

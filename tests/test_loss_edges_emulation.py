@@ -29,3 +29,7 @@ def test_rows_of_weight_0(edges):
 
 def test_references_far_from_the_policy(edges):
     edges("references")
+
+
+def test_ratios_that_fp32_does_not_hold(edges):
+    edges("ratios")

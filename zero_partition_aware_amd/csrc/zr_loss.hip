@@ -39,7 +39,7 @@ struct LossArgs {
   float *loss, *logp;
   double tau, inverse_tau;
   float c;                         // log2(e) / tau
-  float clip_low, clip_high;       // the ratio's borders, and their logarithms
+  double clip_low, clip_high;      // the ratio's borders, and their logarithms
   double log_low, log_high;
   double kl;
   int32_t wide, teacher_bf16;
@@ -79,7 +79,17 @@ __device__ __forceinline__ u32x4 filled(float x) {   // x: exact in bf16
   return u32x4{w, w, w, w};
 }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float exp_fast(float x) { return exp2_fast(x * 1.44269504f); }
+// e^x of any size: the power's fraction in fp32, its whole part in the exponent of 64
+// bits.  What is past that is past fp32 with any fp32 factor too: 0 and infinity.
+__device__ __forceinline__ double exp_of(double x) {
+  const double p = x * 1.4426950408889634;
+  if (p >= 1000.0) return INFINITY;
+  if (p <= -1000.0) return 0.0;
+  if (p != p) return p;
+  const double n = __builtin_rint(p);
+  const uint64_t power = static_cast<uint64_t>(static_cast<int>(n) + 1023) << 52;
+  return static_cast<double>(exp2_fast(static_cast<float>(p - n))) * __builtin_bit_cast(double, power);
+}
 // The natural logarithm of s > 0, off by some 2^-24: of its mantissa in fp32, and
 // the exponent apart.
 __device__ __forceinline__ double log_of(float s) {
@@ -109,7 +119,7 @@ __device__ __forceinline__ AboveOne above_one(double d) {
     const double line = r * d * d;
     return {d + line, line};
   }
-  const double e = exp_fast(x) - 1.0;
+  const double e = exp_of(d) - 1.0;
   return {e, e == INFINITY ? e : e - d};
 }
 
@@ -378,19 +388,19 @@ __device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, cons
     return static_cast<float>(of_row.weight * a.tau);
   } else {
     const double lp = (static_cast<double>(sh.z[0]) - st.m) * a.inverse_tau - log_s;
-    const float w = of_row.weight, adv = of_row.advantage;
+    const double w = of_row.weight, adv = of_row.advantage;
     const double over = lp - of_row.old_logp;
-    float r = exp_fast(static_cast<float>(over));
-    r = r > 3.4e38f ? 3.4e38f : r;   // times an advantage of 0 it is 0
-    const bool cut = (adv > 0.0f && over > a.log_high) || (adv < 0.0f && over < a.log_low);
-    double loss = -adv * (!cut ? r : adv > 0.0f ? a.clip_high : a.clip_low), slope = cut ? 0.0f : -r * adv;
+    // an infinite ratio times an advantage of 0 is 0
+    const double r = exp_of(over), gain = adv == 0.0 && r == INFINITY ? 0.0 : r * adv;
+    const bool cut = (adv > 0.0 && over > a.log_high) || (adv < 0.0 && over < a.log_low);
+    double loss = -(!cut ? gain : adv > 0.0 ? adv * a.clip_high : adv * a.clip_low), slope = cut ? 0.0 : -gain;
     if (a.ref_logp) {
       const AboveOne e = above_one(of_row.ref_logp - lp);
       loss += a.kl * e.line;
       slope -= a.kl * e.exp;
     }
     if (lane == 0 && store) {
-      a.loss[row] = w == 0.0f ? 0.0f : static_cast<float>(w * loss);
+      a.loss[row] = w == 0.0 ? 0.0f : static_cast<float>(w * loss);
       a.logp[row] = static_cast<float>(lp);
     }
     return static_cast<float>(-w * slope * a.inverse_tau);
@@ -902,8 +912,8 @@ extern "C" zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t 
     a.weight = weight;
     a.loss = loss;
     a.logp = logp;
-    a.clip_low = static_cast<float>(1.0 - clip_low);
-    a.clip_high = static_cast<float>(1.0 + clip_high);
+    a.clip_low = 1.0 - clip_low;
+    a.clip_high = 1.0 + clip_high;
     a.log_low = std::log(1.0 - clip_low);
     a.log_high = std::log(1.0 + clip_high);
     a.kl = kl;
