@@ -232,10 +232,39 @@ void ratios() {
   in_all_forms("reference above", Policy{0, false, 1e-12}, rows);
 }
 
+// Rows around 10^8 binary orders from 0, where a row's maximum is no longer the
+// base of its exponentials.
+void far_rows() {
+  for (double tau : {1.0, 1e-8, 1e8}) {
+    const double at = 1e8 * std::log(2.0) * tau;
+    std::vector<PolicyRow> rows;
+    PolicyRow r;
+    r.token = 3;
+    r.old = -4;
+    for (double sign : {-1.0, 1.0})
+      for (int k = -8; k <= 20; ++k) {
+        // a step of fp32 there is 2^-24 to 2^-23 of it, several units of the exponent
+        const double first = sign * at * (1 + k * 0x1p-23), step = at * 0x1p-23;
+        r.z = [=](int64_t v) { return float(v % 5 ? first - step * double(v % 5) : first); };
+        rows.push_back(r);
+        r.z = [=](int64_t v) { return v % 7 ? float(first) : plain(v); };
+        rows.push_back(r);
+        r.weight = 1e-6f;
+        rows.push_back(r);
+        r.weight = 1;
+      }
+    Policy c{0, false, 0, tau};
+    for (int64_t vocab : {301, 5003}) {
+      c.vocab = vocab;
+      check_policy("far", c, rows, false);
+    }
+  }
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
-  const std::map<std::string, void (*)()> sections = {{"weights", weights}, {"references", references}, {"ratios", ratios}};
+  const std::map<std::string, void (*)()> sections = {{"weights", weights}, {"references", references}, {"ratios", ratios}, {"far", far_rows}};
   const auto it = sections.find(argc > 1 ? argv[1] : "");
   CHECK(it != sections.end(), "no such section");
   it->second();

@@ -5,6 +5,7 @@ pieces.  Where values are compared, tolerances are those of test_gpu_losses.py."
 import numpy as np
 import pytest
 
+from oracle.losses import softmax_oracle
 from tests._lib import load
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +94,25 @@ def test_ratios_that_fp32_does_not_hold(rows, vocab, bf16):
     # clipped on either side: the border's loss, and no gradient
     assert np.isclose(loss[7:9], [-1.28, 0.8], rtol=1e-6).all()
     assert (g[5:9] == 0).all() and g[2, 7] == np.inf
+
+
+@pytest.mark.parametrize("tau", [1.0, 1e-8, 1e8])
+@pytest.mark.parametrize("top", [0, 2])
+@pytest.mark.parametrize("vocab", [300, 9001])
+def test_rows_far_from_0(vocab, top, tau):
+    """Around 10^8 binary orders from 0, steps of fp32 apart."""
+    at, rows = 1e8 * np.log(2) * tau, 116
+
+    def values(z):
+        for i in range(rows):
+            first = (-1) ** i * at * (1 + (i // 4 - 8) * 2.0 ** -23)
+            z[i] = first - at * 2.0 ** -23 * (np.arange(vocab) % 5)
+            if i % 4 > 1:
+                z[i, 1::7] = 0.5
+    c = Case(np.random.default_rng(6), rows, vocab, False, top=top, tau=tau, values=values)
+    if not top:   # the row's highest: fp32 holds no ratio to one that is 10^8 orders below
+        c.ids = c.z.argmax(1)
+        c.ids_dev.copy_(torch.from_numpy(c.ids))
+        _put(c, old=np.float32([0.1 + softmax_oracle(z, tau)[1].max() for z in c.z]))
+    c.call()
+    c.check(range(rows))

@@ -33,3 +33,7 @@ def test_references_far_from_the_policy(edges):
 
 def test_ratios_that_fp32_does_not_hold(edges):
     edges("ratios")
+
+
+def test_rows_far_from_0(edges):
+    edges("far")

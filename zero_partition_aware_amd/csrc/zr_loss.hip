@@ -140,10 +140,10 @@ __device__ __forceinline__ Stats joined(const Stats& a, const Stats& b, float c)
 
 // 2^(c (z - m)) for many z, m the same in all lanes.  Fast: an FMA and the
 // exponential, and then `fix` once for all that is off by the rounding of c m.
-// There m is held where c m is under 10^8, so that the rounding is a few units: a
-// sum over logits further out is 0 or infinite, which tells them (logits of the
-// type's lowest value, all of a row's perhaps).  Otherwise the difference is taken
-// first and stays finite.
+// There m is held where c m is under 10^8, so that the rounding is a few units: the
+// sum of a row whose maximum lies further out is not between 1 and its length (it
+// may be 0 or infinite), which tells those rows (logits of the type's lowest value,
+// all of a row's perhaps).  Otherwise the difference is taken first and stays finite.
 struct Powers {
   float m, c, mc, fix;
   __device__ __forceinline__ Powers(float m_, float c_) : m(m_), c(c_), mc(m_ * c_), fix(1.0f) {}
@@ -533,7 +533,8 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     }
     __syncthreads();
     Stats st = over_waves<kWaves>(sh.wave, a.c);
-    const bool far = used && st.m != -INFINITY && (st.s == 0.0f || st.s == INFINITY);
+    // the maximum's term is 1, and there are fewer than 2^30 of them
+    const bool far = used && st.m != -INFINITY && (st.s < 0.5f || st.s > 0x1p31f);
     if (far) st = far_stats<T, kThreads>(a, z, sh.wave);
     const bool some = used && st.s != 0.0f;   // not every logit is -inf
     const bool sloped = some && (kTeacher || asks == kAll);
