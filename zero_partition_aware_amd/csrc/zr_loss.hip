@@ -16,6 +16,7 @@
 // 6,000 cycles a row.)
 
 #include <cmath>
+#include <cstddef>
 #include <type_traits>
 
 #include "zr_layers.h"
@@ -245,15 +246,17 @@ __device__ __forceinline__ V sum_of_wave(V x) {
 // ------------------------------------------------------------- a row's entries
 
 // A row's entries in LDS: their columns (-1: none), what is subtracted from q
-// there, and their logits.
+// there, and their logits.  Four columns are read at a time: each row's lie on 16
+// bytes.
 template <bool kTeacher>
-struct Entries {
+struct alignas(16) Entries {
   static constexpr int kTop = kTeacher ? kMaxTop : 4;
   int32_t id[kTop];
   float p[kTop];
   float z[kTop];
   int32_t used;                // one of the below
 };
+static_assert(sizeof(Entries<true>) % 16 == 0 && offsetof(Entries<true>, id) == 0, "the second row's too");
 // What is asked of a row: nothing; its log-probability, with a loss and a gradient
 // of 0 (the policy's rows of weight 0, whatever their logits are); all.
 enum { kNothing, kLogpOnly, kAll };
