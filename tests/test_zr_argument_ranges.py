@@ -1,0 +1,33 @@
+"""Arguments that do not fit the C call's types are refused, not cut down, and
+what older calls refuse stays refused.  Made without a GPU."""
+
+import pytest
+
+from tests._lib import load
+
+zr = load()
+torch = pytest.importorskip("torch")
+
+
+def _plan():
+    return zr.zr_plan_buckets([48, 48], [0, 0], [(2, 1)], 1000)
+
+
+@pytest.mark.parametrize("query", [zr.zr_linear_forward_workspace, zr.zr_linear_input_grad_workspace])
+@pytest.mark.parametrize("params,counts,words", [
+    ([2 ** 64], [3], "params"), ([-2 ** 63 - 1], [3], "params"), ([0, 2 ** 64 + 1], [3, 4], "params"),
+    ([0], [2 ** 64 + 3], "counts"), ([0, 1], [3, 2 ** 63], "counts"), ([0], [-2 ** 64 + 3], "counts"),
+    ([0.0], [3], "integers"), ([0], [3.0], "integers"), ([0], ["3"], "integers"), ([None], [3], "integers"),
+])
+def test_lists_past_64_bits(query, params, counts, words):
+    with pytest.raises(zr.ZrError, match=words):
+        query(_plan(), params, counts, 8, 6)
+
+
+def test_lists_that_fit():
+    for query in (zr.zr_linear_forward_workspace, zr.zr_linear_input_grad_workspace):
+        for params, counts in (([0, 1], [3, 4]), ((1,), (0,)), ([], []), ([0, 1], range(2))):
+            assert query(_plan(), params, counts, 8, 6) >= 0
+        # the C call's own check
+        with pytest.raises(zr.ZrError, match="param id"):
+            query(_plan(), [2 ** 63 - 1], [3], 8, 6)

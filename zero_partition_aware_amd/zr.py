@@ -999,14 +999,23 @@ def _scratch(workspace, dev):
     return _dense(workspace, "workspace", dev, torch.uint8), workspace.numel()
 
 
+_LIM64 = 1 << 63
+
+
 def _group_list(plan, params, counts):
     """The params and their counts as the C call takes them."""
     n = len(params)
     _expect_len(counts, n, "counts")
     try:
-        return (c_i64 * max(n, 1))(*params), (c_i64 * max(n, 1))(*counts), n
+        lists = (c_i64 * max(n, 1))(*params), (c_i64 * max(n, 1))(*counts), n
     except TypeError:
         raise ZrError(ZR_ERR_INVALID, "params and counts must be integers") from None
+    # ctypes keeps the low 64 bits of what does not fit
+    if n and (min(params) < -_LIM64 or max(params) >= _LIM64):
+        raise ZrError(ZR_ERR_INVALID, "params must fit in int64_t")
+    if n and (min(counts) < -_LIM64 or max(counts) >= _LIM64):
+        raise ZrError(ZR_ERR_INVALID, "counts must fit in int64_t")
+    return lists
 
 
 def zr_linear_forward_workspace(plan, params, counts, n_out, n_in, in_major=False):
