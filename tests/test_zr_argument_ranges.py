@@ -31,3 +31,15 @@ def test_lists_that_fit():
         # the C call's own check
         with pytest.raises(zr.ZrError, match="param id"):
             query(_plan(), [2 ** 63 - 1], [3], 8, 6)
+
+
+def test_empty_rows_with_strided_columns():
+    """Refused by the older layer calls; the products and losses take them, as
+    there is nothing to read."""
+    t = torch.empty(0, 6)[:, ::2]
+    assert t.stride(1) == 2
+    with pytest.raises(zr.ZrError, match="contiguous rows"):
+        zr._rows(t, "x", t.get_device())
+    assert zr._rows(t, "x", t.get_device(), empty=True) == (t.data_ptr(), 6)
+    with pytest.raises(zr.ZrError, match="contiguous rows"):
+        zr._rows(torch.empty(2, 6)[:, ::2], "x", -1, empty=True)

@@ -755,11 +755,11 @@ def _refuse_device(t, name, dev):
                                   f"({dev})")
 
 
-def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS):
+def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS, empty=False):
     """Checks one matrix of contiguous rows (``rows`` x ``cols``, None: any) of
     one of the torch dtypes on the device ``dev`` and returns (address,
     stride).  Rows may lie apart (a slice of wider rows); a strided or
-    broadcast column axis is refused."""
+    broadcast column axis is refused (``empty``: unless there are no rows)."""
     shape = t.shape
     if len(shape) == 2 and t.dtype in dtypes and t.get_device() == dev:
         n, c = shape
@@ -767,7 +767,7 @@ def _rows(t, name, dev, rows=None, cols=None, dtypes=_FLOATS):
         if n < 2 and stride < c:
             stride = c
         if ((rows is None or n == rows) and (cols is None or c == cols) and stride >= c and
-                (step == 1 or c < 2 or n == 0)):
+                (step == 1 or c < 2 or (empty and n == 0))):
             return t.data_ptr(), stride
     if t.dtype not in dtypes:
         raise ZrError(ZR_ERR_INVALID, f"{name} must be one of {dtypes}, not {t.dtype}")
@@ -1062,9 +1062,9 @@ def zr_linear_input_grad(plan, params, counts, parts, dy, dx, in_major=False, wo
 def _product(fn, plan, params, counts, parts, x, x_name, y, y_name, swap, in_major, workspace,
              stream):
     dev = _device_of(x, x_name)
-    xp, xs = _rows(x, x_name, dev, dtypes=(torch.bfloat16,))
+    xp, xs = _rows(x, x_name, dev, dtypes=(torch.bfloat16,), empty=True)
     rows, depth = x.shape
-    yp, ys = _rows(y, y_name, dev, rows)
+    yp, ys = _rows(y, y_name, dev, rows, empty=True)
     cols = y.shape[1]
     p, c, n = _group_list(plan, params, counts)
     first = params[0] if n else 0
@@ -1099,11 +1099,11 @@ def zr_loss_workspace(rows, vocab, top, dtype):
 
 def _loss_rows(logits, dlogits, dev):
     """(address, stride) of the logits and of the gradient (null, vocab)."""
-    z = _rows(logits, "logits", dev)
+    z = _rows(logits, "logits", dev, empty=True)
     rows, vocab = logits.shape
     if dlogits is None:
         return z, (None, vocab)
-    return z, _rows(dlogits, "dlogits", dev, rows, vocab, (logits.dtype,))
+    return z, _rows(dlogits, "dlogits", dev, rows, vocab, (logits.dtype,), empty=True)
 
 
 def _per_row(t, name, dev, rows):
@@ -1130,9 +1130,9 @@ def zr_distill_loss(logits, ids, teacher, weight, loss, dlogits=None, temperatur
     dev = _device_of(logits, "logits")
     (z, zs), (g, gs) = _loss_rows(logits, dlogits, dev)
     rows, vocab = logits.shape
-    i, istride = _rows(ids, "ids", dev, rows, None, _IDS)
+    i, istride = _rows(ids, "ids", dev, rows, None, _IDS, empty=True)
     top = ids.shape[1]
-    t, tstride = _rows(teacher, "teacher", dev, rows, top)
+    t, tstride = _rows(teacher, "teacher", dev, rows, top, empty=True)
     ws, nbytes = _scratch(workspace, dev)
     _check(_lib.zr_distill_loss(
         z, logits.dtype is torch.bfloat16, rows, vocab, zs, i, ids.dtype is torch.int64, istride,
