@@ -694,7 +694,7 @@ zr_status zr_distill_loss(const void* logits, zr_dtype dtype, int64_t rows, int6
  *   tokens[rows]   a token outside [0, vocab) -- padding -- gives zeros.
  *   ref_logp       read where kl is not 0; may be null otherwise.
  *   logp[rows]     receives lp.
- * 0 <= clip_low <= 1. */
+ * 0 <= clip_low <= 1, clip_high >= 0 and finite, kl finite in fp32. */
 zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t rows, int64_t vocab,
                          int64_t logits_stride, const void* tokens, zr_index token_type,
                          const float* old_logp, const float* ref_logp, const float* advantage,

@@ -43,3 +43,12 @@ def test_empty_rows_with_strided_columns():
     assert zr._rows(t, "x", t.get_device(), empty=True) == (t.data_ptr(), 6)
     with pytest.raises(zr.ZrError, match="contiguous rows"):
         zr._rows(torch.empty(2, 6)[:, ::2], "x", -1, empty=True)
+
+
+@pytest.mark.parametrize("kl", [3.5e38, -1e300])
+def test_kl_that_fp32_does_not_hold(kl):
+    """The kernels take it in fp32: infinite there, times a term of 0."""
+    one, A = (3, 10, 10), 0x10000
+    status = zr._lib.zr_policy_loss(A, zr.ZR_BF16, *one, A, zr.ZR_I64, A, A, A, A, 0.2, 0.2, kl, 1.0, A, A, A, 10,
+                                    None, 0, None)
+    assert status == zr.ZR_ERR_INVALID and "kl must" in zr.zr_last_error()

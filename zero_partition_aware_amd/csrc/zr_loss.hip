@@ -935,7 +935,7 @@ extern "C" zr_status zr_policy_loss(const void* logits, zr_dtype dtype, int64_t 
     if (st != ZR_OK) return st;
     if (!(clip_low >= 0.0 && clip_low <= 1.0 && clip_high >= 0.0) || !std::isfinite(clip_high))
       return fail(ZR_ERR_INVALID, "clip_low must lie in [0, 1] and clip_high be finite and >= 0");
-    if (!std::isfinite(kl)) return fail(ZR_ERR_INVALID, "kl must be finite");
+    if (!(std::fabs(kl) <= 0x1.fffffep127)) return fail(ZR_ERR_INVALID, "kl must be finite in fp32");
     if (rows > 0) {
       if (!old_logp || !advantage || !logp) return fail(ZR_ERR_INVALID, "old_logp, advantage or logp is null");
       if (kl != 0.0 && !ref_logp) return fail(ZR_ERR_INVALID, "kl needs ref_logp, which is null");
