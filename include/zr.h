@@ -649,15 +649,19 @@ zr_status zr_linear_input_grad(const zr_plan* plan, const int64_t* params, const
 /* Losses over a vocabulary's logits, with their gradients.  A row z of `vocab`
  * logits (dtype), q = softmax(z / temperature) over it.  Each row has its own
  * loss; their sum's gradient dL/dz goes to dlogits, rows of the same dtype,
- * rounded once: the dy of the layer that made the logits (zr_linear_input_grad,
- * zr_linear_grad).  dlogits may be null (losses only), or be logits itself,
- * pointer and stride, which it then replaces; otherwise outputs must not
- * overlap inputs.  Sums, exponentials and logarithms are fp32; log q and its
- * distances from old_logp and ref_logp are 64-bit differences, so that a ratio
- * next to the clip's border falls on the right side of it; losses are stored in
- * fp32.
+ * rounded once: where that is bf16, the dy of the layer that made the logits
+ * (zr_linear_input_grad, zr_linear_grad, which take no fp32 rows).  dlogits may be
+ * null (losses only), or be logits itself, pointer and stride, which it then
+ * replaces; otherwise outputs must not overlap inputs.
+ *   Sums, exponentials and logarithms are fp32, what is taken from them 64-bit,
+ * and losses and the multiple of q in a gradient are rounded to fp32.  So log q is
+ * off by up to 2^-24 (3 ln vocab + vocab / 256 + 210) and some 3e-8 of it as a
+ * rule: a ratio that lies nearer to the clip's border than that may fall on either
+ * side of it.  A teacher's probability below fp32's least is 0.
+ *   temperature    1e-30 to 1e30
  *   weight[rows]   each row's factor (a mask, one over the tokens of the step);
- *                  null: 1.  Weight 0 gives a loss and a gradient of 0.
+ *                  null: 1.  Weight 0 gives a loss and a gradient of 0,
+ *                  whatever else the row holds.
  * A row that nothing is asked of (no entry in the vocabulary; logits that are
  * all -inf) gives a loss, a log-probability and a gradient of 0.  Elsewhere NaN
  * and +inf spread as in the formulas; logits of -inf have q = 0, and logits of

@@ -9,11 +9,13 @@
 //                 dL/dz = dL/dlp / tau ([v = a] - q).
 // Both gradients are one multiple of q with corrections at few columns, so one
 // kernel serves both: statistics of the row, a handful of numbers, the row
-// written.  Maxima are exact, exponentials and a lane's sums fp32.  log q, and how
-// far it is from old and ref, are 64-bit differences: a ratio next to the clip's
-// border decides between a gradient and none.  (The exponentials and logarithms
-// themselves are fp32: those of 64 bits held wave 0, and all waves behind it, for
-// 6,000 cycles a row.)
+// written.  Maxima are exact, exponentials and sums over a row fp32.  log q, how
+// far it is from old and ref, and what the loss is put together from are 64-bit: a
+// ratio may be past fp32, and next to the clip's border it decides between a
+// gradient and none (by log q, which is as good as the row's fp32 sum: the header
+// gives the bound).  The exponentials and logarithms themselves are fp32 with the
+// exponent apart: functions of 64 bits held wave 0, and all waves behind it, for
+// 6,000 cycles a row.
 
 #include <cmath>
 #include <cstddef>

@@ -10,8 +10,8 @@
 // 16: 1,756; both 2,390 on constant values, at a higher clock), so what counts is
 // energy and no less than cycles: operands cross the LDS once a tile and step, in
 // tiles as large as the registers hold, and go there straight from memory.  2048
-// rows of 128256 x 4096: 1,704 us, 1,263 TFLOP/s; 16384 rows to eight 8192 x 2048
-// unevenly: 510 us, 1,078, of which a tenth are tiles that are not full.  With few
+// rows of 128256 x 4096: 1,703 us, 1,264 TFLOP/s; 16384 rows to eight 8192 x 2048
+// unevenly: 506 us, 1,086, of which a tenth are tiles that are not full.  With few
 // rows the weights' bytes do: 32 rows to eight 8192 x 2048, 268 MB, 58 us, 4.6 TB/s;
 // one row of 50257 x 768, 77 MB, 14 us, 5.5.
 
@@ -828,7 +828,8 @@ constexpr int64_t kSlots = kCus * (2 * S::kLds > 160 * 1024 ? 1 : 2);   // workg
 
 // What a step costs where a CU has one workgroup and where it has two, and what a
 // piece costs beside its steps, in us, measured at 4096 x 4096 with 1 to 4096 rows:
-// straight into LDS, and by way of registers.
+// straight into LDS, and by way of registers.  Elsewhere the second is low: 2304 x
+// 768 with 1531 rows 22 for 30, 4097 x 4095 with 2000 rows 146 for 172 to 177.
 struct Cost {
   double one, two, piece;
 };
