@@ -6,8 +6,8 @@
 // on how the weight is stored, k or n is its fast axis; X's is k.
 //
 // With many rows the products bound it, and behind them the chip's power: MFMAs
-// 16 x 16 x 32 on random values reach 2,035 TFLOP/s from registers alone (32 x 32 x
-// 16: 1,756; both 2,390 on constant values, at a higher clock), so what counts is
+// 16 x 16 x 32 on random values reach 2,070 TFLOP/s from registers alone (32 x 32 x
+// 16: 1,800; both 2,380 on constant values, at a higher clock), so what counts is
 // energy and no less than cycles: operands cross the LDS once a tile and step, in
 // tiles as large as the registers hold, and go there straight from memory.  2048
 // rows of 128256 x 4096: 1,703 us, 1,264 TFLOP/s; 16384 rows to eight 8192 x 2048
