@@ -653,8 +653,9 @@ zr_status zr_linear_input_grad(const zr_plan* plan, const int64_t* params, const
  * (zr_linear_input_grad, zr_linear_grad, which take no fp32 rows).  dlogits may be
  * null (losses only), or be logits itself, pointer and stride, which it then
  * replaces; otherwise outputs must not overlap inputs.
- *   Sums, exponentials and logarithms are fp32, what is taken from them 64-bit,
- * and losses and the multiple of q in a gradient are rounded to fp32.  So log q is
+ *   Sums, exponentials and logarithms are fp32, what is taken from them 64-bit;
+ * losses are rounded to fp32, and so is the multiple of q in a gradient unless it
+ * is past 10^30 there (a large ratio), where gradients are 64-bit.  So log q is
  * off by up to 2^-24 (3 ln vocab + vocab / 256 + 210) and some 3e-8 of it as a
  * rule: a ratio that lies nearer to the clip's border than that may fall on either
  * side of it.  A teacher's probability below fp32's least is 0.

@@ -116,3 +116,39 @@ def test_rows_far_from_0(vocab, top, tau):
         _put(c, old=np.float32([0.1 + softmax_oracle(z, tau)[1].max() for z in c.z]))
     c.call()
     c.check(range(rows))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("rows,vocab", FORMS)
+def test_multiples_that_fp32_does_not_hold(rows, vocab, bf16, in_place):
+    """Each column's gradient is its own: masked ones 0, others finite while fp32
+    holds them."""
+    def values(z):
+        z[:9, 3::11] = -np.inf
+        z[:9, 4::11] = -150.0
+    c = Case(np.random.default_rng(7), rows, vocab, bf16, weighted=False, values=values, in_place=in_place)
+    c.ids[:9] = 9
+    c.ids_dev.copy_(torch.from_numpy(c.ids))
+    lp = np.array([softmax_oracle(c.z[i], 1.0)[1][9] for i in range(9)])
+    old = (lp - [60, 70, 80, 86, 89, 91, 95, 150, 400]).astype(np.float32)
+    _put(c, old=old, advantage=np.float32([-0.5] * 9))
+    c.call()
+    c.check([rows - 1] if rows > 9 else [])
+    got = c.dlogits[:9].double().cpu().numpy()
+    part = U * (3 * np.log(vocab) + vocab / 256 + 210)
+    for i in range(9):
+        q = softmax_oracle(c.z[i], 1.0)[0]
+        q[9] -= 1
+        # the ratio is off by what log q is and 8 U, q by its part and 3 U an order
+        want = -0.5 * np.exp(lp[i] - float(old[i])) * q
+        rel = 2 * part + 3 * U * abs(lp[i]) + 3 * U * 160 + 16 * U + (2.0 ** -8 if bf16 else U)
+        most = float(torch.finfo(c.dlogits.dtype).max)
+        sure = np.abs(np.abs(want) / most - 1) > 2 * rel
+        assert (got[i, 3::11] == 0).all()
+        held = sure & (np.abs(want) < most)
+        tol = 1.01 * rel * np.abs(want[held]) + 2.0 ** -126 * (1 + min(np.exp(lp[i] - float(old[i])), 1e30))
+        assert (np.abs(got[i][held] - want[held]) <= tol).all(), i
+        past = sure & ~held
+        assert (got[i][past] == np.sign(want[past]) * np.inf).all(), i
+    assert held.any() and past.any()

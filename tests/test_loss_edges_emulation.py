@@ -37,3 +37,7 @@ def test_ratios_that_fp32_does_not_hold(edges):
 
 def test_rows_far_from_0(edges):
     edges("far")
+
+
+def test_multiples_that_fp32_does_not_hold(edges):
+    edges("multiples")

@@ -266,7 +266,7 @@ template <bool kTeacher, int kWaves>
 struct Shared {
   Entries<kTeacher> row[2];
   Stats wave[kWaves];
-  float coef;
+  double coef;
   int32_t next;
 };
 
@@ -378,9 +378,9 @@ __device__ __forceinline__ Teacher finish_entries(const LossArgs& a, int64_t row
 // Wave 0, with the row's statistics and the entries' logits: the loss, and the
 // multiple of q in the gradient.
 template <bool kTeacher>
-__device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, const Entries<kTeacher>& sh,
-                                            const Asked& of_row, const Teacher& t, const Stats& st, int lane,
-                                            bool store) {
+__device__ __forceinline__ double finish_row(const LossArgs& a, int64_t row, const Entries<kTeacher>& sh,
+                                             const Asked& of_row, const Teacher& t, const Stats& st, int lane,
+                                             bool store) {
   const double log_s = log_of(st.s);
   if constexpr (kTeacher) {
     // log q[id] = (z - m) / tau - log s
@@ -391,7 +391,7 @@ __device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, cons
     cross = sum_of_wave(cross);
     if (lane == 0 && store)
       a.loss[row] = static_cast<float>(of_row.weight * a.tau * a.tau * ((t.mean - t.lse) - cross));
-    return static_cast<float>(of_row.weight * a.tau);
+    return of_row.weight * a.tau;
   } else {
     const double lp = (static_cast<double>(sh.z[0]) - st.m) * a.inverse_tau - log_s;
     // (The KL term first, and 64 bits only where a value is used: with all of them
@@ -417,7 +417,7 @@ __device__ __forceinline__ float finish_row(const LossArgs& a, int64_t row, cons
       a.loss[row] = w == 0.0f ? 0.0f : static_cast<float>(w * loss);
       a.logp[row] = static_cast<float>(lp);
     }
-    return static_cast<float>(w * slope * a.inverse_tau);
+    return w * slope * a.inverse_tau;
   }
 }
 // A row that does not count.
@@ -448,6 +448,20 @@ __device__ __forceinline__ void put_entries(const LossArgs& a, T* out, const Ent
       }
     }
     put_one(out + id, coef * (exp2_fast((e.z[j] - st.m) * a.c) * part - p));
+  }
+}
+
+// A policy row whose multiple of q may not be an fp32 number, though its columns'
+// gradients are: in 64 bits, element by element.
+__device__ __forceinline__ bool is_wide(float coef) { return __builtin_fabsf(coef) > 1e30f; }
+template <typename T, int kThreads>
+__device__ __forceinline__ void put_wide(const LossArgs& a, const T* z, T* out, int32_t token, double coef,
+                                         const Stats& st, int v0, int v1) {
+  const double part = 1.0 / st.s;
+#pragma unroll 1
+  for (int v = v0 + threadIdx.x; v < v1; v += kThreads) {
+    const double q = exp_of((static_cast<double>(one(z + v)) - st.m) * a.inverse_tau) * part;
+    put_one(out + v, static_cast<float>(coef * (q - (v == token ? 1.0 : 0.0))));
   }
 }
 
@@ -554,7 +568,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     const bool sloped = some && (kTeacher || asks == kAll);
     if (w == 0) {
       // only the policy's gradient waits for the loss
-      float coef = kTeacher ? static_cast<float>(of_row.weight * a.tau) : 0.0f;
+      double coef = kTeacher ? of_row.weight * a.tau : 0.0;
       if (!kTeacher && some) coef = finish_row(a, row, sh.row[now], of_row, t, st, lane, true);
       if (lane == 0) {
         if (!some) put_nothing<kTeacher>(a, row);
@@ -572,10 +586,11 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     }
     T* out = a.grad ? static_cast<T*>(a.grad) + row * a.grad_stride : nullptr;
     const T* ahead = static_cast<const T*>(a.logits) + next * a.stride;
-    const float coef = sloped ? sh.coef : 0.0f;
+    const float coef = sloped ? static_cast<float>(sh.coef) : 0.0f;
+    const bool wide = !kTeacher && is_wide(coef);
     const Powers p = Powers::fast(sloped ? uniform(base(st.m)) : 0.0f, a.c);
     const float scale = sloped ? coef / st.s * p.fix : 0.0f;
-    const bool plain = sloped && !far && out;
+    const bool plain = sloped && !far && !wide && out;
     keep_packed(x);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
@@ -590,6 +605,8 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
             out + static_cast<int64_t>(v) * kPer<T>,
             gradient<true, T>(load_at<u32x4, sizeof(T)>(z + static_cast<int64_t>(v) * kPer<T>), p, scale));
       if (tid < left) put_one(out + end, p.of<true>(last) * scale);
+    } else if (wide && out) {
+      put_wide<T, kThreads>(a, z, out, sh.row[now].id[0], sh.coef, st, 0, a.vocab);
     } else if (out) {
       const Powers q(base(st.m), a.c);
 #pragma unroll 1
@@ -603,7 +620,7 @@ __global__ __launch_bounds__(kThreads, 4) void loss_row_kernel(const LossArgs a)
     }
     if (then && tid < left) last = one(ahead + end);
     stores_done();
-    if (out && sloped) put_entries<T, kThreads>(a, out, sh.row[now], coef, st, 0, a.vocab);
+    if (out && sloped && !wide) put_entries<T, kThreads>(a, out, sh.row[now], coef, st, 0, a.vocab);
     if (next >= rows) break;
     row = next;
     z = ahead;
@@ -701,7 +718,7 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
     const bool first = blockIdx.x == 0;
     if (e.used != kNothing && !empty) {
       const Teacher t = finish_entries<T, kTeacher, false>(a, row, e, lane);
-      const float coef = finish_row(a, row, e, of_row, t, st, lane, first);
+      const double coef = finish_row(a, row, e, of_row, t, st, lane, first);
       if (lane == 0) sh.coef = coef;
     } else if (lane == 0) {
       e.used = kNothing;
@@ -712,7 +729,12 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
   __syncthreads();
   const bool used = kTeacher ? sh.row[0].used != kNothing : sh.row[0].used == kAll;
   const Powers p(base(st.m), a.c);
-  const float scale = used ? sh.coef / st.s : 0.0f;
+  const float coef = used ? static_cast<float>(sh.coef) : 0.0f;
+  if (!kTeacher && is_wide(coef)) {
+    put_wide<T, kPieceThreads>(a, z, out, sh.row[0].id[0], sh.coef, st, v0 * kPer<T>, end ? a.vocab : v1 * kPer<T>);
+    return;
+  }
+  const float scale = used ? coef / st.s : 0.0f;
   for (int v = v0 + tid; v < v1; v += kPieceThreads * kPieceVecs) {
     u32x4 x[kPieceVecs];
 #pragma unroll
@@ -731,7 +753,7 @@ __global__ __launch_bounds__(kPieceThreads) void loss_piece_kernel(const LossArg
   }
   if (!used) return;
   stores_done();
-  put_entries<T, kPieceThreads>(a, out, sh.row[0], sh.coef, st, v0 * kPer<T>, end ? a.vocab : v1 * kPer<T>);
+  put_entries<T, kPieceThreads>(a, out, sh.row[0], coef, st, v0 * kPer<T>, end ? a.vocab : v1 * kPer<T>);
 }
 
 // ---------------------------------------------------------------------- host
